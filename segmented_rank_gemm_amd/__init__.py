@@ -453,3 +453,9 @@ def _flat_dev_bytes(t: torch.Tensor, name: str):
         raise ValueError(f"{name} must be contiguous")
     return int(t.data_ptr()), t.numel() * t.element_size()
 
+
+
+from . import attention as _attention  # noqa: E402  (needs the helpers above)
+from .attention import *  # noqa: E402,F401,F403
+
+__all__ += _attention.__all__

@@ -21,7 +21,8 @@ MEASURE_LIB = os.path.join(HERE, "liblora_measure.so")
 ARCH = "gfx950"
 
 SOURCES = ["lora_abi.hip", "metadata.hip", "metadata_grouped.hip", "shrink.hip", "expand.hip",
-           "token_step.hip"]
+           "token_step.hip", "attention_abi.hip", "rms_norm.hip", "kv_cache.hip",
+           "kv_attention.hip"]
 MEASURE_SOURCES = ["stream_copy.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

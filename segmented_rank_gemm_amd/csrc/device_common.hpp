@@ -97,6 +97,11 @@ __device__ __forceinline__ void store16_stream_coherent(__amdgpu_buffer_rsrc_t r
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// Element i of eight packed bf16.
+__device__ __forceinline__ float bf16_at(u32x4 v, int i) {
+  return (i & 1) ? bf16_hi(v[i >> 1]) : bf16_lo(v[i >> 1]);
+}
+
 // Two fp32 values rounded to bf16 (nearest, ties to even) and packed, `lo` in
 // the low half; one hardware conversion on gfx950.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
