@@ -237,7 +237,7 @@ def test_kv_append_far_positions():
     positions = (131071 - np.arange(T)).astype(np.int32)
     cache = cache_of(pages, kv, d, page)
     whole = torch.full((T, hq * d + 64), 3.0, dtype=torch.bfloat16, device="cuda")
-    q_out = whole[:, :hq * d].view(T, hq, d) if False else whole.as_strided((T, hq, d), (hq * d + 64, d, 1))
+    q_out = whole.as_strided((T, hq, d), (hq * d + 64, d, 1))
     srg.lora_kv_append(qkv, dev(positions), dev(slots), rope, cache, q_out)
     check_append(x, slots, positions, rope, hq, kv, d, pages, page, False, q_out, cache, 0xA5)
     assert (whole[:, hq * d:] == 3).all()
@@ -454,6 +454,41 @@ def test_kv_attention_far_scores():
         c.scale = sign * 3.0
         c.run()
         c.check()
+
+
+def test_kv_attention_scale_of_zero_takes_the_mean():
+    c = Call(19, [90, 200], [3, 40], 4, 2, 64, 16, 50)
+    c.scale = 0.0
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("queries,window", [(5, 0), (5, 3), (40, 0), (150, 0), (150, 20)])
+def test_kv_attention_nan_value_that_some_queries_see(queries, window):
+    """A NaN value block among the last tokens reaches the queries that see its
+    token, and its own elements only."""
+    c = Call(20, [170], [queries], 2, 1, 128, 32, window)
+    t = 170 - queries + queries // 2               # seen from query queries // 2 on
+    data, values = c.data.copy(), c.values.copy()
+    page, at = c.table[0, t // 32], t % 32
+    data[page, 1, 0, 32 * 64 + 2 * 32 + at] = 255   # elements 64..95
+    c.cache = dev(data)
+    c.run()
+    got = R.f64(c.out)
+    out, slack = c.want()
+    hit = np.zeros(got.shape, dtype=bool)
+    last = queries if not window else queries // 2 + window
+    hit[queries // 2:last, :, 64:96] = True
+    assert np.isnan(got[hit]).all() and np.isfinite(got[~hit]).all()
+    assert (np.abs(got - out) <= slack)[~hit].all()
+
+
+@pytest.mark.parametrize("window", [1, 64, 65, 500, 4999, 5000, 2 ** 31 - 1])
+def test_kv_attention_windows_on_the_long_workspace(window):
+    """The workspace is sized without the window; with one the parts are others."""
+    c = Call(21, [5000, 300], [1, 1], 2, 1, 64, 16, window)
+    c.run()
+    c.check()
 
 
 def test_kv_attention_past_four_gigabytes():
