@@ -144,7 +144,7 @@ lora_status_t lora_kv_read(const int64_t *slots, int32_t num_tokens, int32_t kv_
  *   seq_lens     int32 [num_seqs]: cached tokens; taken as at most max_seq_len.
  *   page_table   int32 [num_seqs][ld_table]: entry i of a sequence is the page of
  *                its tokens [i * page_size, (i + 1) * page_size); entries past
- *                its length are not read.  The tokens of a page outside
+ *                its length may be anything.  The tokens of a page outside
  *                [0, num_pages) are skipped.
  *   max_seq_len  1 <= max_seq_len <= ld_table * page_size.
  *   q_heads      multiple of kv_heads, at most 1024.
@@ -153,10 +153,11 @@ lora_status_t lora_kv_read(const int64_t *slots, int32_t num_tokens, int32_t kv_
  *                that a query may see.
  *   out          bf16 [num_tokens][ldo].
  *   workspace    device memory of at least lora_kv_attention_workspace_bytes(...)
- *                bytes, 256-byte aligned, ZERO-FILLED before its first use; its
- *                counters are left zero-filled by every completed call.  Calls
- *                that overlap in time must not share it.  May be NULL if the
- *                size is 0.
+ *                bytes, 256-byte aligned; every call writes what it reads of it.
+ *                Calls that overlap in time must not share it.  May be NULL if
+ *                the size is 0.
+ * Enqueues one kernel, or two where a workspace is needed (the second joins the
+ * parts that long sequences are cut into).
  * q and out are 16-byte aligned, ldq and ldo multiples of 8 and at least
  * q_heads * head_dim.  The same call on the same data gives the same bits.
  */

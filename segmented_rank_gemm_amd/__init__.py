@@ -201,8 +201,10 @@ def _check(fn: str, status: int) -> None:
 
 
 def _stream_handle(stream: Optional[torch.cuda.Stream]) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return int(s.cuda_stream)
+    if stream is None:
+        # the current stream's handle without a Stream object around it (2.8 us)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return int(stream.cuda_stream)
 
 
 def _dev_ptr(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:

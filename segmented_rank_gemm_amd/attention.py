@@ -51,49 +51,52 @@ from . import (_check, _dev_ptr, _flat_dev_bytes, _stream_handle, lib)  # noqa: 
 _declare(lib())
 
 
-def _rows(t: torch.Tensor, name: str, dtype=torch.bfloat16, width: Optional[int] = None,
-          tokens: Optional[int] = None) -> Tuple[int, int]:
-    """Address and row stride of a [tokens, width] matrix with unit column stride."""
-    ptr = _dev_ptr(t, dtype, name)
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be 2-D with unit column stride")
-    if width is not None and t.shape[1] != width:
-        raise ValueError(f"{name} must be {width} wide, is {t.shape[1]}")
-    if tokens is not None and t.shape[0] != tokens:
-        raise ValueError(f"{name} must have {tokens} rows, has {t.shape[0]}")
-    return ptr, _stride(t)
+# The checks below run on every call, and a decode step's calls are as short as
+# they are: each looks at a tensor's type, shape and strides once.
+_BF16, _F32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+_I32T, _I64T, _U8 = torch.int32, torch.int64, torch.uint8
 
 
-def _stride(t: torch.Tensor) -> int:
+def _refuse(t, dtype: torch.dtype, shape, name: str) -> None:
+    _dev_ptr(t, dtype, name)  # raises what the rest of the binding raises
+    raise ValueError(f"{name} must be {list(shape)}, is {list(t.shape)}")
+
+
+def _matrix(t: torch.Tensor, dtype: torch.dtype, rows: int, width: int, name: str):
+    """Address and row stride of a [rows, width] matrix with unit column stride."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or t.shape != (rows, width):
+        _refuse(t, dtype, (rows, width), name)
+    stride, unit = t.stride()
+    if unit != 1 and width > 1:
+        raise ValueError(f"{name} must have unit column stride")
     # a single row's stride is never used for an address: any value that passes will do
-    return int(t.stride(0)) if t.shape[0] > 1 else _width(t)
+    return t.data_ptr(), stride if rows > 1 else width
 
 
-def _width(t: torch.Tensor) -> int:
-    n = 1
-    for s in t.shape[1:]:
-        n *= int(s)
-    return n
+def _heads(t: torch.Tensor, rows: int, heads: int, head_dim: int, name: str):
+    """Address and row stride of a bf16 [rows, heads, head_dim] tensor whose heads
+    lie one behind another."""
+    if (not isinstance(t, torch.Tensor) or t.dtype != _BF16 or not t.is_cuda
+            or t.shape != (rows, heads, head_dim)):
+        _refuse(t, _BF16, (rows, heads, head_dim), name)
+    stride, between, unit = t.stride()
+    if (unit != 1 and head_dim > 1) or (between != head_dim and heads > 1):
+        raise ValueError(f"{name} must have each row's heads contiguous")
+    return t.data_ptr(), stride if rows > 1 else heads * head_dim
 
 
-def _heads(t: torch.Tensor, name: str, tokens: Optional[int] = None,
-           heads: Optional[int] = None, head_dim: Optional[int] = None) -> Tuple[int, int]:
-    """Address and row stride of a bf16 [tokens, heads, head_dim] tensor whose
-    heads lie one behind another."""
-    ptr = _dev_ptr(t, torch.bfloat16, name)
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        raise ValueError(f"{name} must be [tokens, heads, head_dim], each token's heads contiguous")
-    if ((tokens is not None and t.shape[0] != tokens) or (heads is not None and t.shape[1] != heads)
-            or (head_dim is not None and t.shape[2] != head_dim)):
-        raise ValueError(f"{name} must be [{tokens}, {heads}, {head_dim}], is {list(t.shape)}")
-    return ptr, _stride(t)
+def _vector(t: torch.Tensor, dtype: torch.dtype, n: int, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or t.shape != (n,):
+        _refuse(t, dtype, (n,), name)
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _vector(t: torch.Tensor, dtype: torch.dtype, name: str, n: int) -> int:
-    ptr = _dev_ptr(t, dtype, name)
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous [{n}]")
-    return ptr
+def _dims(t: torch.Tensor, n: int, name: str):
+    if not isinstance(t, torch.Tensor) or t.dim() != n:
+        raise ValueError(f"{name} must be a {n}-D tensor")
+    return t.shape
 
 
 def kv_cache_shape(num_pages: int, kv_heads: int, head_dim: int, page_size: int):
@@ -106,13 +109,14 @@ def kv_cache_shape(num_pages: int, kv_heads: int, head_dim: int, page_size: int)
 
 def _cache(cache: torch.Tensor, head_dim: int) -> Tuple[int, int, int, int]:
     """Address, pages, kv_heads and page size of a cache for this head_dim."""
-    ptr = _dev_ptr(cache, torch.uint8, "cache")
+    ptr = _dev_ptr(cache, _U8, "cache")
     if cache.dim() != 4 or cache.shape[1] != 2 or not cache.is_contiguous():
         raise ValueError("cache must be contiguous [num_pages, 2, kv_heads, page_bytes]")
+    pages, _, heads, size = cache.shape
     row = head_dim // 2 + head_dim // 32  # bytes of one token's head
-    if row < 1 or cache.shape[3] % row:
-        raise ValueError(f"cache pages of {cache.shape[3]} bytes hold no heads of {head_dim}")
-    return ptr, int(cache.shape[0]), int(cache.shape[2]), int(cache.shape[3]) // row
+    if row < 1 or size % row:
+        raise ValueError(f"cache pages of {size} bytes hold no heads of {head_dim}")
+    return ptr, pages, heads, size // row
 
 
 def rope_table(rows: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -133,25 +137,27 @@ def lora_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float,
     hidden]; scales: fp32 [tokens, groups], groups scales a row (1: one a row,
     else hidden / 32, / 64, / 128 or / 256).  residual_out = x + residual, y its
     norm, y8 the norm in 8 bits; any of the three may be left out."""
-    px, ldx = _rows(x, "x")
-    T, hidden = x.shape
-    args = {}
-    for name, t in (("residual", residual), ("residual_out", residual_out), ("y", y)):
-        args[name] = (0, 0) if t is None else _rows(t, name, width=hidden, tokens=T)
-    p8, ld8, ps, group = 0, 0, 0, hidden
+    T, hidden = _dims(x, 2, "x")
+    px, ldx = _matrix(x, _BF16, T, hidden, "x")
+    pr = ldr = po = ldo = py = ldy = p8 = ld8 = ps = 0
+    group = hidden
+    if residual is not None:
+        pr, ldr = _matrix(residual, _BF16, T, hidden, "residual")
+    if residual_out is not None:
+        po, ldo = _matrix(residual_out, _BF16, T, hidden, "residual_out")
+    if y is not None:
+        py, ldy = _matrix(y, _BF16, T, hidden, "y")
     if y8 is not None:
-        p8, ld8 = _rows(y8, "y8", torch.float8_e4m3fn, hidden, T)
+        p8, ld8 = _matrix(y8, _E4M3, T, hidden, "y8")
     if scales is not None:
-        ps = _dev_ptr(scales, torch.float32, "scales")
-        if scales.dim() != 2 or scales.shape[0] != T or not scales.is_contiguous():
-            raise ValueError("scales must be contiguous [tokens, groups]")
-        if scales.shape[1] < 1 or hidden % scales.shape[1]:
-            raise ValueError(f"{scales.shape[1]} scales do not divide a row of {hidden}")
-        group = hidden // scales.shape[1]
+        groups = _dims(scales, 2, "scales")[1]
+        ps, ld = _matrix(scales, _F32, T, groups, "scales")
+        if groups < 1 or hidden % groups or ld != groups:
+            raise ValueError(f"scales must be contiguous, a whole number of them a row of {hidden}")
+        group = hidden // groups
     _check("lora_rms_norm", lib().lora_rms_norm(
-        px, ldx, *args["residual"], _vector(weight, torch.bfloat16, "weight", hidden), float(eps),
-        int(T), int(hidden), *args["residual_out"], *args["y"], p8, ld8, ps, group,
-        _stream_handle(stream)))
+        px, ldx, pr, ldr, _vector(weight, _BF16, hidden, "weight"), eps, T, hidden, po, ldo, py, ldy,
+        p8, ld8, ps, group, _stream_handle(stream)))
 
 
 def lora_kv_append(qkv: torch.Tensor, positions: Optional[torch.Tensor], slots: torch.Tensor,
@@ -161,20 +167,20 @@ def lora_kv_append(qkv: torch.Tensor, positions: Optional[torch.Tensor], slots: 
     [tokens]; slots: int64 [tokens]; rope: fp32 [rows, rot_dim] (rope_table), or
     None for no rotation; cache: uint8 (kv_cache_shape); q_out: bf16 [tokens,
     q_heads, head_dim]."""
-    pq, ldq = _heads(q_out, "q_out")
-    T, q_heads, head_dim = q_out.shape
+    T, q_heads, head_dim = _dims(q_out, 3, "q_out")
+    pq, ldq = _heads(q_out, T, q_heads, head_dim, "q_out")
     pc, pages, kv_heads, page_size = _cache(cache, head_dim)
-    px, ldx = _rows(qkv, "qkv", width=(q_heads + 2 * kv_heads) * head_dim, tokens=T)
+    px, ldx = _matrix(qkv, _BF16, T, (q_heads + 2 * kv_heads) * head_dim, "qkv")
     rows = rot = pr = pp = 0
     if rope is not None:
-        pr = _dev_ptr(rope, torch.float32, "rope")
-        if rope.dim() != 2 or not rope.is_contiguous():
-            raise ValueError("rope must be contiguous [rows, rot_dim]")
-        rows, rot = rope.shape
-        pp = _vector(positions, torch.int32, "positions", T)
+        rows, rot = _dims(rope, 2, "rope")
+        pr, ld = _matrix(rope, _F32, rows, rot, "rope")
+        if ld != rot:
+            raise ValueError("rope must be contiguous")
+        pp = _vector(positions, _I32T, T, "positions")
     _check("lora_kv_append", lib().lora_kv_append(
-        px, ldx, pp, _vector(slots, torch.int64, "slots", T), pr, rows, rot, int(bool(interleaved)),
-        T, q_heads, kv_heads, head_dim, pq, ldq, pc, pages, page_size, _stream_handle(stream)))
+        px, ldx, pp, _vector(slots, _I64T, T, "slots"), pr, rows, rot, 1 if interleaved else 0, T,
+        q_heads, kv_heads, head_dim, pq, ldq, pc, pages, page_size, _stream_handle(stream)))
 
 
 def lora_kv_read(slots: torch.Tensor, cache: torch.Tensor, k_out: Optional[torch.Tensor],
@@ -184,16 +190,16 @@ def lora_kv_read(slots: torch.Tensor, cache: torch.Tensor, k_out: Optional[torch
     like = k_out if k_out is not None else v_out
     if like is None:
         raise ValueError("lora_kv_read needs k_out or v_out")
-    if like.dim() != 3:
-        raise ValueError("k_out and v_out must be [tokens, kv_heads, head_dim]")
-    T, kv_heads, head_dim = like.shape
-    pc, pages, heads, page_size = _cache(cache, head_dim)
-    outs = []
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        outs += (0, 0) if t is None else _heads(t, name, T, heads, head_dim)
+    T, heads, head_dim = _dims(like, 3, "k_out and v_out")
+    pc, pages, kv_heads, page_size = _cache(cache, head_dim)
+    pk = ldk = pv = ldv = 0
+    if k_out is not None:
+        pk, ldk = _heads(k_out, T, kv_heads, head_dim, "k_out")
+    if v_out is not None:
+        pv, ldv = _heads(v_out, T, kv_heads, head_dim, "v_out")
     _check("lora_kv_read", lib().lora_kv_read(
-        _vector(slots, torch.int64, "slots", T), T, heads, head_dim, pc, pages, page_size, *outs,
-        _stream_handle(stream)))
+        _vector(slots, _I64T, T, "slots"), T, kv_heads, head_dim, pc, pages, page_size, pk, ldk, pv,
+        ldv, _stream_handle(stream)))
 
 
 def lora_kv_attention_workspace_bytes(num_seqs: int, max_query_len: int, max_seq_len: int,
@@ -204,11 +210,11 @@ def lora_kv_attention_workspace_bytes(num_seqs: int, max_query_len: int, max_seq
 
 def kv_attention_workspace(num_seqs: int, max_query_len: int, max_seq_len: int, q_heads: int,
                            kv_heads: int, head_dim: int, device="cuda") -> Optional[torch.Tensor]:
-    """A zero-filled workspace for lora_kv_attention, reused call after call (one
-    stream at a time); None where the sizes need none."""
+    """A workspace for lora_kv_attention, reused call after call (one stream at a
+    time); None where the sizes need none."""
     n = lora_kv_attention_workspace_bytes(num_seqs, max_query_len, max_seq_len, q_heads, kv_heads,
                                           head_dim)
-    return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
 def lora_kv_attention(q: torch.Tensor, query_start: torch.Tensor, seq_lens: torch.Tensor,
@@ -220,14 +226,12 @@ def lora_kv_attention(q: torch.Tensor, query_start: torch.Tensor, seq_lens: torc
     seq_lens: int32 [num_seqs]; page_table: int32 [num_seqs, pages a sequence];
     max_seq_len: None: all that the page table can hold; workspace: of
     kv_attention_workspace for these sizes (that max_seq_len among them)."""
-    pq, ldq = _heads(q, "q")
-    T, q_heads, head_dim = q.shape
+    T, q_heads, head_dim = _dims(q, 3, "q")
+    pq, ldq = _heads(q, T, q_heads, head_dim, "q")
+    po, ldo = _heads(out, T, q_heads, head_dim, "out")
     pc, pages, kv_heads, page_size = _cache(cache, head_dim)
-    po, ldo = _heads(out, "out", T, q_heads, head_dim)
-    pt = _dev_ptr(page_table, torch.int32, "page_table")
-    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError("page_table must be [num_seqs, pages] with unit column stride")
-    B, per_seq = page_table.shape
+    B, per_seq = _dims(page_table, 2, "page_table")
+    pt, ldt = _matrix(page_table, _I32T, B, per_seq, "page_table")
     if max_seq_len is None:
         max_seq_len = per_seq * page_size
     elif not 1 <= max_seq_len <= per_seq * page_size:
@@ -235,7 +239,7 @@ def lora_kv_attention(q: torch.Tensor, query_start: torch.Tensor, seq_lens: torc
                          f"{per_seq * page_size} tokens")
     wptr, wbytes = (0, 0) if workspace is None else _flat_dev_bytes(workspace, "workspace")
     _check("lora_kv_attention", lib().lora_kv_attention(
-        pq, ldq, _vector(query_start, torch.int32, "query_start", B + 1),
-        _vector(seq_lens, torch.int32, "seq_lens", B), pt, _stride(page_table), pc, pages, page_size,
-        T, B, int(max_query_len), int(max_seq_len), q_heads, kv_heads, head_dim, float(scale),
-        int(window), po, ldo, wptr, wbytes, _stream_handle(stream)))
+        pq, ldq, _vector(query_start, _I32T, B + 1, "query_start"),
+        _vector(seq_lens, _I32T, B, "seq_lens"), pt, ldt, pc, pages, page_size, T, B, max_query_len,
+        max_seq_len, q_heads, kv_heads, head_dim, scale, window, po, ldo, wptr, wbytes,
+        _stream_handle(stream)))

@@ -22,12 +22,14 @@
 // Bound by: HBM (68 bytes a token and head at D = 128) as long as the rows of a
 // key head fit one tile; by the exponentials and the matrix unit for prompts.
 
+
 #include "kv_format.hpp"
 
 namespace lora {
 
 constexpr int kChunk = 64;       // tokens of a wave's step
 constexpr int kTile = 16;        // rows of one matrix product
+__host__ __device__ constexpr int waves_a_simd(int mt) { return mt == 1 ? 2 : (mt == 2 ? 2 : 1); }
 // Waves of a workgroup: they share out one tile's tokens (split), or have tiles
 // of their own.  More row tiles a wave need the registers of four waves.
 __host__ __device__ constexpr int waves_of(int mt, bool split) { return split && mt == 1 ? 8 : 4; }
@@ -47,28 +49,16 @@ struct AttentionArgs {
   int num_tokens, max_query_len, max_seq_len, q_heads, window;
   float scale_log2;   // |scale| * log2(e): the softmax runs in powers of two
   uint32_t sign;      // scale's sign bits, for q (two bf16)
+  int group;          // query heads a key head
+  int group_inverse;  // ceil(2^21 / group)
   int row_tiles;      // of 16 * MT rows, for one sequence and key head
   int parts;          // of one row tile's tokens
   int part_chunks;
-  int* arrivals;      // one counter a (sequence, key head, row tile)
-  float* partial;     // [unit][part][MT * 16][D], then [..][2]: maximum and sum
-};
-
-// What a wave holds of one chunk: keys of token 4 c + j, block g (D = 128) or
-// half block g (D = 64); values of the tokens 16 g + k, elements from c * D / 16.
-template <int D>
-struct Chunk {
-  static constexpr int kKeyWords = D / 32;  // u32 of codes a key tile and lane
-  uint32_t k[4][kKeyWords];
-  uint32_t v[16];
-  uint32_t ks;     // scales of the four keys
-  u32x4 vs;        // scales of the sixteen values
-  bool ok;         // the page of this lane's values (and of its 16 scores) exists
-  bool all_ok;     // and that of its keys
-};
-
-struct Pages {
-  int k, v;  // -1: no token there, or no such page
+  int tile_rows;      // 16 * MT
+  // Of parts, by (sequence, row tile, key head), part, row of the tile: the
+  // maximum and the sum, and the outputs relative to that maximum.
+  float* stats;       // [..][2]
+  float* partial;     // [..][D]
 };
 
 __device__ __forceinline__ uint32_t byte_scale(uint32_t w, int j) {
@@ -87,15 +77,32 @@ __device__ __forceinline__ bf16x8 as_bf16x8(uint32_t a, uint32_t b, uint32_t c, 
   return __builtin_bit_cast(bf16x8, v);
 }
 
-// Eight codes of one word, as the A operand of one product.
-__device__ __forceinline__ bf16x8 word_to_bf16(uint32_t w, float scale) {
-  return as_bf16x8(codes_to_bf16<0>(w, scale), codes_to_bf16<1>(w, scale), codes_to_bf16<2>(w, scale),
-                   codes_to_bf16<3>(w, scale));
+// Eight codes of one word: elements in pairs, the A operand of a product of keys.
+__device__ __forceinline__ u32x4 word_to_bf16(uint32_t w, float scale) {
+  return u32x4{codes_to_bf16<0>(w, scale), codes_to_bf16<1>(w, scale), codes_to_bf16<2>(w, scale),
+               codes_to_bf16<3>(w, scale)};
 }
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
+
+// A lane's part of a chunk's keys: of tokens 4 c + j, the g-th quarter of the head.
+template <int D>
+struct Keys {
+  uint32_t w[4][D / 32];
+  uint32_t scales;  // of the four tokens
+};
+
+// A lane's part of a chunk's values: of tokens 16 g + k, elements from c * D / 16.
+struct Values {
+  uint32_t w[16];
+  u32x4 scales;  // of the sixteen tokens
+};
+
+struct Pages {
+  int k, v;  // of this lane's keys and values; -1: no such page
+};
 
 // One sequence's cache from one key head's point of view.
 template <int D>
@@ -104,106 +111,116 @@ struct Reader {
   const uint8_t* values;
   const int32_t* table;
   int64_t page_stride;
-  int shift, num_pages, last;
+  int shift, num_pages, max_seq_len;
 
   __device__ __forceinline__ int page_at(int token) const {
-    if (token >= last) return -1;
+    if (token >= max_seq_len) return -1;
     const int p = table[token >> shift];
     return p >= 0 && p < num_pages ? p : -1;
   }
   __device__ __forceinline__ Pages pages(int base) const {
     const int lane = lane_id();
-    Pages p;
-    p.k = page_at(base + 16 * ((lane & 15) >> 2));
-    p.v = page_at(base + 16 * (lane >> 4));
-    return p;
+    return Pages{page_at(base + 16 * ((lane & 15) >> 2)), page_at(base + 16 * (lane >> 4))};
   }
   // A page that does not exist reads as page 0, which does, and is masked.
-  __device__ __forceinline__ void load(Chunk<D>& ch, Pages p, int base) const {
-    const int lane = lane_id(), g = lane >> 4, c = lane & 15;
-    const int in = (1 << shift) - 1;
-    const int64_t scales = static_cast<int64_t>(D / 2) << shift;
-    ch.ok = p.v >= 0;
-    ch.all_ok = p.v >= 0 && p.k >= 0;
-    const uint8_t* kb = keys + (p.k < 0 ? 0 : p.k) * page_stride;
-    const uint8_t* vb = values + (p.v < 0 ? 0 : p.v) * page_stride;
-    const int ka = (base + 4 * c) & in, va = (base + 16 * g) & in;
-    const uint8_t* kr = kb + ka * (D / 2) + g * (D / 8);
-    const uint8_t* vr = vb + va * (D / 2) + c * (D / 32);
+  __device__ __forceinline__ void load(Keys<D>& k, Pages p, int base) const {
+    const int lane = lane_id(), g = lane >> 4;
+    const int at = (base + 4 * (lane & 15)) & ((1 << shift) - 1);
+    const uint8_t* b = keys + (p.k < 0 ? 0 : p.k) * page_stride;
+    const uint8_t* row = b + at * (D / 2) + g * (D / 8);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if constexpr (D == 128) {
-        const u32x4 w = load16(kr + j * (D / 2));
+        const u32x4 w = load16(row + j * (D / 2));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ch.k[j][i] = w[i];
+        for (int i = 0; i < 4; ++i) k.w[j][i] = w[i];
       } else {
-        const u32x2 w = load8(kr + j * (D / 2));
-        ch.k[j][0] = w[0];
-        ch.k[j][1] = w[1];
+        const u32x2 w = load8(row + j * (D / 2));
+        k.w[j][0] = w[0];
+        k.w[j][1] = w[1];
       }
     }
-    ch.ks = *(const LORA_GLOBAL uint32_t*)(kb + scales + ((g * (D / 4) / kBlock) << shift) + ka);
+    k.scales = *(const LORA_GLOBAL uint32_t*)(b + (((D / 2) + g * (D / 4) / kBlock) << shift) + at);
+  }
+  __device__ __forceinline__ void load(Values& v, Pages p, int base) const {
+    const int lane = lane_id(), c = lane & 15;
+    const int at = (base + 16 * (lane >> 4)) & ((1 << shift) - 1);
+    const uint8_t* b = values + (p.v < 0 ? 0 : p.v) * page_stride;
+    const uint8_t* row = b + at * (D / 2) + c * (D / 32);
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      if constexpr (D == 128) ch.v[k] = *(const LORA_GLOBAL uint32_t*)(vr + k * (D / 2));
-      else ch.v[k] = *(const LORA_GLOBAL uint16_t*)(vr + k * (D / 2));
+      if constexpr (D == 128) v.w[k] = *(const LORA_GLOBAL uint32_t*)(row + k * (D / 2));
+      else v.w[k] = *(const LORA_GLOBAL uint16_t*)(row + k * (D / 2));
     }
-    ch.vs = load16(vb + scales + ((c * (D / 16) / kBlock) << shift) + va);
+    v.scales = load16(b + (((D / 2) + c * (D / 16) / kBlock) << shift) + at);
   }
 };
 
 // The rows of one wave: MT tiles of 16.
 template <int D, int MT>
 struct Rows {
-  bf16x8 q[MT][D / 32];
   f32x4 acc[MT][D / 16];
   float top[MT], sum[MT];
   int place[MT];  // of row c of the tile: the last token that it sees
 };
 
-// One chunk: scores, running softmax, weighted values.  `masked`: some row does
-// not see all 64 tokens, or a page is missing.
-template <int D, int MT, bool kMasked>
-__device__ __forceinline__ void attend(Rows<D, MT>& r, const Chunk<D>& ch, int base, int first, int last,
-                                       int window, float scale_log2, bool several) {
-  const int lane = lane_id(), g = lane >> 4;
-  uint32_t weights[MT][8];
-  uint32_t seen[MT];
+// Where a chunk stands: which of its tokens are there at all.
+struct Span {
+  int base;           // the chunk's first token
+  int first, last;    // tokens [first, last) are seen by some row
+  int window;
+  bool masked;        // some row does not see all 64, or a page is missing
+  bool several;       // the rows are more than one query's
+  bool ok;            // the page of this lane's 16 values (and scores) exists
+};
+
+// Which of this lane's 16 tokens (base + 16 g + k, bit k) a row at `place` sees.
+__device__ __forceinline__ uint32_t seen_bits(const Span& at, int place) {
+  const int token = at.base + 16 * (lane_id() >> 4);
+  int hi = place - token, lo = at.window ? hi - at.window + 1 : 0;  // lo..hi of 0..15
+  hi = hi < 15 ? hi : 15;
+  lo = lo > 0 ? lo : 0;
+  return at.ok && hi >= lo ? ((2u << hi) - 1u) & ~((1u << lo) - 1u) : 0u;
+}
+
+// Scores of one chunk, the running softmax, and the weights in bf16 (pairs of
+// tokens 16 g + 2 i, + 1).  q: the operand [mt][D / 32][lane] in shared memory.
+template <int D, int MT>
+__device__ __forceinline__ void weigh(Rows<D, MT>& r, uint32_t (&weights)[MT][8], const Keys<D>& k,
+                                      const u32x4* q, const Span& at, float scale_log2) {
+  f32x4 s[MT][4];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) seen[mt] = 0xFFFFu;
-  if constexpr (kMasked) {
+  for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      // this lane's tokens are base + 16 g + [0, 16)
-      const int at = base + 16 * g;
-      int hi = r.place[mt] - at, lo = window ? hi - window + 1 : 0;  // visible: lo..hi of 0..15
-      hi = hi < 15 ? hi : 15;
-      lo = lo > 0 ? lo : 0;
-      seen[mt] = ch.ok && hi >= lo ? ((2u << hi) - 1u) & ~((1u << lo) - 1u) : 0u;
+    for (int j = 0; j < 4; ++j) s[mt][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    bf16x8 b[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+      b[mt] = __builtin_bit_cast(bf16x8, q[(mt * (D / 32) + i) * kWave + lane_id()]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const u32x4 w = word_to_bf16(k.w[j][i], __uint_as_float(byte_scale(k.scales, j)));
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) s[mt][j] = mfma(__builtin_bit_cast(bf16x8, w), b[mt], s[mt][j]);
     }
   }
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    f32x4 s[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float scale = __uint_as_float(byte_scale(ch.ks, j));
-      s[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) s[j] = mfma(word_to_bf16(ch.k[j][i], scale), r.q[mt][i], s[j]);
-    }
-    if constexpr (kMasked) {
+    if (at.masked) {
+      const uint32_t seen = seen_bits(at, r.place[mt]);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (!(seen[mt] >> (4 * i + j) & 1u)) s[j][i] = -INFINITY;
+          if (!(seen >> (4 * i + j) & 1u)) s[mt][j][i] = -INFINITY;
     }
-    float m = s[0][0];
+    float m = s[mt][0][0];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) m = fmaxf(m, s[j][i]);
+      for (int i = 0; i < 4; ++i) m = fmaxf(m, s[mt][j][i]);
     m *= scale_log2;
     if (__any(m > r.top[mt] + kMaxLag)) {
       m = fmaxf(m, __shfl_xor(m, 16));
@@ -221,74 +238,74 @@ __device__ __forceinline__ void attend(Rows<D, MT>& r, const Chunk<D>& ch, int b
     for (int i = 0; i < 4; ++i) {
       float p[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        p[j] = __builtin_amdgcn_exp2f(fmaf(s[j][i], scale_log2, -r.top[mt]));
-        if constexpr (kMasked)
-          if (!(seen[mt] >> (4 * i + j) & 1u)) p[j] = 0.f;
-        r.sum[mt] += p[j];
-      }
+      for (int j = 0; j < 4; ++j)
+        p[j] = __builtin_amdgcn_exp2f(fmaf(s[mt][j][i], scale_log2, -r.top[mt]));
+      r.sum[mt] += (p[0] + p[1]) + (p[2] + p[3]);
       weights[mt][2 * i] = pack_bf16x2(p[0], p[1]);
       weights[mt][2 * i + 1] = pack_bf16x2(p[2], p[3]);
     }
   }
-  u32x4 vs = ch.vs;
-  if constexpr (kMasked) {
-    // Values that no row sees may be anything; their weights are zero, their
-    // scales must not be NaN.
-    uint32_t nan = 0;
-    const int at = base + 16 * g;
+}
+
+// Values that no row sees may be anything: their weights are zero, and their
+// scales are made so.  A NaN block that some rows see and others do not is
+// taken out too and marks the outputs that it reaches: those for which the sum
+// over its tokens of "seen" is not zero.
+template <int D, int MT>
+__device__ __forceinline__ void mask_values(Rows<D, MT>& r, u32x4& scales, const Span& at) {
+  uint32_t nan = 0;
+  const int token = at.base + 16 * (lane_id() >> 4);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const uint32_t byte = (vs[k >> 2] >> (8 * (k & 3))) & 255u;
-      const bool none = !ch.ok || at + k >= last || at + k < first;
-      if (none) vs[k >> 2] &= ~(255u << (8 * (k & 3)));
-      else if (several && byte == kScaleNan) {
-        nan |= 1u << k;
-        vs[k >> 2] &= ~(255u << (8 * (k & 3)));
+  for (int k = 0; k < 16; ++k) {
+    const uint32_t byte = 255u << (8 * (k & 3));
+    const bool none = !at.ok || token + k >= at.last || token + k < at.first;
+    const bool bad = at.several && (scales[k >> 2] & byte) == byte;
+    if (bad && !none) nan |= 1u << k;
+    if (bad || none) scales[k >> 2] &= ~byte;
+  }
+  if (!__any(nan != 0)) return;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const uint32_t seen = seen_bits(at, r.place[mt]);
+    f32x4 hit = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      u32x4 a, b;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = 8 * h + 2 * i;
+        a[i] = (nan >> k & 1u ? 0x3F80u : 0u) | (nan >> (k + 1) & 1u ? 0x3F800000u : 0u);
+        b[i] = (seen >> k & 1u ? 0x3F80u : 0u) | (seen >> (k + 1) & 1u ? 0x3F800000u : 0u);
       }
+      hit = mfma(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), hit);
     }
-    // A NaN block that some rows see and others do not: the sum over its tokens
-    // of "seen" marks the outputs that it reaches.
-    if (several && __any(nan != 0)) {
+    // the D / 16 elements of lane c's tokens share a block, so `hit` serves them all
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        u32x4 a;
+    for (int i = 0; i < 4; ++i) {
+      const float add = hit[i] > 0.f ? NAN : 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          a[i] = (nan >> (8 * h + 2 * i) & 1u ? 0x3F80u : 0u) |
-                 (nan >> (8 * h + 2 * i + 1) & 1u ? 0x3F800000u : 0u);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          u32x4 b;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            b[i] = (seen[mt] >> (8 * h + 2 * i) & 1u ? 0x3F80u : 0u) |
-                   (seen[mt] >> (8 * h + 2 * i + 1) & 1u ? 0x3F800000u : 0u);
-          const f32x4 hit = mfma(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
-                                 f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-          for (int n = 0; n < D / 16; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (hit[i] > 0.f) r.acc[mt][n][i] = NAN;
-        }
-      }
+      for (int n = 0; n < D / 16; ++n) r.acc[mt][n][i] += add;
     }
   }
+}
+
+// The weighted values of one chunk.
+template <int D, int MT>
+__device__ __forceinline__ void add_values(Rows<D, MT>& r, const uint32_t (&weights)[MT][8],
+                                           const Values& v, const u32x4 scales) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t vt[D / 16][4];  // [element][pair of tokens]
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int k = 8 * h + 2 * i;
-      const float sa = __uint_as_float(byte_scale(vs[k >> 2], k & 3));
-      const float sb = __uint_as_float(byte_scale(vs[k >> 2], (k + 1) & 3));
-      const bf16x8 a = word_to_bf16(ch.v[k], sa), b = word_to_bf16(ch.v[k + 1], sb);
-      const u32x4 wa = __builtin_bit_cast(u32x4, a), wb = __builtin_bit_cast(u32x4, b);
+      const float sa = __uint_as_float(byte_scale(scales[k >> 2], k & 3));
+      const float sb = __uint_as_float(byte_scale(scales[k >> 2], (k + 1) & 3));
+      const u32x4 a = word_to_bf16(v.w[k], sa), b = word_to_bf16(v.w[k + 1], sb);
 #pragma unroll
       for (int n = 0; n < D / 32; ++n) {
-        vt[2 * n][i] = __builtin_amdgcn_perm(wb[n], wa[n], 0x05040100u);
-        vt[2 * n + 1][i] = __builtin_amdgcn_perm(wb[n], wa[n], 0x07060302u);
+        vt[2 * n][i] = __builtin_amdgcn_perm(b[n], a[n], 0x05040100u);
+        vt[2 * n + 1][i] = __builtin_amdgcn_perm(b[n], a[n], 0x07060302u);
       }
     }
 #pragma unroll
@@ -302,14 +319,75 @@ __device__ __forceinline__ void attend(Rows<D, MT>& r, const Chunk<D>& ch, int b
   }
 }
 
+// Row `row` of a tile whose first row is head `head0` of query `query0`.
+struct RowOf {
+  int query, head;
+};
+__device__ __forceinline__ RowOf row_of(const AttentionArgs& a, int query0, int head0, int row) {
+  // row + head0 < group + 64: the product is exact enough for a division
+  const int n = head0 + row;
+  const int q = static_cast<int>(static_cast<uint32_t>(n * a.group_inverse) >> 21);
+  return RowOf{query0 + q, n - q * a.group};
+}
+
+// One row tile of a sequence: its rows and the tokens that they see.
+struct RowTile {
+  int start;            // the sequence's first row of q
+  int before;           // tokens before its first query (negative: queries that see none)
+  int rows;             // of this tile
+  int query0, head0;    // the query and head (of the group) of its first row
+  int query1;           // the query of its last row
+  int first, last;      // tokens [first, last) are seen by some row,
+  int all_first, all_last;  // and these by all
+  int chunk0, chunk1;   // the chunks that hold them
+};
+
+// False if the tile has no rows in this call.
+__device__ __forceinline__ bool tile_of(const AttentionArgs& a, int seq, int tile, RowTile& t) {
+  t.start = a.query_start[seq];
+  const int end = a.query_start[seq + 1];
+  int length = a.seq_lens[seq];
+  if (t.start < 0 || t.start >= a.num_tokens || end <= t.start) return false;
+  const int queries = end - t.start;
+  int mine = queries < a.max_query_len ? queries : a.max_query_len;  // that this call does
+  mine = mine < a.num_tokens - t.start ? mine : a.num_tokens - t.start;
+  const int row0 = tile * a.tile_rows;
+  t.rows = mine * a.group - row0;
+  if (t.rows <= 0) return false;
+  t.rows = t.rows < a.tile_rows ? t.rows : a.tile_rows;
+  length = length < 0 ? 0 : (length > a.max_seq_len ? a.max_seq_len : length);
+  t.before = length - queries;
+  t.query0 = row0 / a.group;
+  t.head0 = row0 - t.query0 * a.group;
+  t.query1 = row_of(a, t.query0, t.head0, t.rows - 1).query;
+  const int place0 = t.before + t.query0, place1 = t.before + t.query1;
+  t.last = place1 + 1 > 0 ? place1 + 1 : 0;
+  t.first = a.window && place0 >= a.window ? place0 - a.window + 1 : 0;
+  t.all_first = a.window && place1 >= a.window ? place1 - a.window + 1 : 0;
+  t.all_last = place0 + 1;
+  t.chunk0 = t.first / kChunk;
+  t.chunk1 = (t.last + kChunk - 1) / kChunk;
+  return true;
+}
+
+// The parts of a tile that hold anything; 1 also where nothing is seen.
+__device__ __forceinline__ int parts_of(const AttentionArgs& a, const RowTile& t) {
+  const int n = (t.chunk1 - t.chunk0 + a.part_chunks - 1) / a.part_chunks;
+  return n > 1 ? n : 1;
+}
+
+__device__ __forceinline__ int unit_of(const AttentionArgs& a, int seq, int tile, int kv_head) {
+  return (seq * a.row_tiles + tile) * a.cache.kv_heads + kv_head;
+}
+
 // Four neighbouring outputs of a row, divided by its sum; a row that saw nothing
 // gets zeros.
-__device__ __forceinline__ void store_out(const AttentionArgs& a, int start, int head0, int row,
-                                          int group, int e, int d, f32x4 o, float total) {
-  const int qi = row / group;
+__device__ __forceinline__ void store_out(const AttentionArgs& a, const RowTile& t, int kv_head, int row,
+                                          int d, int e, f32x4 o, float total) {
+  const RowOf at = row_of(a, t.query0, t.head0, row);
   const float inv = total == 0.f ? 0.f : 1.f / total;
-  *(LORA_GLOBAL u32x2*)(a.out + static_cast<int64_t>(start + qi) * a.ldo +
-                        (head0 + row - qi * group) * d + e) =
+  *(LORA_GLOBAL u32x2*)(a.out + static_cast<int64_t>(t.start + at.query) * a.ldo +
+                        (kv_head * a.group + at.head) * d + e) =
       u32x2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
 }
 
@@ -317,105 +395,105 @@ __device__ __forceinline__ void store_out(const AttentionArgs& a, int start, int
 // workgroups of a unit its parts; otherwise each wave has a row tile of its own
 // and walks all of that tile's tokens.
 template <int D, int MT, bool kSplit>
-__global__ __launch_bounds__(waves_of(MT, kSplit) * kWave) void kv_attention_kernel(
+__global__ __launch_bounds__(waves_of(MT, kSplit) * kWave, waves_a_simd(MT)) void kv_attention_kernel(
     AttentionArgs a) {
   constexpr int kWaves = waves_of(MT, kSplit);
   const int tid = static_cast<int>(threadIdx.x);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int lane = lane_id(), g = lane >> 4, c = lane & 15;
-  const int kv_heads = a.cache.kv_heads;
-  const int group = a.q_heads / kv_heads;
 
-  // blockIdx.x = (row tile, or its workgroup of tiles) and part, slowest first;
-  // then the sequence and key head, so that neighbours read different caches
-  const int heads = static_cast<int>(blockIdx.x);
-  const int kv_head = heads % kv_heads, seq = heads / kv_heads;
+  // blockIdx: key head, then row tile (or workgroup of tiles) and part, then
+  // sequence.  Neighbours go to other XCDs; with a multiple of 8 key heads the
+  // workgroups of one head share an XCD and find its cache in their L2.
+  const int kv_head = static_cast<int>(blockIdx.x), seq = static_cast<int>(blockIdx.z);
   const int part = kSplit ? static_cast<int>(blockIdx.y) % a.parts : 0;
   const int tile = kSplit ? static_cast<int>(blockIdx.y) / a.parts
                           : static_cast<int>(blockIdx.y) * kWaves + wave;
-  const int start = a.query_start[seq], end = a.query_start[seq + 1];
-  if (start < 0 || start >= a.num_tokens || end <= start) return;
-  const int queries = end - start;
-  int mine = queries < a.max_query_len ? queries : a.max_query_len;  // that this call does
-  mine = mine < a.num_tokens - start ? mine : a.num_tokens - start;
-  const int row0 = tile * kTile * MT;
-  const int rows = mine * group;
-  if (row0 >= rows) return;  // the whole workgroup (kSplit), or a wave that shares nothing
-  int length = a.seq_lens[seq];
-  length = length < 0 ? 0 : (length > a.max_seq_len ? a.max_seq_len : length);
-
-  // Tokens that some row of the tile sees, and that all of them see.
-  const int q_first = row0 / group;
-  const int row_last = row0 + kTile * MT < rows ? row0 + kTile * MT - 1 : rows - 1;
-  const int q_last = row_last / group;
-  const int place0 = length - queries + q_first, place1 = length - queries + q_last;
-  const int last = place1 + 1 > 0 ? place1 + 1 : 0;
-  int first = a.window ? place0 - a.window + 1 : 0;
-  first = first > 0 ? first : 0;
-  int all_first = a.window ? place1 - a.window + 1 : 0;
-  all_first = all_first > 0 ? all_first : 0;
-  const int all_last = place0 + 1;
-  const int chunk0 = first / kChunk, chunk1 = (last + kChunk - 1) / kChunk;
-  const int active = kSplit ? (chunk1 - chunk0 + a.part_chunks - 1) / a.part_chunks : 1;
-  if (kSplit && part >= (active > 1 ? active : 1)) return;
-
-  Rows<D, MT> r;
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int row = row0 + mt * kTile + c;
-    const int qi = row / group;
-    r.place[mt] = length - queries + qi;
-    r.top[mt] = kNoScore;
-    r.sum[mt] = 0.f;
-#pragma unroll
-    for (int n = 0; n < D / 16; ++n) r.acc[mt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const uint16_t* src = a.q + static_cast<int64_t>(start + qi) * a.ldq +
-                          (kv_head * group + row - qi * group) * D + g * (D / 4);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      u32x4 w = {0, 0, 0, 0};
-      if (row < rows) w = load16(src + 8 * i);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] ^= a.sign;
-      r.q[mt][i] = __builtin_bit_cast(bf16x8, w);
-    }
-  }
 
   Reader<D> reader;
   const int64_t block = static_cast<int64_t>(D / 2 + D / kBlock) << a.cache.page_shift;
   reader.keys = a.cache.data + kv_head * block;
-  reader.values = reader.keys + kv_heads * block;
-  reader.page_stride = 2 * kv_heads * block;
+  reader.values = reader.keys + a.cache.kv_heads * block;
+  reader.page_stride = 2 * a.cache.kv_heads * block;
   reader.table = a.page_table + seq * a.ld_table;
   reader.shift = a.cache.page_shift;
   reader.num_pages = a.cache.num_pages;
-  reader.last = last;
+  reader.max_seq_len = a.max_seq_len;
+  // Without a window the first chunk does not depend on the lengths: its pages
+  // are looked up beside them.
+  constexpr int step = kSplit ? kWaves : 1;
+  int chunk = kSplit ? part * a.part_chunks + wave : 0;
+  Pages pages = {-1, -1};
+  if (!a.window) pages = reader.pages(chunk * kChunk);
 
-  const int step = kSplit ? kWaves : 1;
-  int chunk = chunk0, stop = chunk1;
+  RowTile t;
+  // the whole workgroup (kSplit), or a wave that shares nothing, is done here
+  if (!tile_of(a, seq, tile, t)) return;
+  const int active = kSplit ? parts_of(a, t) : 1;
+  if (kSplit && part >= active) return;
+  chunk += t.chunk0;
+  int stop = t.chunk1;
   if constexpr (kSplit) {
-    chunk = chunk0 + part * a.part_chunks + wave;
-    stop = chunk0 + (part + 1) * a.part_chunks;
-    stop = stop < chunk1 ? stop : chunk1;
+    stop = t.chunk0 + (part + 1) * a.part_chunks;
+    stop = stop < t.chunk1 ? stop : t.chunk1;
   }
-  // The pages of the chunk after next and the codes of the next are on their way
-  // while a chunk is worked on.
+  if (a.window) pages = reader.pages(chunk * kChunk);
+
+  // The queries as B operands in shared memory: one tile for all waves, or one each.
+  __shared__ u32x4 q_shared[kSplit ? 1 : kWaves][MT * (D / 32)][kWave];
+  u32x4(*q)[kWave] = q_shared[kSplit ? 0 : wave];
+  Keys<D> keys;
+  Values values;
   if (chunk < stop) {
-    Chunk<D> now, next;
-    reader.load(now, reader.pages(chunk * kChunk), chunk * kChunk);
-    Pages ahead = reader.pages((chunk + step) * kChunk);
-    for (; chunk < stop; chunk += step) {
-      const int base = chunk * kChunk;
-      if (chunk + step < stop) {
-        reader.load(next, ahead, base + step * kChunk);
-        ahead = reader.pages(base + 2 * step * kChunk);
-      }
-      const bool whole = base >= all_first && base + kChunk <= all_last;
-      if (whole && __all(now.all_ok))
-        attend<D, MT, false>(r, now, base, first, last, a.window, a.scale_log2, q_last != q_first);
-      else
-        attend<D, MT, true>(r, now, base, first, last, a.window, a.scale_log2, q_last != q_first);
-      now = next;
+    reader.load(keys, pages, chunk * kChunk);
+    reader.load(values, pages, chunk * kChunk);
+  }
+  Pages ahead = reader.pages((chunk + step) * kChunk);
+  for (int f = kSplit ? wave : 0; f < MT * (D / 32); f += kSplit ? kWaves : 1) {
+    const int mt = f / (D / 32), i = f % (D / 32);
+    const RowOf at = row_of(a, t.query0, t.head0, mt * kTile + c);
+    u32x4 w = {0, 0, 0, 0};
+    if (mt * kTile + c < t.rows)
+      w = load16(a.q + static_cast<int64_t>(t.start + at.query) * a.ldq +
+                 (kv_head * a.group + at.head) * D + g * (D / 4) + 8 * i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] ^= a.sign;
+    q[f][lane] = w;
+  }
+  Rows<D, MT> r;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    r.place[mt] = t.before + row_of(a, t.query0, t.head0, mt * kTile + c).query;
+    r.top[mt] = kNoScore;
+    r.sum[mt] = 0.f;
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n) r.acc[mt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  if constexpr (kSplit) __syncthreads();
+
+  // The next chunk's keys are on their way from the scores on, its values from
+  // the products on, and the pages of the one after it are looked up.
+  for (; chunk < stop; chunk += step) {
+    Span at;
+    at.base = chunk * kChunk;
+    at.first = t.first;
+    at.last = t.last;
+    at.window = a.window;
+    at.several = t.query1 != t.query0;
+    at.ok = pages.v >= 0;
+    at.masked = at.base < t.all_first || at.base + kChunk > t.all_last ||
+                !__all(pages.v >= 0 && pages.k >= 0);
+    uint32_t weights[MT][8];
+    weigh<D, MT>(r, weights, keys, &q[0][0], at, a.scale_log2);
+    const bool more = chunk + step < stop;
+    if (more) reader.load(keys, ahead, at.base + step * kChunk);
+    u32x4 scales = values.scales;
+    if (at.masked) mask_values<D, MT>(r, scales, at);
+    add_values<D, MT>(r, weights, values, scales);
+    if (more) {
+      reader.load(values, ahead, at.base + step * kChunk);
+      pages = ahead;
+      ahead = reader.pages(at.base + 2 * step * kChunk);
     }
   }
 #pragma unroll
@@ -427,12 +505,11 @@ __global__ __launch_bounds__(waves_of(MT, kSplit) * kWave) void kv_attention_ker
   if constexpr (!kSplit) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const int row = row0 + mt * kTile + c;
-      if (row >= rows) continue;
-      const int qi = row / group;
+      if (mt * kTile + c >= t.rows) continue;
+      const RowOf at = row_of(a, t.query0, t.head0, mt * kTile + c);
       const float inv = r.sum[mt] == 0.f ? 0.f : 1.f / r.sum[mt];
-      uint16_t* dst = a.out + static_cast<int64_t>(start + qi) * a.ldo +
-                      (kv_head * group + row - qi * group) * D + g * (D / 4);
+      uint16_t* dst = a.out + static_cast<int64_t>(t.start + at.query) * a.ldo +
+                      (kv_head * a.group + at.head) * D + g * (D / 4);
       // lane (g, c) has elements g * D / 4 + i * D / 16 + n of row c
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -446,22 +523,18 @@ __global__ __launch_bounds__(waves_of(MT, kSplit) * kWave) void kv_attention_ker
     }
     return;
   } else {
-    // The waves' parts, then the workgroups', added in a fixed order.
-    __shared__ float outs[kWaves][kTile][D];
+    // The waves' results, joined in a fixed order.
+    // (rows 4 words apart from a multiple of the banks)
+    __shared__ float outs[kWaves][kTile][D + 4];
     __shared__ float tops[kWaves][kTile], sums[kWaves][kTile];
-    __shared__ int is_last;
-    constexpr int kLanes = D / 4;                    // threads a row, four elements each
+    constexpr int kLanes = D / 4;  // threads a row, four elements each
     constexpr int kRowsAtOnce = kWaves * kWave / kLanes;
-    constexpr int kSteps = (kTile + kRowsAtOnce - 1) / kRowsAtOnce;
-    const int row_0 = tid / kLanes, e = (tid % kLanes) * 4;
-    const int unit = (tile * static_cast<int>(gridDim.x)) + heads;
-    const int64_t slot = static_cast<int64_t>(unit) * a.parts + part;
-    const int64_t units = static_cast<int64_t>(a.row_tiles) * gridDim.x;
-    float* ml = a.partial + units * a.parts * (MT * kTile * D);
-    const bool alone = active <= 1;
+    const int e = (tid % kLanes) * 4;
+    const int64_t slot =
+        (static_cast<int64_t>(unit_of(a, seq, tile, kv_head)) * a.parts + part) * (MT * kTile);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      if (mt > 0) __syncthreads();
+      if (mt > 0) __syncthreads();  // the tile before has been read
       if (g == 0) {
         tops[wave][c] = r.top[mt];
         sums[wave][c] = r.sum[mt];
@@ -471,71 +544,97 @@ __global__ __launch_bounds__(waves_of(MT, kSplit) * kWave) void kv_attention_ker
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) top = fmaxf(top, tops[w][c]);
       const float f = __builtin_amdgcn_exp2f(r.top[mt] - top);
+      if (mt * kTile + c < t.rows) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int n = 0; n < D / 16; ++n)
-          outs[wave][c][g * (D / 4) + i * (D / 16) + n] = r.acc[mt][n][i] * f;
+          for (int n = 0; n < D / 16; ++n)
+            outs[wave][c][g * (D / 4) + i * (D / 16) + n] = r.acc[mt][n][i] * f;
+      }
       __syncthreads();
-#pragma unroll
-      for (int at_row = 0; at_row < kSteps; ++at_row) {
-        const int row_t = row_0 + at_row * kRowsAtOnce;
-        const int row = row0 + mt * kTile + row_t;
-        if (row_t >= kTile || row >= rows) break;
+      for (int row = tid / kLanes; row < kTile && mt * kTile + row < t.rows; row += kRowsAtOnce) {
         top = kNoScore;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, tops[w][row_t]);
+        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, tops[w][row]);
         float total = 0.f;
         f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-          total += sums[w][row_t] * __builtin_amdgcn_exp2f(tops[w][row_t] - top);
+          total += sums[w][row] * __builtin_amdgcn_exp2f(tops[w][row] - top);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] += outs[w][row_t][e + i];
+          for (int i = 0; i < 4; ++i) o[i] += outs[w][row][e + i];
         }
-        if (alone) {
-          store_out(a, start, kv_head * group, row, group, e, D, o, total);
+        if (active == 1) {
+          store_out(a, t, kv_head, mt * kTile + row, D, e, o, total);
         } else {
-          const int64_t at = slot * (MT * kTile) + mt * kTile + row_t;
-          store16_coherent(buffer_rsrc(a.partial + at * D, D * 4), e * 4,
-                           __builtin_bit_cast(u32x4, o));
+          const int64_t at = slot + mt * kTile + row;
+          store16(a.partial + at * D + e, __builtin_bit_cast(u32x4, o));
           if (e == 0)
-            __builtin_amdgcn_raw_buffer_store_b64(
-                u32x2{__float_as_uint(top), __float_as_uint(total)}, buffer_rsrc(ml + at * 2, 8), 0,
-                0, kCachePolicyCoherent);
+            *(LORA_GLOBAL u32x2*)(a.stats + at * 2) =
+                u32x2{__float_as_uint(top), __float_as_uint(total)};
         }
       }
-    }
-    if (alone) return;
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this thread's parts have been written
-    __syncthreads();
-    if (tid == 0)
-      is_last = __hip_atomic_fetch_add(a.arrivals + unit, 1, __ATOMIC_RELAXED,
-                                       __HIP_MEMORY_SCOPE_AGENT) == active - 1;
-    __syncthreads();
-    if (!is_last) return;
-    if (tid == 0) __hip_atomic_store(a.arrivals + unit, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    // the unit's rows in turn, MT * 16 of them
-    for (int row_t = row_0; row_t < MT * kTile && row0 + row_t < rows; row_t += kRowsAtOnce) {
-      const int64_t at0 = static_cast<int64_t>(unit) * a.parts * (MT * kTile) + row_t;
-      float top = kNoScore, total = 0.f;
-      f32x4 o = {0.f, 0.f, 0.f, 0.f};
-      for (int p = 0; p < active; ++p) {
-        const int64_t at = at0 + static_cast<int64_t>(p) * (MT * kTile);
-        const u32x2 w = load8_coherent(buffer_rsrc(ml + at * 2, 8), 0);
-        const f32x4 part_o = __builtin_bit_cast(
-            f32x4, load16_coherent(buffer_rsrc(a.partial + at * D, D * 4), e * 4));
-        const float m = __uint_as_float(w[0]);
-        const float now = fmaxf(top, m);
-        const float fa = __builtin_amdgcn_exp2f(top - now), fb = __builtin_amdgcn_exp2f(m - now);
-        top = now;
-        total = total * fa + __uint_as_float(w[1]) * fb;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = o[i] * fa + part_o[i] * fb;
-      }
-      store_out(a, start, kv_head * group, row0 + row_t, group, e, D, o, total);
     }
   }
+}
+
+// Joins the parts of tiles that have several, one workgroup a row: D / 4 threads
+// side by side on one part's row, kGroups parts at once, then the groups' sums
+// in their order.  A launch of its own: one compute unit draws too little
+// bandwidth to add a long sequence's parts up by itself (131072 tokens, 8 key
+// heads, 32 parts of 8 rows each: 10 us in the last workgroup to arrive, 4 here).
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ __launch_bounds__(kJoinThreads) void kv_attention_join_kernel(AttentionArgs a) {
+  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
+  const int tid = static_cast<int>(threadIdx.x);
+  const int e = (tid % kLanes) * 4, part_group = tid / kLanes;
+  const int kv_head = static_cast<int>(blockIdx.x), seq = static_cast<int>(blockIdx.z);
+  const int tile = static_cast<int>(blockIdx.y) / a.tile_rows;
+  const int row = static_cast<int>(blockIdx.y) - tile * a.tile_rows;
+  RowTile t;
+  if (!tile_of(a, seq, tile, t) || row >= t.rows) return;
+  const int active = parts_of(a, t);
+  if (active == 1) return;
+  const int64_t slot = static_cast<int64_t>(unit_of(a, seq, tile, kv_head)) * a.parts * a.tile_rows + row;
+  float top = kNoScore, total = 0.f;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int p = part_group; p < active; p += kGroups) {
+    const int64_t at = slot + static_cast<int64_t>(p) * a.tile_rows;
+    const u32x2 m = load8(a.stats + at * 2);
+    const f32x4 w = __builtin_bit_cast(f32x4, load16(a.partial + at * D + e));
+    const float now = fmaxf(top, __uint_as_float(m[0]));
+    const float fa = __builtin_amdgcn_exp2f(top - now);
+    const float fb = __builtin_amdgcn_exp2f(__uint_as_float(m[0]) - now);
+    top = now;
+    total = total * fa + __uint_as_float(m[1]) * fb;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = o[i] * fa + w[i] * fb;
+  }
+  __shared__ f32x4 outs[kGroups][kLanes];
+  __shared__ float tops[kGroups], sums[kGroups];
+  outs[part_group][tid % kLanes] = o;
+  if (e == 0) {
+    tops[part_group] = top;
+    sums[part_group] = total;
+  }
+  __syncthreads();
+  if (part_group > 0) return;
+  top = kNoScore;
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) top = fmaxf(top, tops[i]);
+  total = 0.f;
+  o = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) {
+    const float f = __builtin_amdgcn_exp2f(tops[i] - top);
+    total += sums[i] * f;
+    const f32x4 w = outs[i][tid];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] += w[k] * f;
+  }
+  store_out(a, t, kv_head, row, D, e, o, total);
 }
 
 // How a call is cut up: a function of the sizes alone.
@@ -560,10 +659,11 @@ static AttentionPlan attention_plan(int num_seqs, int max_query_len, int64_t max
   const int64_t chunks = (max_len + kChunk - 1) / kChunk;
   p.part_chunks = static_cast<int>(chunks);
   if (!p.split) return p;
-  // About two workgroups a CU; a part is whole rounds of the waves.
+  // About a workgroup a CU, which its registers fill; a part is whole rounds of
+  // the waves (131072 tokens, 8 key heads: 256 workgroups 42.6 us, 512 47.1, 1024 55.9).
   const int waves = waves_of(p.mt, true);
   const int64_t most = (chunks + waves - 1) / waves;
-  p.most_parts = (2 * kCus + p.units - 1) / p.units;
+  p.most_parts = (kCus + p.units - 1) / p.units;
   p.most_parts = p.most_parts < most ? p.most_parts : most;
   const int64_t rounds = (most + p.most_parts - 1) / p.most_parts;
   p.part_chunks = static_cast<int>(rounds * waves);
@@ -571,30 +671,37 @@ static AttentionPlan attention_plan(int num_seqs, int max_query_len, int64_t max
   return p;
 }
 
-static int64_t counter_bytes(const AttentionPlan& p) { return (p.units * 4 + 255) / 256 * 256; }
+// Bytes of the parts' maxima and sums, which lie before their outputs.
+static int64_t stats_bytes(const AttentionPlan& p) {
+  return (p.units * p.most_parts * p.mt * kTile * 8 + 255) / 256 * 256;
+}
 
 int64_t kv_attention_workspace_bytes(int num_seqs, int max_query_len, int max_seq_len, int q_heads,
                                      int kv_heads, int head_dim) {
   if (num_seqs < 1) return 0;
   const AttentionPlan p = attention_plan(num_seqs, max_query_len, max_seq_len, q_heads, kv_heads);
   if (p.most_parts <= 1) return 0;
-  return counter_bytes(p) + p.units * p.most_parts * p.mt * kTile * (head_dim + 2) * 4;
+  return stats_bytes(p) + p.units * p.most_parts * p.mt * kTile * head_dim * 4;
 }
 
 template <int D, int MT, bool kSplit>
-static void launch(const AttentionArgs& a, int heads, hipStream_t stream) {
+static void launch(const AttentionArgs& a, int num_seqs, hipStream_t stream) {
   constexpr int kWaves = waves_of(MT, kSplit);
   const int groups = kSplit ? a.row_tiles * a.parts : (a.row_tiles + kWaves - 1) / kWaves;
-  hipLaunchKernelGGL((kv_attention_kernel<D, MT, kSplit>), dim3(heads, groups),
+  hipLaunchKernelGGL((kv_attention_kernel<D, MT, kSplit>), dim3(a.cache.kv_heads, groups, num_seqs),
                      dim3(kWaves * kWave), 0, stream, a);
 }
 
 template <int D>
-static void launch_for(const AttentionArgs& a, const AttentionPlan& p, int heads, hipStream_t stream) {
-  if (!p.split) launch<D, 4, false>(a, heads, stream);
-  else if (p.mt == 1) launch<D, 1, true>(a, heads, stream);
-  else if (p.mt == 2) launch<D, 2, true>(a, heads, stream);
-  else launch<D, 4, true>(a, heads, stream);
+static void launch_for(const AttentionArgs& a, const AttentionPlan& p, int num_seqs, hipStream_t stream) {
+  if (!p.split) launch<D, 4, false>(a, num_seqs, stream);
+  else if (p.mt == 1) launch<D, 1, true>(a, num_seqs, stream);
+  else if (p.mt == 2) launch<D, 2, true>(a, num_seqs, stream);
+  else launch<D, 4, true>(a, num_seqs, stream);
+  if (p.parts > 1)
+    hipLaunchKernelGGL(kv_attention_join_kernel<D>,
+                       dim3(a.cache.kv_heads, a.max_query_len * a.group, num_seqs),
+                       dim3(kJoinThreads), 0, stream, a);
 }
 
 hipError_t launch_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* query_start,
@@ -604,6 +711,7 @@ hipError_t launch_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* qu
                                int max_seq_len, int q_heads, int kv_heads, int head_dim,
                                float scale, int window, uint16_t* out, int64_t ldo,
                                void* workspace, hipStream_t stream) {
+  const int group = q_heads / kv_heads;
   // A window bounds the tokens that any tile walks; the parts are then fewer
   // than those that the workspace is sized for.
   if (window >= max_seq_len) window = 0;
@@ -617,14 +725,16 @@ hipError_t launch_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* qu
                      {cache, num_pages, page_shift, kv_heads},
                      ldq, ldo, ld_table, num_tokens, max_query_len, max_seq_len, q_heads, window,
                      fabsf(scale) * 1.44269504f, scale < 0.f ? 0x80008000u : 0u,
-                     p.row_tiles, p.parts, p.part_chunks, nullptr, nullptr};
+                     group, ((1 << 21) + group - 1) / group,
+                     p.row_tiles, p.parts, p.part_chunks, kTile * p.mt, nullptr, nullptr};
+  // scores of zero times a hidden token's -infinity must stay -infinity
+  if (a.scale_log2 < 1.17549435e-38f) a.scale_log2 = 1.17549435e-38f;
   if (p.parts > 1) {
-    a.arrivals = static_cast<int*>(workspace);
-    a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + counter_bytes(p));
+    a.stats = static_cast<float*>(workspace);
+    a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + stats_bytes(p));
   }
-  const int heads = num_seqs * kv_heads;
-  if (head_dim == 64) launch_for<64>(a, p, heads, stream);
-  else launch_for<128>(a, p, heads, stream);
+  if (head_dim == 64) launch_for<64>(a, p, num_seqs, stream);
+  else launch_for<128>(a, p, num_seqs, stream);
   return hipGetLastError();
 }
 
