@@ -293,28 +293,51 @@ __device__ __forceinline__ void mask_values(Rows<D, MT>& r, u32x4& scales, const
 template <int D, int MT>
 __device__ __forceinline__ void add_values(Rows<D, MT>& r, const uint32_t (&weights)[MT][8],
                                            const Values& v, const u32x4 scales) {
+  // D / 32 elements of the lane at a time: their operands are D / 8 registers
+  constexpr int kPairs = D / 64;  // words of two elements
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t vt[D / 16][4];  // [element][pair of tokens]
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = 8 * h + 2 * i;
-      const float sa = __uint_as_float(byte_scale(scales[k >> 2], k & 3));
-      const float sb = __uint_as_float(byte_scale(scales[k >> 2], (k + 1) & 3));
-      const u32x4 a = word_to_bf16(v.w[k], sa), b = word_to_bf16(v.w[k + 1], sb);
+    for (int half = 0; half < 2; ++half) {
+      if constexpr (MT == 1) __builtin_amdgcn_sched_barrier(0);
+      uint32_t vt[2 * kPairs][4];  // [element][pair of tokens]
 #pragma unroll
-      for (int n = 0; n < D / 32; ++n) {
-        vt[2 * n][i] = __builtin_amdgcn_perm(b[n], a[n], 0x05040100u);
-        vt[2 * n + 1][i] = __builtin_amdgcn_perm(b[n], a[n], 0x07060302u);
+      for (int i = 0; i < 4; ++i) {
+        const int k = 8 * h + 2 * i;
+        const float sa = __uint_as_float(byte_scale(scales[k >> 2], k & 3));
+        const float sb = __uint_as_float(byte_scale(scales[k >> 2], (k + 1) & 3));
+        uint32_t a[2], b[2];
+        if (half == 0) {
+          a[0] = codes_to_bf16<0>(v.w[k], sa);
+          b[0] = codes_to_bf16<0>(v.w[k + 1], sb);
+          if constexpr (kPairs == 2) {
+            a[1] = codes_to_bf16<1>(v.w[k], sa);
+            b[1] = codes_to_bf16<1>(v.w[k + 1], sb);
+          }
+        } else {
+          a[0] = codes_to_bf16<kPairs>(v.w[k], sa);
+          b[0] = codes_to_bf16<kPairs>(v.w[k + 1], sb);
+          if constexpr (kPairs == 2) {
+            a[1] = codes_to_bf16<3>(v.w[k], sa);
+            b[1] = codes_to_bf16<3>(v.w[k + 1], sb);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < kPairs; ++n) {
+          vt[2 * n][i] = __builtin_amdgcn_perm(b[n], a[n], 0x05040100u);
+          vt[2 * n + 1][i] = __builtin_amdgcn_perm(b[n], a[n], 0x07060302u);
+        }
       }
-    }
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const bf16x8 p = as_bf16x8(weights[mt][4 * h], weights[mt][4 * h + 1], weights[mt][4 * h + 2],
-                                 weights[mt][4 * h + 3]);
+      for (int mt = 0; mt < MT; ++mt) {
+        const bf16x8 p = as_bf16x8(weights[mt][4 * h], weights[mt][4 * h + 1],
+                                   weights[mt][4 * h + 2], weights[mt][4 * h + 3]);
 #pragma unroll
-      for (int n = 0; n < D / 16; ++n)
-        r.acc[mt][n] = mfma(as_bf16x8(vt[n][0], vt[n][1], vt[n][2], vt[n][3]), p, r.acc[mt][n]);
+        for (int n = 0; n < 2 * kPairs; ++n) {
+          const int at = half * 2 * kPairs + n;
+          r.acc[mt][at] = mfma(as_bf16x8(vt[n][0], vt[n][1], vt[n][2], vt[n][3]), p, r.acc[mt][at]);
+        }
+      }
     }
   }
 }
@@ -380,6 +403,34 @@ __device__ __forceinline__ int unit_of(const AttentionArgs& a, int seq, int tile
   return (seq * a.row_tiles + tile) * a.cache.kv_heads + kv_head;
 }
 
+// The sequence that the index'th workgroups of a launch take: the one with the
+// index'th most work (its tokens times row tiles), so that the longest start
+// first and the shortest fill the gaps at the end.  Every wave ranks the
+// sequences for itself; with more than a wave's lanes of them, many workgroups a
+// compute unit even the work out and they are taken as they come.
+__device__ __forceinline__ int sequence_at(const AttentionArgs& a, int index) {
+  const int n = static_cast<int>(gridDim.z);
+  if (n == 1 || n > kWave) return index;
+  const int lane = lane_id();
+  float work = -1.f;
+  if (lane < n) {
+    uint32_t queries = static_cast<uint32_t>(a.query_start[lane + 1]) -
+                       static_cast<uint32_t>(a.query_start[lane]);
+    const uint32_t most = static_cast<uint32_t>(a.max_query_len);
+    queries = queries < most ? queries : most;
+    const int length = a.seq_lens[lane];
+    work = static_cast<float>(length > 0 ? length : 0) *
+           static_cast<float>((queries * a.group + a.tile_rows - 1) / a.tile_rows);
+  }
+  int rank = 0;
+  for (int i = 0; i < n; ++i) {
+    const float other = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(work), i));
+    rank += other > work || (other == work && i < lane) ? 1 : 0;
+  }
+  const unsigned long long hit = __ballot(lane < n && rank == index);
+  return __ffsll(static_cast<long long>(hit)) - 1;
+}
+
 // Four neighbouring outputs of a row, divided by its sum; a row that saw nothing
 // gets zeros.
 __device__ __forceinline__ void store_out(const AttentionArgs& a, const RowTile& t, int kv_head, int row,
@@ -405,10 +456,11 @@ __global__ __launch_bounds__(waves_of(MT, kSplit) * kWave, waves_a_simd(MT)) voi
   // blockIdx: key head, then row tile (or workgroup of tiles) and part, then
   // sequence.  Neighbours go to other XCDs; with a multiple of 8 key heads the
   // workgroups of one head share an XCD and find its cache in their L2.
-  const int kv_head = static_cast<int>(blockIdx.x), seq = static_cast<int>(blockIdx.z);
+  const int kv_head = static_cast<int>(blockIdx.x);
+  const int seq = sequence_at(a, static_cast<int>(blockIdx.z));
   const int part = kSplit ? static_cast<int>(blockIdx.y) % a.parts : 0;
   const int tile = kSplit ? static_cast<int>(blockIdx.y) / a.parts
-                          : static_cast<int>(blockIdx.y) * kWaves + wave;
+                          : (static_cast<int>(gridDim.y - 1 - blockIdx.y)) * kWaves + wave;
 
   Reader<D> reader;
   const int64_t block = static_cast<int64_t>(D / 2 + D / kBlock) << a.cache.page_shift;
@@ -650,7 +702,7 @@ static AttentionPlan attention_plan(int num_seqs, int max_query_len, int64_t max
                                     int kv_heads) {
   AttentionPlan p;
   const int64_t rows = static_cast<int64_t>(max_query_len) * (q_heads / kv_heads);
-  p.mt = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
+  p.mt = rows <= 16 ? 1 : (rows <= 32 || rows >= 256 ? 2 : 4);
   p.split = rows < 256;
   p.row_tiles = static_cast<int>((rows + kTile * p.mt - 1) / (kTile * p.mt));
   p.units = static_cast<int64_t>(num_seqs) * kv_heads * p.row_tiles;
@@ -694,7 +746,7 @@ static void launch(const AttentionArgs& a, int num_seqs, hipStream_t stream) {
 
 template <int D>
 static void launch_for(const AttentionArgs& a, const AttentionPlan& p, int num_seqs, hipStream_t stream) {
-  if (!p.split) launch<D, 4, false>(a, num_seqs, stream);
+  if (!p.split) launch<D, 2, false>(a, num_seqs, stream);
   else if (p.mt == 1) launch<D, 1, true>(a, num_seqs, stream);
   else if (p.mt == 2) launch<D, 2, true>(a, num_seqs, stream);
   else launch<D, 4, true>(a, num_seqs, stream);
