@@ -147,7 +147,9 @@ lora_status_t lora_kv_read(const int64_t *slots, int32_t num_tokens, int32_t kv_
  *                its length may be anything.  The tokens of a page outside
  *                [0, num_pages) are skipped.
  *   max_seq_len  1 <= max_seq_len <= ld_table * page_size.
- *   q_heads      multiple of kv_heads, at most 1024.
+ *   num_seqs     0 <= num_seqs <= 65535.
+ *   q_heads      multiple of kv_heads, at most 1024.  max_query_len * (q_heads /
+ *                kv_heads) <= 2^22 (LORA_ERR_UNSUPPORTED otherwise).
  *   scale        finite.
  *   window       0 (none) or the number of keys, the query's own among them,
  *                that a query may see.

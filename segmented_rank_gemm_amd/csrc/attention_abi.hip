@@ -37,7 +37,8 @@ namespace {
 constexpr int32_t kMaxTokens = 1 << 24;
 constexpr int32_t kMaxHidden = 65536;
 constexpr int32_t kMaxHeads = 1024;
-constexpr int32_t kMaxSeqs = 1 << 16;
+constexpr int32_t kMaxSeqs = 65535;     // a grid dimension
+constexpr int64_t kMaxRows = 1 << 22;   // queries times heads a key head, of one sequence
 constexpr int32_t kMaxSeqLen = 1 << 30;
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -151,7 +152,8 @@ int64_t lora_kv_attention_workspace_bytes(int32_t num_seqs, int32_t max_query_le
                                           int32_t max_seq_len, int32_t q_heads, int32_t kv_heads,
                                           int32_t head_dim) {
   if (!attention_sizes_ok(num_seqs, max_query_len, max_seq_len, q_heads, kv_heads) ||
-      (head_dim != 64 && head_dim != 128))
+      (head_dim != 64 && head_dim != 128) ||
+      static_cast<int64_t>(max_query_len) * (q_heads / kv_heads) > kMaxRows)
     return 0;
   return lora::kv_attention_workspace_bytes(num_seqs, max_query_len, max_seq_len, q_heads, kv_heads,
                                             head_dim);
@@ -179,6 +181,8 @@ lora_status_t lora_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* q
   if (num_tokens > 0 && (!rows_ok(q, ldq, width) || !rows_ok(out, ldo, width)))
     return LORA_ERR_INVALID_ARGUMENT;
   if (st != LORA_OK) return st;
+  if (static_cast<int64_t>(max_query_len) * (q_heads / kv_heads) > kMaxRows)
+    return LORA_ERR_UNSUPPORTED;
   const int64_t need = lora_kv_attention_workspace_bytes(num_seqs, max_query_len, max_seq_len,
                                                          q_heads, kv_heads, head_dim);
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))

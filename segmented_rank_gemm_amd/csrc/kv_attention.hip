@@ -29,10 +29,13 @@ namespace lora {
 
 constexpr int kChunk = 64;       // tokens of a wave's step
 constexpr int kTile = 16;        // rows of one matrix product
-__host__ __device__ constexpr int waves_a_simd(int mt) { return mt == 1 ? 2 : (mt == 2 ? 2 : 1); }
-// Waves of a workgroup: they share out one tile's tokens (split), or have tiles
-// of their own.  More row tiles a wave need the registers of four waves.
-__host__ __device__ constexpr int waves_of(int mt, bool split) { return split && mt == 1 ? 8 : 4; }
+// Waves that share out the tokens of a tile of mt * 16 rows: two a SIMD at the
+// registers that they take.
+__host__ __device__ constexpr int split_waves(int mt) { return mt == 1 ? 8 : 4; }
+// Many rows: waves of a workgroup, and 16-row tiles of a wave.
+constexpr int kRowWaves = 4;
+constexpr int kRowTiles = 2;
+constexpr int kManyRows = 128;
 constexpr float kNoScore = -3.402823466e38f;  // the running maximum before any score
 // The running maximum moves only when a score passes it by this many powers of
 // two; weights up to 2^8 lose nothing in fp32 sums or bf16 mantissas.
@@ -183,29 +186,11 @@ __device__ __forceinline__ uint32_t seen_bits(const Span& at, int place) {
   return at.ok && hi >= lo ? ((2u << hi) - 1u) & ~((1u << lo) - 1u) : 0u;
 }
 
-// Scores of one chunk, the running softmax, and the weights in bf16 (pairs of
-// tokens 16 g + 2 i, + 1).  q: the operand [mt][D / 32][lane] in shared memory.
+// The running softmax over one chunk's scores s[mt][j][i] (of token 16 g + 4 i + j),
+// and the weights in bf16 (pairs of tokens 16 g + 2 i, + 1).
 template <int D, int MT>
-__device__ __forceinline__ void weigh(Rows<D, MT>& r, uint32_t (&weights)[MT][8], const Keys<D>& k,
-                                      const u32x4* q, const Span& at, float scale_log2) {
-  f32x4 s[MT][4];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s[mt][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    bf16x8 b[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-      b[mt] = __builtin_bit_cast(bf16x8, q[(mt * (D / 32) + i) * kWave + lane_id()]);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const u32x4 w = word_to_bf16(k.w[j][i], __uint_as_float(byte_scale(k.scales, j)));
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) s[mt][j] = mfma(__builtin_bit_cast(bf16x8, w), b[mt], s[mt][j]);
-    }
-  }
+__device__ __forceinline__ void soften(Rows<D, MT>& r, uint32_t (&weights)[MT][8],
+                                       f32x4 (&s)[MT][4], const Span& at, float scale_log2) {
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     if (at.masked) {
@@ -247,22 +232,37 @@ __device__ __forceinline__ void weigh(Rows<D, MT>& r, uint32_t (&weights)[MT][8]
   }
 }
 
-// Values that no row sees may be anything: their weights are zero, and their
-// scales are made so.  A NaN block that some rows see and others do not is
-// taken out too and marks the outputs that it reaches: those for which the sum
-// over its tokens of "seen" is not zero.
+// Scores of one chunk and their weights.  q: the operand [mt][D / 32][lane] in
+// shared memory.
 template <int D, int MT>
-__device__ __forceinline__ void mask_values(Rows<D, MT>& r, u32x4& scales, const Span& at) {
-  uint32_t nan = 0;
-  const int token = at.base + 16 * (lane_id() >> 4);
+__device__ __forceinline__ void weigh(Rows<D, MT>& r, uint32_t (&weights)[MT][8], const Keys<D>& k,
+                                      const u32x4* q, const Span& at, float scale_log2) {
+  f32x4 s[MT][4];
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const uint32_t byte = 255u << (8 * (k & 3));
-    const bool none = !at.ok || token + k >= at.last || token + k < at.first;
-    const bool bad = at.several && (scales[k >> 2] & byte) == byte;
-    if (bad && !none) nan |= 1u << k;
-    if (bad || none) scales[k >> 2] &= ~byte;
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[mt][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    bf16x8 b[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+      b[mt] = __builtin_bit_cast(bf16x8, q[(mt * (D / 32) + i) * kWave + lane_id()]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const u32x4 w = word_to_bf16(k.w[j][i], __uint_as_float(byte_scale(k.scales, j)));
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) s[mt][j] = mfma(__builtin_bit_cast(bf16x8, w), b[mt], s[mt][j]);
+    }
   }
+  soften<D, MT>(r, weights, s, at, scale_log2);
+}
+
+// Bits `nan` of this lane's 16 tokens: value blocks that held a NaN and were
+// taken out.  Marks the outputs that they reach: those for which the sum over
+// these tokens of "seen" is not zero.
+template <int D, int MT>
+__device__ __forceinline__ void mark_nan(Rows<D, MT>& r, uint32_t nan, const Span& at) {
   if (!__any(nan != 0)) return;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
@@ -287,6 +287,24 @@ __device__ __forceinline__ void mask_values(Rows<D, MT>& r, u32x4& scales, const
       for (int n = 0; n < D / 16; ++n) r.acc[mt][n][i] += add;
     }
   }
+}
+
+// Values that no row sees may be anything: their weights are zero, and their
+// scales are made so.  A NaN block that some rows see and others do not is
+// taken out too (mark_nan).
+template <int D, int MT>
+__device__ __forceinline__ void mask_values(Rows<D, MT>& r, u32x4& scales, const Span& at) {
+  uint32_t nan = 0;
+  const int token = at.base + 16 * (lane_id() >> 4);
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const uint32_t byte = 255u << (8 * (k & 3));
+    const bool none = !at.ok || token + k >= at.last || token + k < at.first;
+    const bool bad = at.several && (scales[k >> 2] & byte) == byte;
+    if (bad && !none) nan |= 1u << k;
+    if (bad || none) scales[k >> 2] &= ~byte;
+  }
+  mark_nan<D, MT>(r, nan, at);
 }
 
 // The weighted values of one chunk.
@@ -399,32 +417,27 @@ __device__ __forceinline__ int parts_of(const AttentionArgs& a, const RowTile& t
   return n > 1 ? n : 1;
 }
 
-__device__ __forceinline__ int unit_of(const AttentionArgs& a, int seq, int tile, int kv_head) {
-  return (seq * a.row_tiles + tile) * a.cache.kv_heads + kv_head;
+__device__ __forceinline__ int64_t unit_of(const AttentionArgs& a, int seq, int tile, int kv_head) {
+  return (static_cast<int64_t>(seq) * a.row_tiles + tile) * a.cache.kv_heads + kv_head;
 }
 
 // The sequence that the index'th workgroups of a launch take: the one with the
-// index'th most work (its tokens times row tiles), so that the longest start
-// first and the shortest fill the gaps at the end.  Every wave ranks the
+// index'th most tokens, so that the longest start first and the shortest fill
+// the gaps at the end.  Every wave ranks the
 // sequences for itself; with more than a wave's lanes of them, many workgroups a
 // compute unit even the work out and they are taken as they come.
 __device__ __forceinline__ int sequence_at(const AttentionArgs& a, int index) {
   const int n = static_cast<int>(gridDim.z);
   if (n == 1 || n > kWave) return index;
   const int lane = lane_id();
-  float work = -1.f;
+  int work = -1;
   if (lane < n) {
-    uint32_t queries = static_cast<uint32_t>(a.query_start[lane + 1]) -
-                       static_cast<uint32_t>(a.query_start[lane]);
-    const uint32_t most = static_cast<uint32_t>(a.max_query_len);
-    queries = queries < most ? queries : most;
-    const int length = a.seq_lens[lane];
-    work = static_cast<float>(length > 0 ? length : 0) *
-           static_cast<float>((queries * a.group + a.tile_rows - 1) / a.tile_rows);
+    work = a.seq_lens[lane];
+    work = work < 0 || a.query_start[lane + 1] <= a.query_start[lane] ? 0 : work;
   }
   int rank = 0;
   for (int i = 0; i < n; ++i) {
-    const float other = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(work), i));
+    const int other = __builtin_amdgcn_readlane(work, i);
     rank += other > work || (other == work && i < lane) ? 1 : 0;
   }
   const unsigned long long hit = __ballot(lane < n && rank == index);
@@ -442,13 +455,41 @@ __device__ __forceinline__ void store_out(const AttentionArgs& a, const RowTile&
       u32x2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
 }
 
-// kSplit: the workgroup's waves share out the tokens of one row tile, and the
-// workgroups of a unit its parts; otherwise each wave has a row tile of its own
-// and walks all of that tile's tokens.
-template <int D, int MT, bool kSplit>
-__global__ __launch_bounds__(waves_of(MT, kSplit) * kWave, waves_a_simd(MT)) void kv_attention_kernel(
-    AttentionArgs a) {
-  constexpr int kWaves = waves_of(MT, kSplit);
+template <int D>
+__device__ __forceinline__ Reader<D> reader_of(const AttentionArgs& a, int seq, int kv_head) {
+  Reader<D> r;
+  const int64_t block = static_cast<int64_t>(D / 2 + D / kBlock) << a.cache.page_shift;
+  r.keys = a.cache.data + kv_head * block;
+  r.values = r.keys + a.cache.kv_heads * block;
+  r.page_stride = 2 * a.cache.kv_heads * block;
+  r.table = a.page_table + seq * a.ld_table;
+  r.shift = a.cache.page_shift;
+  r.num_pages = a.cache.num_pages;
+  r.max_seq_len = a.max_seq_len;
+  return r;
+}
+
+// Lane (g, c)'s part of the i-th B operand of 16 queries: elements g * D / 4 +
+// 8 i .. + 7 of tile row `row` (c's); rows past the tile's are zero.
+template <int D>
+__device__ __forceinline__ u32x4 query_operand(const AttentionArgs& a, const RowTile& t, int kv_head,
+                                               int row, int i) {
+  u32x4 w = {0, 0, 0, 0};
+  if (row < t.rows) {
+    const RowOf at = row_of(a, t.query0, t.head0, row);
+    w = load16(a.q + static_cast<int64_t>(t.start + at.query) * a.ldq +
+               (kv_head * a.group + at.head) * D + (lane_id() >> 4) * (D / 4) + 8 * i);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] ^= a.sign;
+  return w;
+}
+
+// Few rows: the workgroup's waves share out the tokens of one row tile, and the
+// workgroups of a unit (sequence, key head, row tile) its parts.
+template <int D, int MT>
+__global__ __launch_bounds__(split_waves(MT) * kWave, 2) void kv_attention_kernel(AttentionArgs a) {
+  constexpr int kWaves = split_waves(MT);
   const int tid = static_cast<int>(threadIdx.x);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int lane = lane_id(), g = lane >> 4, c = lane & 15;
@@ -458,60 +499,36 @@ __global__ __launch_bounds__(waves_of(MT, kSplit) * kWave, waves_a_simd(MT)) voi
   // workgroups of one head share an XCD and find its cache in their L2.
   const int kv_head = static_cast<int>(blockIdx.x);
   const int seq = sequence_at(a, static_cast<int>(blockIdx.z));
-  const int part = kSplit ? static_cast<int>(blockIdx.y) % a.parts : 0;
-  const int tile = kSplit ? static_cast<int>(blockIdx.y) / a.parts
-                          : (static_cast<int>(gridDim.y - 1 - blockIdx.y)) * kWaves + wave;
+  const int tile = static_cast<int>(blockIdx.y) / a.parts;
+  const int part = static_cast<int>(blockIdx.y) - tile * a.parts;
 
-  Reader<D> reader;
-  const int64_t block = static_cast<int64_t>(D / 2 + D / kBlock) << a.cache.page_shift;
-  reader.keys = a.cache.data + kv_head * block;
-  reader.values = reader.keys + a.cache.kv_heads * block;
-  reader.page_stride = 2 * a.cache.kv_heads * block;
-  reader.table = a.page_table + seq * a.ld_table;
-  reader.shift = a.cache.page_shift;
-  reader.num_pages = a.cache.num_pages;
-  reader.max_seq_len = a.max_seq_len;
+  const Reader<D> reader = reader_of<D>(a, seq, kv_head);
   // Without a window the first chunk does not depend on the lengths: its pages
   // are looked up beside them.
-  constexpr int step = kSplit ? kWaves : 1;
-  int chunk = kSplit ? part * a.part_chunks + wave : 0;
+  int chunk = part * a.part_chunks + wave;
   Pages pages = {-1, -1};
   if (!a.window) pages = reader.pages(chunk * kChunk);
 
   RowTile t;
-  // the whole workgroup (kSplit), or a wave that shares nothing, is done here
   if (!tile_of(a, seq, tile, t)) return;
-  const int active = kSplit ? parts_of(a, t) : 1;
-  if (kSplit && part >= active) return;
+  const int active = parts_of(a, t);
+  if (part >= active) return;
   chunk += t.chunk0;
-  int stop = t.chunk1;
-  if constexpr (kSplit) {
-    stop = t.chunk0 + (part + 1) * a.part_chunks;
-    stop = stop < t.chunk1 ? stop : t.chunk1;
-  }
+  int stop = t.chunk0 + (part + 1) * a.part_chunks;
+  stop = stop < t.chunk1 ? stop : t.chunk1;
   if (a.window) pages = reader.pages(chunk * kChunk);
 
-  // The queries as B operands in shared memory: one tile for all waves, or one each.
-  __shared__ u32x4 q_shared[kSplit ? 1 : kWaves][MT * (D / 32)][kWave];
-  u32x4(*q)[kWave] = q_shared[kSplit ? 0 : wave];
+  // The queries as B operands, for all waves.
+  __shared__ u32x4 q[MT * (D / 32)][kWave];
   Keys<D> keys;
   Values values;
   if (chunk < stop) {
     reader.load(keys, pages, chunk * kChunk);
     reader.load(values, pages, chunk * kChunk);
   }
-  Pages ahead = reader.pages((chunk + step) * kChunk);
-  for (int f = kSplit ? wave : 0; f < MT * (D / 32); f += kSplit ? kWaves : 1) {
-    const int mt = f / (D / 32), i = f % (D / 32);
-    const RowOf at = row_of(a, t.query0, t.head0, mt * kTile + c);
-    u32x4 w = {0, 0, 0, 0};
-    if (mt * kTile + c < t.rows)
-      w = load16(a.q + static_cast<int64_t>(t.start + at.query) * a.ldq +
-                 (kv_head * a.group + at.head) * D + g * (D / 4) + 8 * i);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] ^= a.sign;
-    q[f][lane] = w;
-  }
+  Pages ahead = reader.pages((chunk + kWaves) * kChunk);
+  for (int f = wave; f < MT * (D / 32); f += kWaves)
+    q[f][lane] = query_operand<D>(a, t, kv_head, (f / (D / 32)) * kTile + c, f % (D / 32));
   Rows<D, MT> r;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
@@ -521,11 +538,11 @@ __global__ __launch_bounds__(waves_of(MT, kSplit) * kWave, waves_a_simd(MT)) voi
 #pragma unroll
     for (int n = 0; n < D / 16; ++n) r.acc[mt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  if constexpr (kSplit) __syncthreads();
+  __syncthreads();
 
   // The next chunk's keys are on their way from the scores on, its values from
   // the products on, and the pages of the one after it are looked up.
-  for (; chunk < stop; chunk += step) {
+  for (; chunk < stop; chunk += kWaves) {
     Span at;
     at.base = chunk * kChunk;
     at.first = t.first;
@@ -537,15 +554,15 @@ __global__ __launch_bounds__(waves_of(MT, kSplit) * kWave, waves_a_simd(MT)) voi
                 !__all(pages.v >= 0 && pages.k >= 0);
     uint32_t weights[MT][8];
     weigh<D, MT>(r, weights, keys, &q[0][0], at, a.scale_log2);
-    const bool more = chunk + step < stop;
-    if (more) reader.load(keys, ahead, at.base + step * kChunk);
+    const bool more = chunk + kWaves < stop;
+    if (more) reader.load(keys, ahead, at.base + kWaves * kChunk);
     u32x4 scales = values.scales;
     if (at.masked) mask_values<D, MT>(r, scales, at);
     add_values<D, MT>(r, weights, values, scales);
     if (more) {
-      reader.load(values, ahead, at.base + step * kChunk);
+      reader.load(values, ahead, at.base + kWaves * kChunk);
       pages = ahead;
-      ahead = reader.pages(at.base + 2 * step * kChunk);
+      ahead = reader.pages(at.base + 2 * kWaves * kChunk);
     }
   }
 #pragma unroll
@@ -554,135 +571,346 @@ __global__ __launch_bounds__(waves_of(MT, kSplit) * kWave, waves_a_simd(MT)) voi
     r.sum[mt] += __shfl_xor(r.sum[mt], 32);
   }
 
-  if constexpr (!kSplit) {
+  // The waves' results, joined in a fixed order.
+  // (rows 4 words apart from a multiple of the banks)
+  __shared__ float outs[kWaves][kTile][D + 4];
+  __shared__ float tops[kWaves][kTile], sums[kWaves][kTile];
+  constexpr int kLanes = D / 4;  // threads a row, four elements each
+  constexpr int kRowsAtOnce = kWaves * kWave / kLanes;
+  const int e = (tid % kLanes) * 4;
+  const int64_t slot =
+      (unit_of(a, seq, tile, kv_head) * a.parts + part) * (MT * kTile);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      if (mt * kTile + c >= t.rows) continue;
-      const RowOf at = row_of(a, t.query0, t.head0, mt * kTile + c);
-      const float inv = r.sum[mt] == 0.f ? 0.f : 1.f / r.sum[mt];
-      uint16_t* dst = a.out + static_cast<int64_t>(t.start + at.query) * a.ldo +
-                      (kv_head * a.group + at.head) * D + g * (D / 4);
-      // lane (g, c) has elements g * D / 4 + i * D / 16 + n of row c
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w[D / 32];
-#pragma unroll
-        for (int n = 0; n < D / 32; ++n)
-          w[n] = pack_bf16x2(r.acc[mt][2 * n][i] * inv, r.acc[mt][2 * n + 1][i] * inv);
-        if constexpr (D == 128) store16(dst + i * (D / 16), u32x4{w[0], w[1], w[2], w[3]});
-        else *(LORA_GLOBAL u32x2*)(dst + i * (D / 16)) = u32x2{w[0], w[1]};
-      }
+  for (int mt = 0; mt < MT; ++mt) {
+    if (mt > 0) __syncthreads();  // the tile before has been read
+    if (g == 0) {
+      tops[wave][c] = r.top[mt];
+      sums[wave][c] = r.sum[mt];
     }
-    return;
-  } else {
-    // The waves' results, joined in a fixed order.
-    // (rows 4 words apart from a multiple of the banks)
-    __shared__ float outs[kWaves][kTile][D + 4];
-    __shared__ float tops[kWaves][kTile], sums[kWaves][kTile];
-    constexpr int kLanes = D / 4;  // threads a row, four elements each
-    constexpr int kRowsAtOnce = kWaves * kWave / kLanes;
-    const int e = (tid % kLanes) * 4;
-    const int64_t slot =
-        (static_cast<int64_t>(unit_of(a, seq, tile, kv_head)) * a.parts + part) * (MT * kTile);
+    __syncthreads();
+    float top = kNoScore;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      if (mt > 0) __syncthreads();  // the tile before has been read
-      if (g == 0) {
-        tops[wave][c] = r.top[mt];
-        sums[wave][c] = r.sum[mt];
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, tops[w][c]);
+    const float f = __builtin_amdgcn_exp2f(r.top[mt] - top);
+    if (mt * kTile + c < t.rows) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n)
+          outs[wave][c][g * (D / 4) + i * (D / 16) + n] = r.acc[mt][n][i] * f;
+    }
+    __syncthreads();
+    for (int row = tid / kLanes; row < kTile && mt * kTile + row < t.rows; row += kRowsAtOnce) {
+      top = kNoScore;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, tops[w][row]);
+      float total = 0.f;
+      f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        total += sums[w][row] * __builtin_amdgcn_exp2f(tops[w][row] - top);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] += outs[w][row][e + i];
       }
-      __syncthreads();
-      float top = kNoScore;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, tops[w][c]);
-      const float f = __builtin_amdgcn_exp2f(r.top[mt] - top);
-      if (mt * kTile + c < t.rows) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int n = 0; n < D / 16; ++n)
-            outs[wave][c][g * (D / 4) + i * (D / 16) + n] = r.acc[mt][n][i] * f;
-      }
-      __syncthreads();
-      for (int row = tid / kLanes; row < kTile && mt * kTile + row < t.rows; row += kRowsAtOnce) {
-        top = kNoScore;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, tops[w][row]);
-        float total = 0.f;
-        f32x4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          total += sums[w][row] * __builtin_amdgcn_exp2f(tops[w][row] - top);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] += outs[w][row][e + i];
-        }
-        if (active == 1) {
-          store_out(a, t, kv_head, mt * kTile + row, D, e, o, total);
-        } else {
-          const int64_t at = slot + mt * kTile + row;
-          store16(a.partial + at * D + e, __builtin_bit_cast(u32x4, o));
-          if (e == 0)
-            *(LORA_GLOBAL u32x2*)(a.stats + at * 2) =
-                u32x2{__float_as_uint(top), __float_as_uint(total)};
-        }
+      if (active == 1) {
+        store_out(a, t, kv_head, mt * kTile + row, D, e, o, total);
+      } else {
+        const int64_t at = slot + mt * kTile + row;
+        store16(a.partial + at * D + e, __builtin_bit_cast(u32x4, o));
+        if (e == 0)
+          *(LORA_GLOBAL u32x2*)(a.stats + at * 2) =
+              u32x2{__float_as_uint(top), __float_as_uint(total)};
       }
     }
   }
 }
 
-// Joins the parts of tiles that have several, one workgroup a row: D / 4 threads
-// side by side on one part's row, kGroups parts at once, then the groups' sums
-// in their order.  A launch of its own: one compute unit draws too little
-// bandwidth to add a long sequence's parts up by itself (131072 tokens, 8 key
-// heads, 32 parts of 8 rows each: 10 us in the last workgroup to arrive, 4 here).
+// Many rows (pieces of prompts): each of the workgroup's waves has kRowTiles * 16
+// rows of its own, and all walk the same chunks.  A chunk's codes are turned into
+// bf16 operands once for all of them: each wave takes a quarter of the keys and of
+// the values, and leaves its operands in shared memory in the order in which the
+// matrix unit's lanes take them (16 bytes a lane, so neither side has bank
+// conflicts).  Two buffers and one barrier a chunk; the codes of the next chunk
+// are on their way meanwhile.
+template <int D>
+__global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel(AttentionArgs a) {
+  constexpr int MT = kRowTiles;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+  const int lane = lane_id(), g = lane >> 4, c = lane & 15;
+  const int kv_head = static_cast<int>(blockIdx.x);
+  const int seq = sequence_at(a, static_cast<int>(blockIdx.z));
+  // the last rows of a sequence see the most
+  const int tile = static_cast<int>(gridDim.y - 1 - blockIdx.y);
+  RowTile t;
+  if (!tile_of(a, seq, tile, t)) return;
+  const Reader<D> reader = reader_of<D>(a, seq, kv_head);
+
+  // This wave's rows, and what they see.
+  const int row0 = wave * (MT * kTile);
+  const int left = t.rows - row0;
+  const int mine = left < 0 ? 0 : (left < MT * kTile ? left : MT * kTile);
+  int first = 0, last = 0, all_first = 0, all_last = 0;
+  if (mine > 0) {
+    const int place0 = t.before + row_of(a, t.query0, t.head0, row0).query;
+    const int place1 = t.before + row_of(a, t.query0, t.head0, row0 + mine - 1).query;
+    last = place1 + 1;
+    first = a.window && place0 >= a.window ? place0 - a.window + 1 : 0;
+    all_first = a.window && place1 >= a.window ? place1 - a.window + 1 : 0;
+    all_last = place0 + 1;
+  }
+  bf16x8 q[MT][D / 32];
+  Rows<D, MT> r;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int row = row0 + mt * kTile + c;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+      q[mt][i] = __builtin_bit_cast(bf16x8, query_operand<D>(a, t, kv_head, row, i));
+    r.place[mt] = t.before + row_of(a, t.query0, t.head0, row).query;
+    r.top[mt] = kNoScore;
+    r.sum[mt] = 0.f;
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n) r.acc[mt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  __shared__ u32x4 keys[2][4][D / 32][kWave];    // [buffer][tile j][step i][lane]
+  __shared__ u32x4 values[2][2][D / 16][kWave];  // [buffer][half of the tokens][element][lane]
+  __shared__ uint32_t nans[2][2][4][D / kBlock];  // [buffer][half][g][block]: bits of 8 tokens
+
+  // What this wave turns into operands: the keys of tile j = wave, and of the
+  // values the tokens' half `half` and the elements' half `side`.
+  const int half = wave >> 1, side = wave & 1;
+  uint32_t kw[D / 32], vw[8];
+  uint32_t kscale;
+  u32x2 vscale;
+  bool ok = false, all_ok = false;
+  auto load = [&](Pages p, int base) {
+    ok = p.v >= 0;
+    all_ok = __all(p.v >= 0 && p.k >= 0);
+    const int in = (1 << reader.shift) - 1;
+    const int ka = (base + 4 * c) & in, va = (base + 16 * g) & in;
+    const uint8_t* kb = reader.keys + (p.k < 0 ? 0 : p.k) * reader.page_stride;
+    const uint8_t* vb = reader.values + (p.v < 0 ? 0 : p.v) * reader.page_stride;
+    const uint8_t* kr = kb + (ka + wave) * (D / 2) + g * (D / 8);
+    const uint8_t* vr = vb + (va + 8 * half) * (D / 2) + c * (D / 32);
+    if constexpr (D == 128) {
+      const u32x4 w = load16(kr);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) kw[i] = w[i];
+    } else {
+      const u32x2 w = load8(kr);
+      kw[0] = w[0];
+      kw[1] = w[1];
+    }
+    kscale = *(const LORA_GLOBAL uint32_t*)(kb + (((D / 2) + g * (D / 4) / kBlock) << reader.shift) + ka);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if constexpr (D == 128) vw[k] = *(const LORA_GLOBAL uint32_t*)(vr + k * (D / 2));
+      else vw[k] = *(const LORA_GLOBAL uint16_t*)(vr + k * (D / 2));
+    }
+    vscale = load8(vb + (((D / 2) + c * (D / 16) / kBlock) << reader.shift) + va + 8 * half);
+  };
+  // True if some row of the workgroup does not see all of the chunk at `base`.
+  auto partial = [&](int base) {
+    return base < t.all_first || base + kChunk > t.all_last || !all_ok;
+  };
+  auto stage = [&](int buffer, int base) {
+    const float ks = __uint_as_float(((kscale >> (8 * wave)) & 255u) << 23);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) keys[buffer][wave][i][lane] = word_to_bf16(kw[i], ks);
+    if (partial(base)) {
+      // as mask_values, for the tokens that no row of the workgroup sees
+      const bool several = t.query1 != t.query0;
+      uint32_t nan = 0;
+      const int token = base + 16 * g + 8 * half;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t byte = 255u << (8 * (k & 3));
+        const bool none = !ok || token + k >= t.last || token + k < t.first;
+        const bool bad = several && (vscale[k >> 2] & byte) == byte;
+        if (bad && !none) nan |= 1u << k;
+        if (bad || none) vscale[k >> 2] &= ~byte;
+      }
+      constexpr int kLanesABlock = kBlock / (D / 16);
+      if (side == 0 && c % kLanesABlock == 0) nans[buffer][half][g][c / kLanesABlock] = nan;
+    }
+    constexpr int kPairs = D / 64;  // words of two elements
+    uint32_t vt[2 * kPairs][4];     // [element][pair of tokens]
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = 2 * i;
+      const float sa = __uint_as_float(byte_scale(vscale[k >> 2], k & 3));
+      const float sb = __uint_as_float(byte_scale(vscale[k >> 2], (k + 1) & 3));
+      // this side's elements in the low bytes
+      const uint32_t wa = vw[k] >> (8 * kPairs * side), wb = vw[k + 1] >> (8 * kPairs * side);
+      uint32_t ea[2], eb[2];
+      ea[0] = codes_to_bf16<0>(wa, sa);
+      eb[0] = codes_to_bf16<0>(wb, sb);
+      if constexpr (kPairs == 2) {
+        ea[1] = codes_to_bf16<1>(wa, sa);
+        eb[1] = codes_to_bf16<1>(wb, sb);
+      }
+#pragma unroll
+      for (int n = 0; n < kPairs; ++n) {
+        vt[2 * n][i] = __builtin_amdgcn_perm(eb[n], ea[n], 0x05040100u);
+        vt[2 * n + 1][i] = __builtin_amdgcn_perm(eb[n], ea[n], 0x07060302u);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < 2 * kPairs; ++n)
+      values[buffer][half][side * 2 * kPairs + n][lane] = u32x4{vt[n][0], vt[n][1], vt[n][2], vt[n][3]};
+  };
+
+  int chunk = t.chunk0;
+  bool chunk_partial = false, lane_ok = false, pages_ok = false;
+  if (chunk < t.chunk1) {
+    load(reader.pages(chunk * kChunk), chunk * kChunk);
+    chunk_partial = partial(chunk * kChunk);
+    lane_ok = ok;
+    pages_ok = all_ok;
+    stage(0, chunk * kChunk);
+    if (chunk + 1 < t.chunk1) load(reader.pages((chunk + 1) * kChunk), (chunk + 1) * kChunk);
+  }
+  Pages ahead = reader.pages((chunk + 2) * kChunk);
+  __syncthreads();
+  for (int buffer = 0; chunk < t.chunk1; ++chunk, buffer ^= 1) {
+    Span at;
+    at.base = chunk * kChunk;
+    at.first = t.first;
+    at.last = t.last;
+    at.window = a.window;
+    at.several = t.query1 != t.query0;
+    at.ok = lane_ok;
+    at.masked = at.base < all_first || at.base + kChunk > all_last || !pages_ok;
+    const bool whole = !chunk_partial;
+    if (at.base < last && at.base + kChunk > first) {  // some row of this wave sees some of it
+      f32x4 s[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[mt][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bf16x8 k = __builtin_bit_cast(bf16x8, keys[buffer][j][i][lane]);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) s[mt][j] = mfma(k, q[mt][i], s[mt][j]);
+        }
+      uint32_t weights[MT][8];
+      soften<D, MT>(r, weights, s, at, a.scale_log2);
+      if (!whole) {
+        const int b = c / (kBlock / (D / 16));
+        mark_nan<D, MT>(r, nans[buffer][0][g][b] | nans[buffer][1][g][b] << 8, at);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          const bf16x8 v = __builtin_bit_cast(bf16x8, values[buffer][h][n][lane]);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            r.acc[mt][n] = mfma(v,
+                                as_bf16x8(weights[mt][4 * h], weights[mt][4 * h + 1],
+                                          weights[mt][4 * h + 2], weights[mt][4 * h + 3]),
+                                r.acc[mt][n]);
+        }
+    }
+    if (chunk + 1 < t.chunk1) {
+      chunk_partial = partial(at.base + kChunk);
+      lane_ok = ok;
+      pages_ok = all_ok;
+      stage(buffer ^ 1, at.base + kChunk);
+      if (chunk + 2 < t.chunk1) {
+        load(ahead, at.base + 2 * kChunk);
+        ahead = reader.pages(at.base + 3 * kChunk);
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    float sum = r.sum[mt];
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    const int row = row0 + mt * kTile + c;
+    if (row >= t.rows) continue;
+    const RowOf at = row_of(a, t.query0, t.head0, row);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint16_t* dst = a.out + static_cast<int64_t>(t.start + at.query) * a.ldo +
+                    (kv_head * a.group + at.head) * D + g * (D / 4);
+    // lane (g, c) has elements g * D / 4 + i * D / 16 + n of row c
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[D / 32];
+#pragma unroll
+      for (int n = 0; n < D / 32; ++n)
+        w[n] = pack_bf16x2(r.acc[mt][2 * n][i] * inv, r.acc[mt][2 * n + 1][i] * inv);
+      if constexpr (D == 128) store16(dst + i * (D / 16), u32x4{w[0], w[1], w[2], w[3]});
+      else *(LORA_GLOBAL u32x2*)(dst + i * (D / 16)) = u32x2{w[0], w[1]};
+    }
+  }
+}
+
+// Joins the parts of tiles that have several.  D / 4 threads side by side take one
+// part's row; a workgroup takes 1 << rows_shift rows and, of each, as many parts at
+// once as it has threads left, then adds those sums up in their order.  A launch of
+// its own: one compute unit draws too little bandwidth to add a long sequence's
+// parts up by itself (131072 tokens, 8 key heads, 32 parts of 8 rows each: 10 us in
+// the last workgroup to arrive, 4 here).
 constexpr int kJoinThreads = 256;
 template <int D>
-__global__ __launch_bounds__(kJoinThreads) void kv_attention_join_kernel(AttentionArgs a) {
-  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
+__global__ __launch_bounds__(kJoinThreads) void kv_attention_join_kernel(AttentionArgs a,
+                                                                         int rows_shift) {
+  constexpr int kLanes = D / 4, kTeams = kJoinThreads / kLanes;
   const int tid = static_cast<int>(threadIdx.x);
-  const int e = (tid % kLanes) * 4, part_group = tid / kLanes;
+  const int e = (tid % kLanes) * 4, team = tid / kLanes;
+  const int teams = kTeams >> rows_shift;  // of a row
+  const int of_row = team & (teams - 1);
   const int kv_head = static_cast<int>(blockIdx.x), seq = static_cast<int>(blockIdx.z);
-  const int tile = static_cast<int>(blockIdx.y) / a.tile_rows;
-  const int row = static_cast<int>(blockIdx.y) - tile * a.tile_rows;
+  // a workgroup's rows are of one tile: tiles have whole powers of two of them
+  const int index = (static_cast<int>(blockIdx.y) << rows_shift) + team / teams;
+  const int tile = index / a.tile_rows;
+  const int row = index - tile * a.tile_rows;
   RowTile t;
-  if (!tile_of(a, seq, tile, t) || row >= t.rows) return;
+  if (!tile_of(a, seq, tile, t)) return;  // the whole workgroup, here and below
   const int active = parts_of(a, t);
   if (active == 1) return;
-  const int64_t slot = static_cast<int64_t>(unit_of(a, seq, tile, kv_head)) * a.parts * a.tile_rows + row;
   float top = kNoScore, total = 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  if (row < t.rows) {
+    const int64_t slot = unit_of(a, seq, tile, kv_head) * a.parts * a.tile_rows + row;
 #pragma unroll 4
-  for (int p = part_group; p < active; p += kGroups) {
-    const int64_t at = slot + static_cast<int64_t>(p) * a.tile_rows;
-    const u32x2 m = load8(a.stats + at * 2);
-    const f32x4 w = __builtin_bit_cast(f32x4, load16(a.partial + at * D + e));
-    const float now = fmaxf(top, __uint_as_float(m[0]));
-    const float fa = __builtin_amdgcn_exp2f(top - now);
-    const float fb = __builtin_amdgcn_exp2f(__uint_as_float(m[0]) - now);
-    top = now;
-    total = total * fa + __uint_as_float(m[1]) * fb;
+    for (int p = of_row; p < active; p += teams) {
+      const int64_t at = slot + static_cast<int64_t>(p) * a.tile_rows;
+      const u32x2 m = load8(a.stats + at * 2);
+      const f32x4 w = __builtin_bit_cast(f32x4, load16(a.partial + at * D + e));
+      const float now = fmaxf(top, __uint_as_float(m[0]));
+      const float fa = __builtin_amdgcn_exp2f(top - now);
+      const float fb = __builtin_amdgcn_exp2f(__uint_as_float(m[0]) - now);
+      top = now;
+      total = total * fa + __uint_as_float(m[1]) * fb;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = o[i] * fa + w[i] * fb;
+      for (int i = 0; i < 4; ++i) o[i] = o[i] * fa + w[i] * fb;
+    }
   }
-  __shared__ f32x4 outs[kGroups][kLanes];
-  __shared__ float tops[kGroups], sums[kGroups];
-  outs[part_group][tid % kLanes] = o;
+  __shared__ f32x4 outs[kTeams][kLanes];
+  __shared__ float tops[kTeams], sums[kTeams];
+  outs[team][tid % kLanes] = o;
   if (e == 0) {
-    tops[part_group] = top;
-    sums[part_group] = total;
+    tops[team] = top;
+    sums[team] = total;
   }
   __syncthreads();
-  if (part_group > 0) return;
+  if (of_row > 0 || row >= t.rows) return;
   top = kNoScore;
-#pragma unroll
-  for (int i = 0; i < kGroups; ++i) top = fmaxf(top, tops[i]);
+  for (int i = team; i < team + teams; ++i) top = fmaxf(top, tops[i]);
   total = 0.f;
   o = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < kGroups; ++i) {
+  for (int i = team; i < team + teams; ++i) {
     const float f = __builtin_amdgcn_exp2f(tops[i] - top);
     total += sums[i] * f;
-    const f32x4 w = outs[i][tid];
+    const f32x4 w = outs[i][tid % kLanes];
 #pragma unroll
     for (int k = 0; k < 4; ++k) o[k] += w[k] * f;
   }
@@ -691,8 +919,8 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attention_join_kernel(Attenti
 
 // How a call is cut up: a function of the sizes alone.
 struct AttentionPlan {
-  int mt;          // row tiles of 16 a wave
-  bool split;      // the waves share out the tokens (see the kernel)
+  bool many;       // many rows a key head: the rows kernel
+  int tile_rows;   // of a workgroup
   int row_tiles, parts, part_chunks;
   int64_t units;   // (sequence, key head, row tile)
   int64_t most_parts;  // no fewer than the parts of any smaller max_len
@@ -702,20 +930,30 @@ static AttentionPlan attention_plan(int num_seqs, int max_query_len, int64_t max
                                     int kv_heads) {
   AttentionPlan p;
   const int64_t rows = static_cast<int64_t>(max_query_len) * (q_heads / kv_heads);
-  p.mt = rows <= 16 ? 1 : (rows <= 32 || rows >= 256 ? 2 : 4);
-  p.split = rows < 256;
-  p.row_tiles = static_cast<int>((rows + kTile * p.mt - 1) / (kTile * p.mt));
+  const int mt = rows <= kTile ? 1 : 2;
+  // Workgroups of the rows kernel; with fewer than fill the device twice over
+  // (their registers), cutting the tokens up as well gains more than sharing the
+  // operands (us, split / rows: 1 sequence of 128 queries of 4096 tokens, 8 key
+  // heads of 8, 64 workgroups 44 / 121; 512 queries, 256: 114 / 124; 2048 of 2048,
+  // 1024: 148 / 101).
+  const int64_t wide = (rows + kRowWaves * kRowTiles * kTile - 1) / (kRowWaves * kRowTiles * kTile);
+  p.many = rows >= kManyRows && wide * num_seqs * kv_heads >= 2 * kCus;
+  p.tile_rows = p.many ? kRowWaves * kRowTiles * kTile : mt * kTile;
+  p.row_tiles = static_cast<int>((rows + p.tile_rows - 1) / p.tile_rows);
   p.units = static_cast<int64_t>(num_seqs) * kv_heads * p.row_tiles;
   p.parts = 1;
   p.most_parts = 1;
   const int64_t chunks = (max_len + kChunk - 1) / kChunk;
   p.part_chunks = static_cast<int>(chunks);
-  if (!p.split) return p;
-  // About a workgroup a CU, which its registers fill; a part is whole rounds of
-  // the waves (131072 tokens, 8 key heads: 256 workgroups 42.6 us, 512 47.1, 1024 55.9).
-  const int waves = waves_of(p.mt, true);
+  if (p.many) return p;
+  // About a workgroup a CU (131072 tokens, 8 key heads, one row tile: 256
+  // workgroups 42.6 us, 512 47.1, 1024 55.9); two where two fit a CU (four waves
+  // each) and a part is still many rounds of them (128 queries of 32768 tokens
+  // 274 -> 216 us).  A part is whole rounds of the waves.
+  const int waves = split_waves(mt);
   const int64_t most = (chunks + waves - 1) / waves;
   p.most_parts = (kCus + p.units - 1) / p.units;
+  if (mt == 2 && most >= 16 * p.most_parts) p.most_parts = (2 * kCus + p.units - 1) / p.units;
   p.most_parts = p.most_parts < most ? p.most_parts : most;
   const int64_t rounds = (most + p.most_parts - 1) / p.most_parts;
   p.part_chunks = static_cast<int>(rounds * waves);
@@ -725,7 +963,7 @@ static AttentionPlan attention_plan(int num_seqs, int max_query_len, int64_t max
 
 // Bytes of the parts' maxima and sums, which lie before their outputs.
 static int64_t stats_bytes(const AttentionPlan& p) {
-  return (p.units * p.most_parts * p.mt * kTile * 8 + 255) / 256 * 256;
+  return (p.units * p.most_parts * p.tile_rows * 8 + 255) / 256 * 256;
 }
 
 int64_t kv_attention_workspace_bytes(int num_seqs, int max_query_len, int max_seq_len, int q_heads,
@@ -733,27 +971,29 @@ int64_t kv_attention_workspace_bytes(int num_seqs, int max_query_len, int max_se
   if (num_seqs < 1) return 0;
   const AttentionPlan p = attention_plan(num_seqs, max_query_len, max_seq_len, q_heads, kv_heads);
   if (p.most_parts <= 1) return 0;
-  return stats_bytes(p) + p.units * p.most_parts * p.mt * kTile * head_dim * 4;
-}
-
-template <int D, int MT, bool kSplit>
-static void launch(const AttentionArgs& a, int num_seqs, hipStream_t stream) {
-  constexpr int kWaves = waves_of(MT, kSplit);
-  const int groups = kSplit ? a.row_tiles * a.parts : (a.row_tiles + kWaves - 1) / kWaves;
-  hipLaunchKernelGGL((kv_attention_kernel<D, MT, kSplit>), dim3(a.cache.kv_heads, groups, num_seqs),
-                     dim3(kWaves * kWave), 0, stream, a);
+  return stats_bytes(p) + p.units * p.most_parts * p.tile_rows * head_dim * 4;
 }
 
 template <int D>
-static void launch_for(const AttentionArgs& a, const AttentionPlan& p, int num_seqs, hipStream_t stream) {
-  if (!p.split) launch<D, 2, false>(a, num_seqs, stream);
-  else if (p.mt == 1) launch<D, 1, true>(a, num_seqs, stream);
-  else if (p.mt == 2) launch<D, 2, true>(a, num_seqs, stream);
-  else launch<D, 4, true>(a, num_seqs, stream);
-  if (p.parts > 1)
+static void launch_for(const AttentionArgs& a, const AttentionPlan& p, int num_seqs,
+                       hipStream_t stream) {
+  const int heads = a.cache.kv_heads;
+  const dim3 grid(heads, p.row_tiles * p.parts, num_seqs);
+  if (p.many)
+    hipLaunchKernelGGL(kv_attention_rows_kernel<D>, grid, dim3(kRowWaves * kWave), 0, stream, a);
+  else if (p.tile_rows == kTile)
+    hipLaunchKernelGGL((kv_attention_kernel<D, 1>), grid, dim3(split_waves(1) * kWave), 0, stream, a);
+  else
+    hipLaunchKernelGGL((kv_attention_kernel<D, 2>), grid, dim3(split_waves(2) * kWave), 0, stream, a);
+  if (p.parts > 1) {
+    // of a workgroup's threads, as many a row as its parts keep busy
+    int shift = 0;
+    while ((kJoinThreads / (D / 4) >> (shift + 1)) >= p.parts) ++shift;
+    const int rows = a.max_query_len * a.group;
     hipLaunchKernelGGL(kv_attention_join_kernel<D>,
-                       dim3(a.cache.kv_heads, a.max_query_len * a.group, num_seqs),
-                       dim3(kJoinThreads), 0, stream, a);
+                       dim3(heads, (rows + (1 << shift) - 1) >> shift, num_seqs),
+                       dim3(kJoinThreads), 0, stream, a, shift);
+  }
 }
 
 hipError_t launch_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* query_start,
@@ -778,7 +1018,7 @@ hipError_t launch_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* qu
                      ldq, ldo, ld_table, num_tokens, max_query_len, max_seq_len, q_heads, window,
                      fabsf(scale) * 1.44269504f, scale < 0.f ? 0x80008000u : 0u,
                      group, ((1 << 21) + group - 1) / group,
-                     p.row_tiles, p.parts, p.part_chunks, kTile * p.mt, nullptr, nullptr};
+                     p.row_tiles, p.parts, p.part_chunks, p.tile_rows, nullptr, nullptr};
   // scores of zero times a hidden token's -infinity must stay -infinity
   if (a.scale_log2 < 1.17549435e-38f) a.scale_log2 = 1.17549435e-38f;
   if (p.parts > 1) {

@@ -90,8 +90,8 @@ def rotate(x: np.ndarray, rope: np.ndarray, positions, interleaved: bool) -> np.
 
 # ---------------------------------------------------------------- attention
 def attention(q, values, query_start, seq_lens, page_table, page, scale, window=0,
-              max_seq_len=None, max_query_len=1 << 30):
-    """(out, slack) for q [tokens, q_heads, d] and cache values [pages, 2, kv_heads,
+              max_seq_len=None, max_query_len=1 << 30, only=None):
+    """(out, slack), of the rows in `only` ([tokens, q_heads], all by default), for q [tokens, q_heads, d] and cache values [pages, 2, kv_heads,
     page, d].  slack bounds how far a kernel may be that keeps scores and sums in
     fp32 and rounds the weights and the result to bf16 (see attention_slack)."""
     T, hq, d = q.shape
@@ -102,7 +102,7 @@ def attention(q, values, query_start, seq_lens, page_table, page, scale, window=
         first, queries = query_start[s], query_start[s + 1] - query_start[s]
         length = max(0, seq_lens[s] if max_seq_len is None else min(seq_lens[s], max_seq_len))
         for i in range(min(queries, max_query_len)):
-            if not 0 <= first + i < T:
+            if not 0 <= first + i < T or (only is not None and not only[first + i].any()):
                 continue
             place = length - queries + i
             low = max(0, place - window + 1) if window else 0
@@ -114,6 +114,8 @@ def attention(q, values, query_start, seq_lens, page_table, page, scale, window=
             seen = np.array(seen)
             held_at = np.asarray(page_table[s])[seen // page]
             for h in range(hq):
+                if only is not None and not only[first + i, h]:
+                    continue
                 k = values[held_at, 0, h // (hq // kv), seen % page]
                 v = values[held_at, 1, h // (hq // kv), seen % page]
                 score = scale * (k @ q[first + i, h])

@@ -99,6 +99,7 @@ ATTENTION = dict(q=FAKE, ldq=512, query_start=FAKE, seq_lens=FAKE, page_table=FA
     (dict(ld_table=3), INVALID), (dict(max_seq_len=65), INVALID), (dict(max_seq_len=0), INVALID),
     (dict(max_seq_len=(1 << 30) + 1, ld_table=1 << 40), INVALID), (dict(max_query_len=0), INVALID),
     (dict(num_seqs=-1), INVALID), (dict(num_seqs=(1 << 16) + 1), INVALID),
+    (dict(num_seqs=1 << 16), INVALID), (dict(max_query_len=(1 << 21) + 1), UNSUPPORTED),
     (dict(num_tokens=-1), INVALID), (dict(q_heads=5), INVALID), (dict(q_heads=1), INVALID),
     (dict(q_heads=1026), INVALID), (dict(scale=float("nan")), INVALID),
     (dict(scale=float("inf")), INVALID), (dict(window=-1), INVALID), (dict(out=None), INVALID),

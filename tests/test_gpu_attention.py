@@ -298,6 +298,8 @@ class Call:
         self.cache = dev(self.data)
         self.dev = [dev(a) for a in (self.start, self.lens, self.table)]
         self.workspace = srg.kv_attention_workspace(len(lens), max(queries), self.table.shape[1] * page, hq, kv, d)
+        if self.workspace is not None:
+            self.workspace.fill_(255)   # NaN in every float
 
     def run(self, stream=None, **more):
         srg.lora_kv_attention(self.q, *self.dev, self.cache, self.out, self.scale, self.workspace,
@@ -315,12 +317,11 @@ class Call:
         assert np.isfinite(got[rows]).all()
         over = np.abs(got[rows] - out[rows]) - slack[rows]
         assert (over <= 0).all(), (over.max(), np.unravel_index(over.argmax(), over.shape))
-        if self.workspace is not None:
-            assert self.counters_clear()
+        assert self.runs_alike()
         return out, slack
 
-    def counters_clear(self):
-        # a second call on the workspace as the first one left it gives the same bits
+    def runs_alike(self):
+        # a second call, on the workspace as the first one left it, gives the same bits
         first = self.out.clone()
         self.run()
         torch.cuda.synchronize()
@@ -357,6 +358,63 @@ def test_kv_attention(case):
     c = Call(len(case[0]) + case[0][0], *case)
     c.run()
     c.check()
+
+
+# Many rows over enough (sequence, key head, 128 rows) that operands are shared by a
+# workgroup: lens, queries, q_heads, kv_heads, head_dim, page, window
+MANY = [
+    ([128, 300, 1, 0, 64, 65, 190, 257] * 2, [128] * 16, 32, 32, 64, 16, 0),
+    ([300, 900, 431, 77], [300, 129, 250, 77], 64, 8, 128, 64, 0),
+    ([300, 900, 431, 77], [300, 129, 250, 90], 64, 8, 128, 16, 100),
+    ([500, 200, 640], [180, 200, 1], 48, 16, 64, 32, 0),
+    ([500, 200, 640], [180, 200, 1], 48, 16, 128, 128, 37),
+]
+
+
+def sample(T, hq, n, seed=0):
+    rng = np.random.default_rng(seed)
+    only = np.zeros((T, hq), dtype=bool)
+    only[rng.integers(0, T, n), rng.integers(0, hq, n)] = True
+    only[[0, -1]] = True
+    return only
+
+
+@pytest.mark.parametrize("case", MANY, ids=[str(i) for i in range(len(MANY))])
+def test_kv_attention_many_rows(case):
+    c = Call(30 + len(case[0]), *case)
+    for s in range(0, len(case[0]), 2):             # and pages that do not exist
+        if c.table.shape[1] > 3:
+            c.table[s, 2] = c.pages + s
+    c.dev[2] = dev(c.table)
+    c.run()
+    only = sample(*c.shape[:2], 1500)
+    out, slack = c.want(only=only)
+    got = R.f64(c.out)
+    assert np.isfinite(got).all()
+    assert (np.abs(got - out) <= slack)[only].all()
+    assert c.runs_alike()
+
+
+@pytest.mark.parametrize("window", [0, 60])
+def test_kv_attention_many_rows_nan_values(window):
+    c = Call(31, [400, 310, 350, 300], [300, 290, 280, 300], 64, 8, 64, 32, window)
+    data, hit = c.data.copy(), np.zeros((*c.shape[:2], 64), dtype=bool)
+    for s, t in ((0, 120), (0, 399), (1, 5), (2, 200), (3, 0)):
+        page, at = c.table[s, t // 32], t % 32
+        data[page, 1, 3, 32 * 32 + (t % 2) * 32 + at] = 255     # head 3, block t % 2
+        queries, length = c.start[s + 1] - c.start[s], c.lens[s]
+        for i in range(queries):
+            place = length - queries + i
+            if t <= place and (not window or t > place - window):
+                hit[c.start[s] + i, 24:32, (t % 2) * 32:(t % 2) * 32 + 32] = True
+    c.cache = dev(data)
+    c.run()
+    got = R.f64(c.out)
+    assert np.array_equal(np.isnan(got), hit)
+    only = sample(*c.shape[:2], 1000, 1)
+    only[:, 24:32] |= sample(c.shape[0], 8, 400, 2)
+    out, slack = c.want(only=only)
+    assert (np.abs(got - out) <= slack)[only[..., None] & ~hit].all()
 
 
 def test_kv_attention_strides_and_rows_of_no_sequence():
