@@ -70,20 +70,9 @@ __device__ __forceinline__ uint32_t byte_scale(uint32_t w, int j) {
   return s & 0x7F800000u;
 }
 
-template <int S>
-__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t w, float scale) {
-  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, S));
-}
-
 __device__ __forceinline__ bf16x8 as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   const u32x4 v = {a, b, c, d};
   return __builtin_bit_cast(bf16x8, v);
-}
-
-// Eight codes of one word: elements in pairs, the A operand of a product of keys.
-__device__ __forceinline__ u32x4 word_to_bf16(uint32_t w, float scale) {
-  return u32x4{codes_to_bf16<0>(w, scale), codes_to_bf16<1>(w, scale), codes_to_bf16<2>(w, scale),
-               codes_to_bf16<3>(w, scale)};
 }
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {

@@ -22,11 +22,13 @@ struct AppendArgs {
   int q_heads, kv_heads;
 };
 
-// Code (0..7) of a magnitude u <= 7 among 0, 0.5, 1, 1.5, 2, 3, 4, 6: the
-// nearest, ties to the even code; larger magnitudes give 6.
-__device__ __forceinline__ uint32_t magnitude_code(float u) {
-  const float c = u < 2.f ? rintf(u * 2.f) : (u < 4.f ? rintf(u) + 2.f : rintf(u * 0.5f) + 4.f);
-  return static_cast<uint32_t>(c > 7.f ? 7.f : c);
+// The codes of v / scale, element 0 in the lowest bits: the nearest of 0, 0.5, 1,
+// 1.5, 2, 3, 4, 6, ties to the even code, and 6 for more (the hardware's rounding).
+__device__ __forceinline__ uint32_t to_codes(const float v[8], float scale) {
+  uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0, v[0], v[1], scale, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], scale, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], scale, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], scale, 3);
 }
 
 // The element of the rotated head at position e + k (k < 8), in fp32.  The
@@ -98,13 +100,7 @@ __global__ __launch_bounds__(kKvThreads) void kv_append_kernel(AppendArgs a) {
     bits = max(bits, static_cast<uint32_t>(__shfl_xor(static_cast<int>(bits), 2)));
     const bool finite = bits < 0x7F800000u;
     const uint32_t sb = finite ? scale_byte(__uint_as_float(bits)) : kScaleNan;
-    uint32_t codes = 0;
-    if (finite) {
-      const float inv = scale_value(2 * kScaleBias - sb);  // 2^-e, a normal number
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        codes |= (magnitude_code(fabsf(v[k] * inv)) | (__float_as_uint(v[k]) >> 31 << 3)) << (4 * k);
-    }
+    const uint32_t codes = finite ? to_codes(v, scale_value(sb)) : 0u;
     const int kv_head = head - a.q_heads - (value ? a.kv_heads : 0);
     const int page = static_cast<int>(slot >> a.cache.page_shift);
     const int at = static_cast<int>(slot & (a.cache.page_size() - 1));
@@ -114,20 +110,6 @@ __global__ __launch_bounds__(kKvThreads) void kv_append_kernel(AppendArgs a) {
       block[a.cache.template scales_at<D>() + ((e / kBlock) << a.cache.page_shift) + at] =
           static_cast<uint8_t>(sb);
   }
-}
-
-// Elements 2j and 2j + 1 of eight codes, times a block's scale, as bf16: exact.
-__device__ __forceinline__ uint32_t decode_pair(uint32_t codes, int j, float scale) {
-  float v[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const uint32_t c = (codes >> (8 * j + 4 * k)) & 15u;
-    const uint32_t m = c & 7u;
-    // 0, 0.5, 1, 1.5, 2, 3, 4, 6
-    const float u = m < 4 ? 0.5f * m : (m < 6 ? 2.f + (m - 4.f) : 4.f + 2.f * (m - 6.f));
-    v[k] = (c & 8u ? -u : u) * scale;
-  }
-  return pack_bf16x2(v[0], v[1]);
 }
 
 template <int D>
@@ -155,9 +137,7 @@ __global__ __launch_bounds__(kKvThreads) void kv_read_kernel(const int64_t* slot
       const uint32_t codes = *(const LORA_GLOBAL uint32_t*)(block + at * (D / 2) + e / 2);
       const uint32_t sb =
           block[cache.template scales_at<D>() + ((e / kBlock) << cache.page_shift) + at];
-      const float scale = sb == kScaleNan ? __uint_as_float(0x7FC00000u) : scale_value(sb);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = decode_pair(codes, k, scale);
+      o = word_to_bf16(codes, scale_value(sb));
     }
     store16(out + token * (part ? ldv : ldk) + kv_head * D + e, o);
   }

@@ -36,7 +36,8 @@ struct Cache {
   __device__ __forceinline__ int scales_at() const { return (D / 2) << page_shift; }
 };
 
-// 2^(b - 127) for b in [1, 254], from its bits; b = 255 gives infinity, 0 gives 0.
+// A scale byte as the scale operand of the conversions below, which take its
+// exponent: 2^(b - 127), and NaN for b = 255 (an infinity here).
 __device__ __forceinline__ float scale_value(uint32_t b) { return __uint_as_float(b << 23); }
 
 // Scale byte of a block whose largest magnitude is `largest` (fp32, not NaN or
@@ -48,6 +49,19 @@ __device__ __forceinline__ uint32_t scale_byte(float largest) {
   int e = static_cast<int>(bits >> 23) - kScaleBias - 2 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   e = e < kMinExponent ? kMinExponent : (e > kMaxExponent ? kMaxExponent : e);
   return static_cast<uint32_t>(e + kScaleBias);
+}
+
+// Codes 2 S and 2 S + 1 of a word times a scale, as two bf16: exact (one
+// significant bit after the first, times a power of two).
+template <int S>
+__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t w, float scale) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, S));
+}
+
+// All eight of them.
+__device__ __forceinline__ u32x4 word_to_bf16(uint32_t w, float scale) {
+  return u32x4{codes_to_bf16<0>(w, scale), codes_to_bf16<1>(w, scale), codes_to_bf16<2>(w, scale),
+               codes_to_bf16<3>(w, scale)};
 }
 
 }  // namespace lora

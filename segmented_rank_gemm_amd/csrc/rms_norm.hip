@@ -5,17 +5,18 @@
 //   s = max(fp32(max|v| / 448), 2^-126), y8 = e4m3(v / s)
 //
 // The row stays in registers between the sum and the outputs, so each input is
-// read once.  v is kept in 64 bits up to its one rounding to bf16 or (through
-// fp32) to 8 bits: next to a border between two codes the result is then that
-// of the formula.
+// read once.  Up to its one rounding to bf16 or 8 bits (through fp32) v carries
+// about 48 bits: next to a border between two codes the result is then that of the
+// formula.  h w is exact in fp32 (8 by 8 significant bits); it is multiplied by a
+// factor held as the sum of two fp32 numbers, which costs four operations where
+// 64-bit arithmetic takes a multiplication and two conversions at a quarter of
+// the rate.  Only the sum of squares is in 64 bits.
 
 #include "device_common.hpp"
 #include "lora_attention.h"
 
 namespace lora {
 
-constexpr int kNormThreads = 256;
-constexpr int kNormWaves = kNormThreads / kWave;
 constexpr double kE4m3Max = 448.0;
 constexpr float kMinScale = 1.17549435e-38f;  // 2^-126
 
@@ -31,109 +32,256 @@ struct NormArgs {
   double eps;
   int hidden;
   int group;        // elements a scale; hidden: one a row
+  int group_shift;  // log2 of the chunks of 8 a group, where there are several groups
 };
 
 // Larger of two magnitudes; NaN if either is.
 __device__ __forceinline__ double max_nan(double a, double b) { return a > b || a != a ? a : b; }
 
-// C: chunks of 8 elements a thread.
-template <int C>
-__global__ __launch_bounds__(kNormThreads) void rms_norm_kernel(NormArgs a) {
-  const int64_t row = blockIdx.x;
-  const int tid = static_cast<int>(threadIdx.x);
-  const int chunks = a.hidden >> 3;
-  const bool per_row = a.group == a.hidden;
+// A factor as the sum of two fp32 numbers, and a product with it to about 48
+// bits, rounded to fp32.  Holds while neither part nor the product leaves fp32's
+// normal range: for factors in [2^-60, 2^60].
+struct Factor {
+  float high, low;
+};
+__device__ __forceinline__ Factor factor(double f) {
+  const float high = static_cast<float>(f);
+  return Factor{high, static_cast<float>(f - static_cast<double>(high))};
+}
+__device__ __forceinline__ float times(float p, Factor f) {
+  const float high = p * f.high;
+  return high + fmaf(p, f.low, fmaf(p, f.high, -high));
+}
+
+// Largest of the magnitudes' bits over 1 << shift (2 to 5) neighbouring lanes, on
+// data-parallel moves inside 16 lanes.  All lanes of the wave take part.
+template <int kCtrl>
+__device__ __forceinline__ uint32_t max_with(uint32_t v) {
+  const int other = __builtin_amdgcn_update_dpp(0, static_cast<int>(v), kCtrl, 0xF, 0xF, false);
+  return max(v, static_cast<uint32_t>(other));
+}
+__device__ __forceinline__ uint32_t group_max(uint32_t v, int shift) {
+  v = max_with<0xB1>(v);                   // the other of each two lanes
+  v = max_with<0x4E>(v);                   // the other two of each four
+  if (shift > 2) v = max_with<0x141>(v);   // eight, mirrored
+  if (shift > 3) v = max_with<0x140>(v);   // sixteen, mirrored
+  if (shift > 4) v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), 16)));
+  return v;
+}
+
+// 1 / s for a normal fp32 number s in [2^-126, 2^125], to about 45 bits.
+__device__ __forceinline__ double inverse(float s) {
+  const double x = __builtin_amdgcn_rcpf(s);
+  return fma(x, fma(-x, s, 1.0), x);
+}
+
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+  int q = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  q = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, q, true);
+  return static_cast<uint32_t>(q);
+}
+
+// A thread's part of a row: C chunks of 8 elements, T (threads of the row) apart.
+template <int T, int C>
+struct NormRow {
   u32x4 h[C];
-  double sum = 0.0, top = 0.0;
+  int chunks;     // of the row
+  bool per_row;   // one scale
+  double r;       // 1 / sqrt(mean h^2 + eps)
+
+  __device__ __forceinline__ static int at(int c) {
+    return c * T + static_cast<int>(threadIdx.x);
+  }
+  // No lane of this wave has a chunk c.
+  __device__ __forceinline__ bool past(int c) const { return at(c) - lane_id() >= chunks; }
+};
+
+// The outputs where h w and its factors stay well inside fp32's range; top: the
+// largest |h w| of the row.
+template <int T, int C>
+__device__ __forceinline__ void emit(const NormArgs& a, const NormRow<T, C>& n, int64_t row, double top) {
+  const Factor to_v = factor(n.r);
+  const double per_scale = n.r / kE4m3Max;
+  float s = static_cast<float>(top * per_scale);
+  s = s < kMinScale ? kMinScale : s;
+  double code = n.r * inverse(s);  // what turns h w into the number that is coded
+  if (a.y8 && n.per_row && threadIdx.x == 0) a.scales[row] = s;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int i = c * kNormThreads + tid;
-    if (i >= chunks) continue;
-    h[c] = load16(a.x + row * a.ldx + 8 * i);
-    if (a.residual) {
-      const u32x4 r = load16(a.residual + row * a.ldr + 8 * i);
+    if (n.past(c)) break;
+    const int i = n.at(c);
+    const bool in = i < n.chunks;
+    u32x4 w = {0, 0, 0, 0};
+    if (in) w = load16(a.weight + 8 * i);
+    float p[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        h[c][k] = pack_bf16x2(bf16_lo(h[c][k]) + bf16_lo(r[k]), bf16_hi(h[c][k]) + bf16_hi(r[k]));
-      if (a.sum) store16(a.sum + row * a.lds + 8 * i, h[c]);
+    for (int k = 0; k < 8; ++k) p[k] = in ? bf16_at(n.h[c], k) * bf16_at(w, k) : 0.f;
+    if (a.y && in) {
+      u32x4 o;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = pack_bf16x2(times(p[2 * k], to_v), times(p[2 * k + 1], to_v));
+      store16(a.y + row * a.ldy + 8 * i, o);
     }
+    if (!a.y8) continue;
+    if (!n.per_row) {
+      // a group is 4 to 32 neighbouring lanes, all inside the row or none
+      uint32_t bits = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) bits = max(bits, __float_as_uint(p[k]) & 0x7FFFFFFFu);
+      bits = group_max(bits, a.group_shift);
+      s = static_cast<float>(__uint_as_float(bits) * per_scale);
+      s = s < kMinScale ? kMinScale : s;
+      code = n.r * inverse(s);
+      if (in && (i & ((1 << a.group_shift) - 1)) == 0)
+        a.scales[row * (n.chunks >> a.group_shift) + (i >> a.group_shift)] = s;
+    }
+    if (!in) continue;
+    float u[8];
+    if (code >= 0x1p-60 && code <= 0x1p60) {
+      const Factor f = factor(code);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) u[k] = times(p[k], f);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) u[k] = static_cast<float>(p[k] * code);
+    }
+    *(LORA_GLOBAL u32x2*)(a.y8 + row * a.ldy8 + 8 * i) =
+        u32x2{pack_e4m3x4(u[0], u[1], u[2], u[3]), pack_e4m3x4(u[4], u[5], u[6], u[7])};
+  }
+}
+
+// The outputs of any other row (very large or very small ones, infinities, NaN):
+// everything in 64 bits, nothing for speed.  shared: (T / kWave) numbers that all
+// threads are done with.
+template <int T, int C>
+__device__ __forceinline__ void emit_wide(const NormArgs& a, const NormRow<T, C>& n, int64_t row,
+                                       double* shared) {
+  auto v = [&](u32x4 h, u32x4 w, int k) {
+    return static_cast<double>(bf16_at(h, k)) * bf16_at(w, k) * n.r;
+  };
+  auto largest = [&](int c) {
+    double big = 0.0;
+    const int i = n.at(c);
+    if (i < n.chunks) {
+      const u32x4 w = load16(a.weight + 8 * i);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) big = max_nan(fabs(v(n.h[c], w, k)), big);
+    }
+    return big;
+  };
+  double row_top = 0.0;
+  if (n.per_row) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) row_top = max_nan(largest(c), row_top);
+    for (int m = 1; m < kWave; m <<= 1) row_top = max_nan(__shfl_xor(row_top, m), row_top);
+    if (lane_id() == 0) shared[threadIdx.x / kWave] = row_top;
+    __syncthreads();
+    row_top = 0.0;
+    for (int i = 0; i < (T / kWave); ++i) row_top = max_nan(shared[i], row_top);
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int i = n.at(c);
+    const bool in = i < n.chunks;
+    double top = row_top;
+    if (!n.per_row) {
+      top = largest(c);
+      for (int m = 1; m < 1 << a.group_shift; m <<= 1) top = max_nan(__shfl_xor(top, m), top);
+    }
+    if (!in) continue;
+    float s = static_cast<float>(top / kE4m3Max);
+    s = s < kMinScale ? kMinScale : s;
     const u32x4 w = load16(a.weight + 8 * i);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const double e = bf16_at(h[c], k);
-      sum += e * e;
-      top = max_nan(fabs(e * bf16_at(w, k)), top);
+      const double e = v(n.h[c], w, k);
+      const float u = static_cast<float>(e / s);
+      if (a.y)
+        a.y[row * a.ldy + 8 * i + k] = static_cast<uint16_t>(pack_bf16x2(static_cast<float>(e), 0.f));
+      if (a.y8) a.y8[row * a.ldy8 + 8 * i + k] = static_cast<uint8_t>(pack_e4m3x4(u, u, u, u));
+    }
+    if (!a.y8) continue;
+    if (n.per_row ? i == 0 : (i & ((1 << a.group_shift) - 1)) == 0)
+      a.scales[n.per_row ? row : row * (n.chunks >> a.group_shift) + (i >> a.group_shift)] = s;
+  }
+}
+
+template <int T, int C>
+__global__ __launch_bounds__(T) void rms_norm_kernel(NormArgs a) {
+  const int64_t row = blockIdx.x;
+  const int tid = static_cast<int>(threadIdx.x);
+  NormRow<T, C> n;
+  n.chunks = a.hidden >> 3;
+  n.per_row = a.group == a.hidden;
+  // All of the row's loads go out before the first is waited for.
+  u32x4 res[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int i = n.at(c);
+    n.h[c] = u32x4{0, 0, 0, 0};
+    res[c] = u32x4{0, 0, 0, 0};
+    if (i >= n.chunks) continue;
+    n.h[c] = load16(a.x + row * a.ldx + 8 * i);
+    if (a.residual) res[c] = load16(a.residual + row * a.ldr + 8 * i);
+  }
+  double sum = 0.0;
+  uint32_t top_bits = 0;  // of the largest |h w|: integer order, infinity and NaN on top
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int i = n.at(c);
+    if (i >= n.chunks) continue;
+    const u32x4 w = load16(a.weight + 8 * i);
+    if (a.residual) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        n.h[c][k] = pack_bf16x2(bf16_lo(n.h[c][k]) + bf16_lo(res[c][k]),
+                                bf16_hi(n.h[c][k]) + bf16_hi(res[c][k]));
+      if (a.sum) store16(a.sum + row * a.lds + 8 * i, n.h[c]);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float e = bf16_at(n.h[c], k);
+      const double e64 = e;
+      sum = fma(e64, e64, sum);
+      top_bits = max(top_bits, __float_as_uint(e * bf16_at(w, k)) & 0x7FFFFFFFu);
     }
   }
-  __shared__ double part_sum[kNormWaves], part_top[kNormWaves];
+  __shared__ double part_sum[(T / kWave)];
+  __shared__ uint32_t part_top[(T / kWave)];
+  __shared__ double spare[(T / kWave)];
 #pragma unroll
   for (int m = 1; m < kWave; m <<= 1) {
     sum += __shfl_xor(sum, m);
-    top = max_nan(__shfl_xor(top, m), top);
+    top_bits = max(top_bits, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top_bits), m)));
   }
   if (lane_id() == 0) {
     part_sum[tid / kWave] = sum;
-    part_top[tid / kWave] = top;
+    part_top[tid / kWave] = top_bits;
   }
   __syncthreads();
   sum = 0.0;
-  top = 0.0;
+  top_bits = 0;
 #pragma unroll
-  for (int i = 0; i < kNormWaves; ++i) {
+  for (int i = 0; i < (T / kWave); ++i) {
     sum += part_sum[i];
-    top = max_nan(part_top[i], top);
+    top_bits = max(top_bits, part_top[i]);
   }
-  const double r = 1.0 / sqrt(sum / a.hidden + a.eps);
   if (!a.y && !a.y8) return;
+  n.r = 1.0 / sqrt(sum / a.hidden + a.eps);
+  // the same for all threads of the row
+  if (top_bits < 0x7F800000u && n.r >= 0x1p-60 && n.r <= 0x1p10)
+    emit<T, C>(a, n, row, __uint_as_float(top_bits));
+  else
+    emit_wide<T, C>(a, n, row, spare);
+}
 
-  float scale = static_cast<float>(top * r / kE4m3Max);
-  scale = scale < kMinScale ? kMinScale : scale;
-  if (a.y8 && per_row && tid == 0) a.scales[row] = scale;
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int i = c * kNormThreads + tid;
-    const bool in = i < chunks;
-    double v[8];
-    double big = 0.0;
-    if (in) {
-      const u32x4 w = load16(a.weight + 8 * i);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        v[k] = static_cast<double>(bf16_at(h[c], k)) * bf16_at(w, k) * r;
-        big = max_nan(fabs(v[k]), big);
-      }
-      if (a.y) {
-        u32x4 o;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          o[k] = pack_bf16x2(static_cast<float>(v[2 * k]), static_cast<float>(v[2 * k + 1]));
-        store16(a.y + row * a.ldy + 8 * i, o);
-      }
-    }
-    if (!a.y8) continue;
-    float s = scale;
-    if (!per_row) {
-      // a group is group / 8 neighbouring lanes (4 to 32), all inside the row or none
-      for (int m = 1; m < (a.group >> 3); m <<= 1) big = max_nan(__shfl_xor(big, m), big);
-      s = static_cast<float>(big / kE4m3Max);
-      s = s < kMinScale ? kMinScale : s;
-      if (in && (8 * i) % a.group == 0)
-        a.scales[row * (a.hidden / a.group) + 8 * i / a.group] = s;
-    }
-    if (in) {
-      const double inv = 1.0 / static_cast<double>(s);
-      u32x2 o;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        int p = __builtin_amdgcn_cvt_pk_fp8_f32(static_cast<float>(v[4 * k] * inv),
-                                                static_cast<float>(v[4 * k + 1] * inv), 0, false);
-        p = __builtin_amdgcn_cvt_pk_fp8_f32(static_cast<float>(v[4 * k + 2] * inv),
-                                            static_cast<float>(v[4 * k + 3] * inv), p, true);
-        o[k] = static_cast<uint32_t>(p);
-      }
-      *(LORA_GLOBAL u32x2*)(a.y8 + row * a.ldy8 + 8 * i) = o;
-    }
-  }
+template <int T>
+static void launch(const NormArgs& a, int chunks, int rows, hipStream_t stream) {
+  const dim3 grid(rows), block(T);
+  if (chunks <= 1) hipLaunchKernelGGL((rms_norm_kernel<T, 1>), grid, block, 0, stream, a);
+  else if (chunks <= 2) hipLaunchKernelGGL((rms_norm_kernel<T, 2>), grid, block, 0, stream, a);
+  else if (chunks <= 4) hipLaunchKernelGGL((rms_norm_kernel<T, 4>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((rms_norm_kernel<T, 8>), grid, block, 0, stream, a);
 }
 
 hipError_t launch_rms_norm(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr,
@@ -141,15 +289,16 @@ hipError_t launch_rms_norm(const uint16_t* x, int64_t ldx, const uint16_t* resid
                            uint16_t* sum, int64_t lds, uint16_t* y, int64_t ldy, uint8_t* y8,
                            int64_t ldy8, float* scales, int group, hipStream_t stream) {
   const NormArgs a = {x, residual, weight, sum, y, y8, scales, ldx, ldr, lds, ldy, ldy8,
-                      eps, hidden, group};
-  const int need = (hidden / 8 + kNormThreads - 1) / kNormThreads;
-  const dim3 grid(num_tokens), block(kNormThreads);
-  if (need <= 1) rms_norm_kernel<1><<<grid, block, 0, stream>>>(a);
-  else if (need <= 2) rms_norm_kernel<2><<<grid, block, 0, stream>>>(a);
-  else if (need <= 4) rms_norm_kernel<4><<<grid, block, 0, stream>>>(a);
-  else if (need <= 8) rms_norm_kernel<8><<<grid, block, 0, stream>>>(a);
-  else if (need <= 16) rms_norm_kernel<16><<<grid, block, 0, stream>>>(a);
-  else rms_norm_kernel<32><<<grid, block, 0, stream>>>(a);
+                      eps, hidden, group, group < hidden ? __builtin_ctz(group / 8) : 0};
+  const int chunks = hidden / 8;
+  // Threads a row: enough that a thread has few chunks, and no more, since idle
+  // waves cost their launch (us, 64 / 256 / 512 / 1024 threads: 8192 rows of 512
+  // 10.9 / 16.7 / 27.3 / 52.9; 2048 of 4096 - / 15.9 / 16.9 / 21.5; 16 of 8192
+  // - / 6.5 / 5.1 / 5.2; 8192 of 8192 - / 116 / 111 / 117).
+  if (hidden <= 1024) launch<64>(a, (chunks + 63) / 64, num_tokens, stream);
+  else if (hidden <= 4096) launch<256>(a, (chunks + 255) / 256, num_tokens, stream);
+  else if (hidden <= 32768) launch<512>(a, (chunks + 511) / 512, num_tokens, stream);
+  else launch<1024>(a, (chunks + 1023) / 1024, num_tokens, stream);
   return hipGetLastError();
 }
 

@@ -106,9 +106,10 @@ def test_rms_norm_in_place(hidden):
     check_norm(x0, w, r0, 1e-5, hidden, x, y, None, None)
 
 
-@pytest.mark.parametrize("group", [512, 32])
-def test_rms_norm_of_special_rows(group):
-    x, w, _ = norm_case(np.random.default_rng(6), 8, 512, False)
+@pytest.mark.parametrize("hidden,group", [(512, 512), (512, 32), (2304, 2304), (2304, 256), (12288, 12288),
+                                          (12288, 64)])
+def test_rms_norm_of_special_rows(hidden, group):
+    x, w, _ = norm_case(np.random.default_rng(6), 8, hidden, False)
     x[0] = 0                      # nothing: scales of 2^-126, zeros
     x[1, 77] = float("inf")       # its own v NaN, the others 0
     x[2, 5] = float("nan")        # all NaN
@@ -117,8 +118,8 @@ def test_rms_norm_of_special_rows(group):
     w[9] = 0
     x[5, 100] = -float("inf")
     x[6] *= 1e-30
-    y, y8 = torch.empty_like(x), torch.empty(8, 512, dtype=torch.float8_e4m3fn, device="cuda")
-    scales = torch.empty(8, 512 // group, device="cuda")
+    y, y8 = torch.empty_like(x), torch.empty(8, hidden, dtype=torch.float8_e4m3fn, device="cuda")
+    scales = torch.empty(8, hidden // group, device="cuda")
     for eps in (1e-5, 0.0):
         y.fill_(1), y8.fill_(1), scales.fill_(1)
         srg.lora_rms_norm(x[0 if eps else 1:], w, eps, y=y[0 if eps else 1:], y8=y8[0 if eps else 1:],
