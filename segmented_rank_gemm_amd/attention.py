@@ -46,9 +46,12 @@ def _declare(L: ctypes.CDLL) -> None:
     L.lora_kv_attention.restype = ctypes.c_int
 
 
-from . import (_check, _dev_ptr, _flat_dev_bytes, _stream_handle, lib)  # noqa: E402
+from . import LoraError, _dev_ptr, _flat_dev_bytes, _stream_handle, lib  # noqa: E402
 
 _declare(lib())
+# the entry points themselves: looking them up costs as much as a check
+_rms_norm, _kv_append = lib().lora_rms_norm, lib().lora_kv_append
+_kv_read, _kv_attention = lib().lora_kv_read, lib().lora_kv_attention
 
 
 # The checks below run on every call, and a decode step's calls are as short as
@@ -155,9 +158,11 @@ def lora_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float,
         if groups < 1 or hidden % groups or ld != groups:
             raise ValueError(f"scales must be contiguous, a whole number of them a row of {hidden}")
         group = hidden // groups
-    _check("lora_rms_norm", lib().lora_rms_norm(
+    status = _rms_norm(
         px, ldx, pr, ldr, _vector(weight, _BF16, hidden, "weight"), eps, T, hidden, po, ldo, py, ldy,
-        p8, ld8, ps, group, _stream_handle(stream)))
+        p8, ld8, ps, group, _stream_handle(stream))
+    if status:
+        raise LoraError("lora_rms_norm", status)
 
 
 def lora_kv_append(qkv: torch.Tensor, positions: Optional[torch.Tensor], slots: torch.Tensor,
@@ -178,9 +183,11 @@ def lora_kv_append(qkv: torch.Tensor, positions: Optional[torch.Tensor], slots: 
         if ld != rot:
             raise ValueError("rope must be contiguous")
         pp = _vector(positions, _I32T, T, "positions")
-    _check("lora_kv_append", lib().lora_kv_append(
+    status = _kv_append(
         px, ldx, pp, _vector(slots, _I64T, T, "slots"), pr, rows, rot, 1 if interleaved else 0, T,
-        q_heads, kv_heads, head_dim, pq, ldq, pc, pages, page_size, _stream_handle(stream)))
+        q_heads, kv_heads, head_dim, pq, ldq, pc, pages, page_size, _stream_handle(stream))
+    if status:
+        raise LoraError("lora_kv_append", status)
 
 
 def lora_kv_read(slots: torch.Tensor, cache: torch.Tensor, k_out: Optional[torch.Tensor],
@@ -197,9 +204,11 @@ def lora_kv_read(slots: torch.Tensor, cache: torch.Tensor, k_out: Optional[torch
         pk, ldk = _heads(k_out, T, kv_heads, head_dim, "k_out")
     if v_out is not None:
         pv, ldv = _heads(v_out, T, kv_heads, head_dim, "v_out")
-    _check("lora_kv_read", lib().lora_kv_read(
+    status = _kv_read(
         _vector(slots, _I64T, T, "slots"), T, kv_heads, head_dim, pc, pages, page_size, pk, ldk, pv,
-        ldv, _stream_handle(stream)))
+        ldv, _stream_handle(stream))
+    if status:
+        raise LoraError("lora_kv_read", status)
 
 
 def lora_kv_attention_workspace_bytes(num_seqs: int, max_query_len: int, max_seq_len: int,
@@ -238,8 +247,10 @@ def lora_kv_attention(q: torch.Tensor, query_start: torch.Tensor, seq_lens: torc
         raise ValueError(f"max_seq_len {max_seq_len} is not within the page table's "
                          f"{per_seq * page_size} tokens")
     wptr, wbytes = (0, 0) if workspace is None else _flat_dev_bytes(workspace, "workspace")
-    _check("lora_kv_attention", lib().lora_kv_attention(
+    status = _kv_attention(
         pq, ldq, _vector(query_start, _I32T, B + 1, "query_start"),
         _vector(seq_lens, _I32T, B, "seq_lens"), pt, ldt, pc, pages, page_size, T, B, max_query_len,
         max_seq_len, q_heads, kv_heads, head_dim, scale, window, po, ldo, wptr, wbytes,
-        _stream_handle(stream)))
+        _stream_handle(stream))
+    if status:
+        raise LoraError("lora_kv_attention", status)

@@ -5,8 +5,8 @@
 //   s = max(fp32(max|v| / 448), 2^-126), y8 = e4m3(v / s)
 //
 // The row stays in registers between the sum and the outputs, so each input is
-// read once.  Up to its one rounding to bf16 or 8 bits (through fp32) v carries
-// about 48 bits: next to a border between two codes the result is then that of the
+// read once.  Up to its one rounding to bf16 (through fp32) or 8 bits v carries
+// about 46 bits: next to a border between two codes the result is then that of the
 // formula.  h w is exact in fp32 (8 by 8 significant bits); it is multiplied by a
 // factor held as the sum of two fp32 numbers, which costs four operations where
 // 64-bit arithmetic takes a multiplication and two conversions at a quarter of
@@ -38,9 +38,9 @@ struct NormArgs {
 // Larger of two magnitudes; NaN if either is.
 __device__ __forceinline__ double max_nan(double a, double b) { return a > b || a != a ? a : b; }
 
-// A factor as the sum of two fp32 numbers, and a product with it to about 48
-// bits, rounded to fp32.  Holds while neither part nor the product leaves fp32's
-// normal range: for factors in [2^-60, 2^60].
+// A factor as the sum of two fp32 numbers, and a product with it to about 46
+// bits.  Holds while neither part nor the product leaves fp32's normal range: for
+// factors in [2^-60, 2^60].
 struct Factor {
   float high, low;
 };
@@ -48,9 +48,36 @@ __device__ __forceinline__ Factor factor(double f) {
   const float high = static_cast<float>(f);
   return Factor{high, static_cast<float>(f - static_cast<double>(high))};
 }
+// The product rounded to fp32.
 __device__ __forceinline__ float times(float p, Factor f) {
+#pragma clang fp contract(off)  // `high` has to be the same rounded number in all three places
   const float high = p * f.high;
   return high + fmaf(p, f.low, fmaf(p, f.high, -high));
+}
+
+// A number `high + low` (|low| at most half a step of high) as the fp32 number that
+// rounds to 8 bits as the sum does: of the two neighbours, where it is neither, the
+// odd one.  The nearest one will not do: h w and the row's largest are numbers of
+// few bits, so their quotients lie on borders between codes (within 2^-24, the
+// rounding of the scale) thousands of times as often as by chance, and a first
+// rounding onto the border would send them to the even side.
+__device__ __forceinline__ float odd(float high, float low) {
+  const uint32_t bits = __float_as_uint(high);
+  const bool away = (__float_as_uint(low) ^ bits) >> 31 == 0;  // low points away from zero
+  const uint32_t moved = away ? bits + 1 : bits - 1;
+  return __uint_as_float(low != 0.f && (bits & 1) == 0 ? moved : bits);
+}
+__device__ __forceinline__ float times_odd(float p, Factor f) {
+#pragma clang fp contract(off)
+  const float first = p * f.high;
+  const float rest = fmaf(p, f.low, fmaf(p, f.high, -first));
+  const float high = first + rest;
+  return odd(high, rest - (high - first));
+}
+__device__ __forceinline__ float to_odd(double v) {
+  const float high = static_cast<float>(v);
+  // past fp32, infinite or NaN there is no rest
+  return fabsf(high) < INFINITY ? odd(high, static_cast<float>(v - high)) : high;
 }
 
 // Largest of the magnitudes' bits over 1 << shift (2 to 5) neighbouring lanes, on
@@ -140,10 +167,10 @@ __device__ __forceinline__ void emit(const NormArgs& a, const NormRow<T, C>& n, 
     if (code >= 0x1p-60 && code <= 0x1p60) {
       const Factor f = factor(code);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] = times(p[k], f);
+      for (int k = 0; k < 8; ++k) u[k] = times_odd(p[k], f);
     } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] = static_cast<float>(p[k] * code);
+      for (int k = 0; k < 8; ++k) u[k] = to_odd(p[k] * code);
     }
     *(LORA_GLOBAL u32x2*)(a.y8 + row * a.ldy8 + 8 * i) =
         u32x2{pack_e4m3x4(u[0], u[1], u[2], u[3]), pack_e4m3x4(u[4], u[5], u[6], u[7])};
@@ -195,7 +222,7 @@ __device__ __forceinline__ void emit_wide(const NormArgs& a, const NormRow<T, C>
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const double e = v(n.h[c], w, k);
-      const float u = static_cast<float>(e / s);
+      const float u = to_odd(e / s);
       if (a.y)
         a.y[row * a.ldy + 8 * i + k] = static_cast<uint16_t>(pack_bf16x2(static_cast<float>(e), 0.f));
       if (a.y8) a.y8[row * a.ldy8 + 8 * i + k] = static_cast<uint8_t>(pack_e4m3x4(u, u, u, u));

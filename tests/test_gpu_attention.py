@@ -72,6 +72,36 @@ def test_rms_norm(T, hidden, residual, group):
     check_norm(x, w, r, 1e-5, group, sums, y, y8, scales)
 
 
+def nearest_e4m3(u):
+    """(values, how far each u is from a border between two, relative to u)."""
+    levels = torch.arange(0, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    middles = (levels[1:] + levels[:-1]) / 2
+    a = np.abs(u)
+    code = np.searchsorted(middles, a)
+    near = np.minimum(np.abs(a - middles[np.minimum(code, 125)]), np.abs(a - middles[np.maximum(code - 1, 0)]))
+    return np.copysign(levels[code], u), near / np.maximum(a, 1e-300)
+
+
+@pytest.mark.parametrize("hidden,group", [(512, 512), (4096, 4096), (11008, 128)])
+def test_rms_norm_codes_are_those_of_the_formula(hidden, group):
+    """v is kept to 2^-40 and more up to its rounding: away from a border by more
+    than the 2^-24 of the fp32 number in between, each code is the nearest one."""
+    x, w, r = norm_case(np.random.default_rng(7), 256, hidden, True)
+    y = torch.empty_like(x)
+    y8, scales = torch.empty(256, hidden, dtype=torch.float8_e4m3fn, device="cuda"), \
+        torch.empty(256, hidden // group, device="cuda")
+    srg.lora_rms_norm(x, w, 1e-5, residual=r, y=y, y8=y8, scales=scales)
+    _, v, s = R.rms_norm(x, r, w, 1e-5, group)
+    assert (R.f64(scales) == s).all()
+    want, near = nearest_e4m3((v.reshape(256, -1, group) / s[..., None]).reshape(256, hidden))
+    wrong = (R.f64(y8) != want) & (near > 2.0 ** -40)
+    # an fp32 number in between may round to a border itself: a share of 2^-24 / 2^-4 of
+    # them comes that near, and half of those then go to the wrong side
+    assert wrong.sum() == (wrong & (near < 2.0 ** -24)).sum() and wrong.mean() <= 2.0 ** -20
+    bits = torch.from_numpy(v).float().bfloat16()
+    assert (bits == y.cpu()).double().mean() >= 1 - 2.0 ** -30
+
+
 @pytest.mark.parametrize("which", ["y", "y8", "sum", "y+y8 without sum"])
 def test_rms_norm_outputs_may_be_left_out(which):
     x, w, r = norm_case(np.random.default_rng(3), 5, 520, True)
