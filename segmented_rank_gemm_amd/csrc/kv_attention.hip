@@ -106,9 +106,9 @@ struct Reader {
   int shift, num_pages, max_seq_len;
 
   __device__ __forceinline__ int page_at(int token) const {
-    if (token >= max_seq_len) return -1;
-    const int p = table[token >> shift];
-    return p >= 0 && p < num_pages ? p : -1;
+    const bool there = token < max_seq_len;
+    const int p = table[(there ? token : max_seq_len - 1) >> shift];
+    return there && p >= 0 && p < num_pages ? p : -1;
   }
   __device__ __forceinline__ Pages pages(int base) const {
     const int lane = lane_id();
@@ -509,13 +509,19 @@ __global__ __launch_bounds__(split_waves(MT) * kWave, 2) void kv_attention_kerne
 
   // The queries as B operands, for all waves.
   __shared__ u32x4 q[MT * (D / 32)][kWave];
+  // Loads are never behind a condition inside the loop: the wait before a use
+  // counts the loads after it, and where paths with and without some meet, it
+  // waits for those too.  The last step loads its own chunk once more instead.
   Keys<D> keys;
   Values values;
+  const auto next_of = [&](int at) { return at + kWaves < stop ? at + kWaves : at; };
+  int next = next_of(chunk);
+  Pages ahead = {-1, -1};
   if (chunk < stop) {
     reader.load(keys, pages, chunk * kChunk);
     reader.load(values, pages, chunk * kChunk);
+    ahead = reader.pages(next * kChunk);
   }
-  Pages ahead = reader.pages((chunk + kWaves) * kChunk);
   for (int f = wave; f < MT * (D / 32); f += kWaves)
     q[f][lane] = query_operand<D>(a, t, kv_head, (f / (D / 32)) * kTile + c, f % (D / 32));
   Rows<D, MT> r;
@@ -532,6 +538,7 @@ __global__ __launch_bounds__(split_waves(MT) * kWave, 2) void kv_attention_kerne
   // The next chunk's keys are on their way from the scores on, its values from
   // the products on, and the pages of the one after it are looked up.
   for (; chunk < stop; chunk += kWaves) {
+    const int after = next_of(next);
     Span at;
     at.base = chunk * kChunk;
     at.first = t.first;
@@ -543,16 +550,14 @@ __global__ __launch_bounds__(split_waves(MT) * kWave, 2) void kv_attention_kerne
                 !__all(pages.v >= 0 && pages.k >= 0);
     uint32_t weights[MT][8];
     weigh<D, MT>(r, weights, keys, &q[0][0], at, a.scale_log2);
-    const bool more = chunk + kWaves < stop;
-    if (more) reader.load(keys, ahead, at.base + kWaves * kChunk);
+    reader.load(keys, ahead, next * kChunk);
     u32x4 scales = values.scales;
     if (at.masked) mask_values<D, MT>(r, scales, at);
     add_values<D, MT>(r, weights, values, scales);
-    if (more) {
-      reader.load(values, ahead, at.base + kWaves * kChunk);
-      pages = ahead;
-      ahead = reader.pages(at.base + 2 * kWaves * kChunk);
-    }
+    reader.load(values, ahead, next * kChunk);
+    pages = ahead;
+    next = after;
+    ahead = reader.pages(next * kChunk);
   }
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
@@ -752,15 +757,19 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel
 
   int chunk = t.chunk0;
   bool chunk_partial = false, lane_ok = false, pages_ok = false;
+  // (as above: loads without conditions, past the end of the last chunk)
+  const int end = t.chunk1 - 1;
+  auto upto = [&](int at) { return (at < end ? at : end) * kChunk; };
+  Pages ahead = {-1, -1};
   if (chunk < t.chunk1) {
     load(reader.pages(chunk * kChunk), chunk * kChunk);
     chunk_partial = partial(chunk * kChunk);
     lane_ok = ok;
     pages_ok = all_ok;
     stage(0, chunk * kChunk);
-    if (chunk + 1 < t.chunk1) load(reader.pages((chunk + 1) * kChunk), (chunk + 1) * kChunk);
+    load(reader.pages(upto(chunk + 1)), upto(chunk + 1));
+    ahead = reader.pages(upto(chunk + 2));
   }
-  Pages ahead = reader.pages((chunk + 2) * kChunk);
   __syncthreads();
   for (int buffer = 0; chunk < t.chunk1; ++chunk, buffer ^= 1) {
     Span at;
@@ -805,16 +814,14 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel
                                 r.acc[mt][n]);
         }
     }
-    if (chunk + 1 < t.chunk1) {
-      chunk_partial = partial(at.base + kChunk);
-      lane_ok = ok;
-      pages_ok = all_ok;
-      stage(buffer ^ 1, at.base + kChunk);
-      if (chunk + 2 < t.chunk1) {
-        load(ahead, at.base + 2 * kChunk);
-        ahead = reader.pages(at.base + 3 * kChunk);
-      }
-    }
+    // past the last chunk this makes operands that nobody reads
+    const int to = upto(chunk + 1);
+    chunk_partial = partial(to);
+    lane_ok = ok;
+    pages_ok = all_ok;
+    stage(buffer ^ 1, to);
+    load(ahead, upto(chunk + 2));
+    ahead = reader.pages(upto(chunk + 3));
     __syncthreads();
   }
 #pragma unroll
