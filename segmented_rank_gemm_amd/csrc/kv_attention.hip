@@ -29,8 +29,8 @@ namespace lora {
 
 constexpr int kChunk = 64;       // tokens of a wave's step
 constexpr int kTile = 16;        // rows of one matrix product
-// Waves that share out the tokens of a tile of mt * 16 rows: two a SIMD at the
-// registers that they take.
+// Waves that share out the tokens of a tile of mt * 16 rows.  Two workgroups fit
+// a compute unit: four waves a SIMD at 128 registers, or two at 256.
 __host__ __device__ constexpr int split_waves(int mt) { return mt == 1 ? 8 : 4; }
 // Many rows: waves of a workgroup, and 16-row tiles of a wave.
 constexpr int kRowWaves = 4;
@@ -410,11 +410,14 @@ __device__ __forceinline__ int64_t unit_of(const AttentionArgs& a, int seq, int 
   return (static_cast<int64_t>(seq) * a.row_tiles + tile) * a.cache.kv_heads + kv_head;
 }
 
-// The sequence that the index'th workgroups of a launch take: the one with the
-// index'th most tokens, so that the longest start first and the shortest fill
-// the gaps at the end.  Every wave ranks the
-// sequences for itself; with more than a wave's lanes of them, many workgroups a
-// compute unit even the work out and they are taken as they come.
+// The sequence that the index'th workgroups of a launch take: longest first, so
+// that short ones fill the gaps at the end.  A compute unit holds two workgroups;
+// where a launch has no more than that, nothing is left for gaps, and those that
+// come second to their unit go shortest first, each beside a long one (64
+// sequences of 17 to 8192 tokens, 8 key heads: as they come 105 us, longest first
+// 72, this 64; the last two with the loop's present loads).  Every wave ranks the
+// sequences for itself; with more of them than lanes, many workgroups a compute
+// unit even the work out and they are taken as they come.
 __device__ __forceinline__ int sequence_at(const AttentionArgs& a, int index) {
   const int n = static_cast<int>(gridDim.z);
   if (n == 1 || n > kWave) return index;
@@ -429,7 +432,11 @@ __device__ __forceinline__ int sequence_at(const AttentionArgs& a, int index) {
     const int other = __builtin_amdgcn_readlane(work, i);
     rank += other > work || (other == work && i < lane) ? 1 : 0;
   }
-  const unsigned long long hit = __ballot(lane < n && rank == index);
+  int wanted = index;
+  const int each = static_cast<int>(gridDim.x * gridDim.y);  // workgroups of a sequence
+  if (each * n > kCus && each * n <= 2 * kCus && index >= kCus / each)
+    wanted = n - 1 - (index - kCus / each);
+  const unsigned long long hit = __ballot(lane < n && rank == wanted);
   return __ffsll(static_cast<long long>(hit)) - 1;
 }
 
@@ -477,7 +484,7 @@ __device__ __forceinline__ u32x4 query_operand(const AttentionArgs& a, const Row
 // Few rows: the workgroup's waves share out the tokens of one row tile, and the
 // workgroups of a unit (sequence, key head, row tile) its parts.
 template <int D, int MT>
-__global__ __launch_bounds__(split_waves(MT) * kWave, 2) void kv_attention_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(split_waves(MT) * kWave, MT == 1 ? 4 : 2) void kv_attention_kernel(AttentionArgs a) {
   constexpr int kWaves = split_waves(MT);
   const int tid = static_cast<int>(threadIdx.x);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -943,9 +950,9 @@ static AttentionPlan attention_plan(int num_seqs, int max_query_len, int64_t max
   p.part_chunks = static_cast<int>(chunks);
   if (p.many) return p;
   // About a workgroup a CU (131072 tokens, 8 key heads, one row tile: 256
-  // workgroups 42.6 us, 512 47.1, 1024 55.9); two where two fit a CU (four waves
-  // each) and a part is still many rounds of them (128 queries of 32768 tokens
-  // 274 -> 216 us).  A part is whole rounds of the waves.
+  // workgroups 39 us, 1024 45, 2048 58); two for two row tiles where a part is
+  // still many rounds of the waves (128 queries of 32768 tokens 274 -> 216 us).
+  // A part is whole rounds of the waves.
   const int waves = split_waves(mt);
   const int64_t most = (chunks + waves - 1) / waves;
   p.most_parts = (kCus + p.units - 1) / p.units;
