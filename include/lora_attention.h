@@ -12,6 +12,7 @@
  *     error without a synchronisation; each call states what it does instead.
  *     No such value makes a kernel read or write outside its buffers.
  *   - Inputs are never written; outputs are written only where stated.
+ *   - num_tokens is at most 2^22.
  *   - A call over zero tokens (or sequences) returns LORA_OK and enqueues
  *     nothing; its tensors may then be NULL.
  *
@@ -56,7 +57,6 @@ extern "C" {
  *   x, residual  bf16 [num_tokens][ldx], [ldr]; residual may be NULL.
  *   weight       bf16 [hidden].
  *   eps          >= 0, finite.
- *   num_tokens   0 <= num_tokens <= 2^24.
  *   hidden       multiple of 8, 8 <= hidden <= 65536.
  *   residual_out bf16 [num_tokens][ldo]: h; may be NULL; needs a residual.  May be
  *                x or residual itself (same address and stride).

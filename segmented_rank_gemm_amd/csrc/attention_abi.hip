@@ -34,7 +34,7 @@ hipError_t launch_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* qu
 
 namespace {
 
-constexpr int32_t kMaxTokens = 1 << 24;
+constexpr int32_t kMaxTokens = 1 << 22;  // times 1024 threads: a grid dimension
 constexpr int32_t kMaxHidden = 65536;
 constexpr int32_t kMaxHeads = 1024;
 constexpr int32_t kMaxSeqs = 65535;     // a grid dimension

@@ -104,11 +104,13 @@ __global__ __launch_bounds__(kKvThreads) void kv_append_kernel(AppendArgs a) {
   const int step = static_cast<int>(gridDim.y) * (kKvThreads / kChunks);
   int head = (static_cast<int>(blockIdx.y) * kKvThreads + static_cast<int>(threadIdx.x)) / kChunks;
   const uint16_t* row = a.qkv + token * a.ldqkv;
-  u32x4 own = {0, 0, 0, 0}, other = {0, 0, 0, 0};
+  // (without conditions, so that a head's use waits for its own loads only; past
+  // the last head, and for partners that are not needed, what is there is loaded)
+  u32x4 own, other;
   auto load = [&](int h) {
-    if (h >= heads) return;
-    own = load16(row + h * D + p.e);
-    if (p.partner != p.e && h < a.q_heads + a.kv_heads) other = load16(row + h * D + p.partner);
+    const uint16_t* src = row + (h < heads ? h : heads - 1) * D;
+    own = load16(src + p.e);
+    other = load16(src + p.partner);
   };
   load(head);
   for (; head < heads; head += step) {

@@ -43,6 +43,7 @@ NORM = dict(x=FAKE, ldx=64, residual=FAKE, ldr=64, weight=FAKE, eps=1e-5, num_to
     (dict(residual_out=None, y=None, y8=None, scales=None), INVALID),
     (dict(eps=-1e-9), INVALID), (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID),
     (dict(num_tokens=-1), INVALID), (dict(num_tokens=(1 << 24) + 1), INVALID),
+    (dict(num_tokens=(1 << 22) + 1), INVALID),
     (dict(hidden=0), INVALID), (dict(hidden=60), INVALID), (dict(hidden=65544, ldx=65544), INVALID),
     (dict(group=0), INVALID), (dict(group=48), INVALID), (dict(group=16), UNSUPPORTED),
     (dict(group=8), UNSUPPORTED),
