@@ -19,9 +19,11 @@
 // times a power of two).  Scores, maxima, sums and outputs are fp32; the weights
 // are rounded to bf16 for the second product, as the matrix unit takes them.
 //
-// Bound by: HBM (68 bytes a token and head at D = 128) as long as the rows of a
-// key head fit one tile; by the exponentials and the matrix unit for prompts.
-
+// Bound by: HBM (136 bytes a token and key head at D = 128) as long as the rows of
+// a key head fit one tile (4.5 TB/s at 64 sequences of up to 8192 tokens, where a
+// copy reaches 4.9); for prompts by the vector unit beside the matrix unit (1030
+// TFLOP/s at 8 sequences of 2048 queries over 8192 tokens, where a library product
+// reaches 1340), which one wave uses in turn.
 
 #include "kv_format.hpp"
 
@@ -958,6 +960,9 @@ static AttentionPlan attention_plan(int num_seqs, int max_query_len, int64_t max
   p.most_parts = (kCus + p.units - 1) / p.units;
   if (mt == 2 && most >= 16 * p.most_parts) p.most_parts = (2 * kCus + p.units - 1) / p.units;
   p.most_parts = p.most_parts < most ? p.most_parts : most;
+  // One round less is not worth the launch that joins the parts (1000 tokens, 8
+  // key heads: 2 rounds 10.1 us, 2 parts of 1 round 10.7; 2000: 13.5 and 10.9).
+  if (most - (most + p.most_parts - 1) / p.most_parts < 2) p.most_parts = 1;
   const int64_t rounds = (most + p.most_parts - 1) / p.most_parts;
   p.part_chunks = static_cast<int>(rounds * waves);
   p.parts = static_cast<int>((most + rounds - 1) / rounds);

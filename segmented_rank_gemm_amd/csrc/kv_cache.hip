@@ -3,6 +3,11 @@
 //
 // A thread takes 8 elements of a head (16 bytes of bf16, 4 bytes of codes); four
 // neighbouring lanes share a 32-element block and its scale byte.
+//
+// Bound by: HBM and, for the rotation, the 64-bit conversions beside it (4096
+// tokens of 32 and 32 heads of 128: append 40 us, 3.8 TB/s, read 18 us, 4.6 TB/s,
+// where a copy reaches 4.9; 64 tokens of 64 and 8 heads 3.4 and 2.6 us, of which
+// an empty launch is about 2).
 
 #include "kv_format.hpp"
 
