@@ -24,7 +24,9 @@
  *                                       one mantissa bit, the magnitudes
  *                                       0, 0.5, 1, 1.5, 2, 3, 4, 6;
  *   scales  [head_dim / 32][page_size]  one byte b for each 32 elements of one
- *                                       token's head: 2^(b - 127), or NaN (b = 255).
+ *                                       token's head: 2^(b - 127) for b in
+ *                                       [2, 252], NaN for b = 255; lora_kv_append
+ *                                       writes no others.
  * An element is its code's value times its block's scale, a bf16 number exactly.
  * A place (slot) is page * page_size + offset in the page.
  */

@@ -34,7 +34,7 @@ struct NormArgs {
   uint8_t* y8;      // or nullptr
   float* scales;    // with y8
   int64_t ldx, ldr, lds, ldy, ldy8;
-  double eps;
+  double eps, inv_hidden;
   int hidden;
   int group;        // elements a scale; hidden: one a row
   int group_shift;  // log2 of the chunks of 8 a group, where there are several groups
@@ -101,6 +101,17 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v, int shift) {
   return v;
 }
 
+// 1 / sqrt(x) to about 50 bits: the hardware's estimate and two Newton steps, a
+// third of what a division and a root cost every thread.  0, infinity and NaN
+// give what the estimate gives.
+__device__ __forceinline__ double inverse_root(double x) {
+  const double first = __builtin_amdgcn_rsq(x);
+  double r = first;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) r = fma(0.5 * r, fma(-x * r, r, 1.0), r);
+  return r == r ? r : first;
+}
+
 // 1 / s for a normal fp32 number s in [2^-126, 2^125], to about 45 bits.
 __device__ __forceinline__ double inverse(float s) {
   const double x = __builtin_amdgcn_rcpf(s);
@@ -124,6 +135,8 @@ struct NormRow {
   __device__ __forceinline__ static int at(int c) {
     return c * T + static_cast<int>(threadIdx.x);
   }
+  // Past the row's end, its last chunk: loads need no condition.
+  __device__ __forceinline__ int load_at(int c) const { return at(c) < chunks ? at(c) : chunks - 1; }
   // No lane of this wave has a chunk c.
   __device__ __forceinline__ bool past(int c) const { return at(c) - lane_id() >= chunks; }
 };
@@ -132,8 +145,13 @@ struct NormRow {
 // largest |h w| of the row.
 template <int T, int C>
 __device__ __forceinline__ void emit(const NormArgs& a, const NormRow<T, C>& n, int64_t row, double top) {
+  // The weights again (from the L1 cache), all of them before the first output: a
+  // load's wait counts the stores before it.
+  u32x4 w[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) w[c] = load16(a.weight + 8 * n.load_at(c));
   const Factor to_v = factor(n.r);
-  const double per_scale = n.r / kE4m3Max;
+  const double per_scale = n.r * (1.0 / kE4m3Max);
   float s = static_cast<float>(top * per_scale);
   s = s < kMinScale ? kMinScale : s;
   double code = n.r * inverse(s);  // what turns h w into the number that is coded
@@ -143,11 +161,9 @@ __device__ __forceinline__ void emit(const NormArgs& a, const NormRow<T, C>& n, 
     if (n.past(c)) break;
     const int i = n.at(c);
     const bool in = i < n.chunks;
-    u32x4 w = {0, 0, 0, 0};
-    if (in) w = load16(a.weight + 8 * i);
     float p[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) p[k] = in ? bf16_at(n.h[c], k) * bf16_at(w, k) : 0.f;
+    for (int k = 0; k < 8; ++k) p[k] = bf16_at(n.h[c], k) * bf16_at(w[c], k);
     if (a.y && in) {
       u32x4 o;
 #pragma unroll
@@ -168,14 +184,25 @@ __device__ __forceinline__ void emit(const NormArgs& a, const NormRow<T, C>& n, 
         a.scales[row * (n.chunks >> a.group_shift) + (i >> a.group_shift)] = s;
     }
     if (!in) continue;
+    // Only where the nearest fp32 number is itself a border between two codes (its
+    // last 20 bits, a one and zeros; or something below 2^-6, where they are others)
+    // does it matter on which side of it the product is.
+    const Factor f = factor(code);
     float u[8];
-    if (code >= 0x1p-60 && code <= 0x1p60) {
-      const Factor f = factor(code);
+    uint32_t border = ~0u, least = ~0u;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] = times_odd(p[k], f);
-    } else {
+    for (int k = 0; k < 8; ++k) {
+      u[k] = times(p[k], f);
+      const uint32_t bits = __float_as_uint(u[k]);
+      border = min(border, (bits & 0xFFFFFu) ^ 0x80000u);
+      least = min(least, bits & 0x7FFFFFFFu);
+    }
+    if (!(code >= 0x1p-60 && code <= 0x1p60)) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) u[k] = to_odd(p[k] * code);
+    } else if (border == 0 || least < __float_as_uint(0x1p-6f)) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) u[k] = times_odd(p[k], f);
     }
     *(LORA_GLOBAL u32x2*)(a.y8 + row * a.ldy8 + 8 * i) =
         u32x2{pack_e4m3x4(u[0], u[1], u[2], u[3]), pack_e4m3x4(u[4], u[5], u[6], u[7])};
@@ -299,7 +326,7 @@ __global__ __launch_bounds__(T) void rms_norm_kernel(NormArgs a) {
     top_bits = max(top_bits, part_top[i]);
   }
   if (!a.y && !a.y8) return;
-  n.r = 1.0 / sqrt(sum / a.hidden + a.eps);
+  n.r = inverse_root(fma(sum, a.inv_hidden, a.eps));
   // the same for all threads of the row
   if (top_bits < 0x7F800000u && n.r >= 0x1p-60 && n.r <= 0x1p10)
     emit<T, C>(a, n, row, __uint_as_float(top_bits));
@@ -321,7 +348,7 @@ hipError_t launch_rms_norm(const uint16_t* x, int64_t ldx, const uint16_t* resid
                            uint16_t* sum, int64_t lds, uint16_t* y, int64_t ldy, uint8_t* y8,
                            int64_t ldy8, float* scales, int group, hipStream_t stream) {
   const NormArgs a = {x, residual, weight, sum, y, y8, scales, ldx, ldr, lds, ldy, ldy8,
-                      eps, hidden, group, group < hidden ? __builtin_ctz(group / 8) : 0};
+                      eps, 1.0 / hidden, hidden, group, group < hidden ? __builtin_ctz(group / 8) : 0};
   const int chunks = hidden / 8;
   // Threads a row: enough that a thread has few chunks, and no more, since idle
   // waves cost their launch (us, 64 / 256 / 512 / 1024 threads: 8192 rows of 512
