@@ -21,7 +21,7 @@
 //
 // Bound by: HBM (136 bytes a token and key head at D = 128) as long as the rows of
 // a key head fit one tile (4.5 TB/s at 64 sequences of up to 8192 tokens, where a
-// copy reaches 4.9); for prompts by the vector unit beside the matrix unit (1030
+// copy reaches 4.9); for prompts by the vector unit beside the matrix unit (1050
 // TFLOP/s at 8 sequences of 2048 queries over 8192 tokens, where a library product
 // reaches 1340), which one wave uses in turn.
 
@@ -177,50 +177,50 @@ __device__ __forceinline__ uint32_t seen_bits(const Span& at, int place) {
   return at.ok && hi >= lo ? ((2u << hi) - 1u) & ~((1u << lo) - 1u) : 0u;
 }
 
-// The running softmax over one chunk's scores s[mt][j][i] (of token 16 g + 4 i + j),
-// and the weights in bf16 (pairs of tokens 16 g + 2 i, + 1).
+// The first half of the running softmax over one chunk's scores of row tile mt,
+// s[j][i] of token 16 g + 4 i + j: hides what a row does not see and moves the
+// running maximum.
 template <int D, int MT>
-__device__ __forceinline__ void soften(Rows<D, MT>& r, uint32_t (&weights)[MT][8],
-                                       f32x4 (&s)[MT][4], const Span& at, float scale_log2) {
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    if (at.masked) {
-      const uint32_t seen = seen_bits(at, r.place[mt]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!(seen >> (4 * i + j) & 1u)) s[mt][j][i] = -INFINITY;
-    }
-    float m = s[mt][0][0];
+__device__ __forceinline__ void raise(Rows<D, MT>& r, int mt, f32x4 (&s)[4], const Span& at,
+                                      float scale_log2) {
+  if (at.masked) {
+    const uint32_t seen = seen_bits(at, r.place[mt]);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) m = fmaxf(m, s[mt][j][i]);
-    m *= scale_log2;
-    if (__any(m > r.top[mt] + kMaxLag)) {
-      m = fmaxf(m, __shfl_xor(m, 16));
-      m = fmaxf(m, __shfl_xor(m, 32));
-      const float now = fmaxf(r.top[mt], m);
-      const float shrink = __builtin_amdgcn_exp2f(r.top[mt] - now);
-      r.top[mt] = now;
-      r.sum[mt] *= shrink;
-#pragma unroll
-      for (int n = 0; n < D / 16; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r.acc[mt][n][i] *= shrink;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float p[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        p[j] = __builtin_amdgcn_exp2f(fmaf(s[mt][j][i], scale_log2, -r.top[mt]));
-      r.sum[mt] += (p[0] + p[1]) + (p[2] + p[3]);
-      weights[mt][2 * i] = pack_bf16x2(p[0], p[1]);
-      weights[mt][2 * i + 1] = pack_bf16x2(p[2], p[3]);
-    }
+      for (int i = 0; i < 4; ++i)
+        if (!(seen >> (4 * i + j) & 1u)) s[j][i] = -INFINITY;
   }
+  float m = s[0][0];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, s[j][i]);
+  m *= scale_log2;
+  if (__any(m > r.top[mt] + kMaxLag)) {
+    m = fmaxf(m, __shfl_xor(m, 16));
+    m = fmaxf(m, __shfl_xor(m, 32));
+    const float now = fmaxf(r.top[mt], m);
+    const float shrink = __builtin_amdgcn_exp2f(r.top[mt] - now);
+    r.top[mt] = now;
+    r.sum[mt] *= shrink;
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.acc[mt][n][i] *= shrink;
+  }
+}
+
+// The second half, a quarter of it: the weights of the tokens 16 g + 4 i + j, in
+// bf16 (pairs of tokens 16 g + 2 i, + 1).
+__device__ __forceinline__ void powers(uint32_t (&weights)[8], float& sum, const f32x4 (&s)[4], int i,
+                                       float top, float scale_log2) {
+  float p[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) p[j] = __builtin_amdgcn_exp2f(fmaf(s[j][i], scale_log2, -top));
+  sum += (p[0] + p[1]) + (p[2] + p[3]);
+  weights[2 * i] = pack_bf16x2(p[0], p[1]);
+  weights[2 * i + 1] = pack_bf16x2(p[2], p[3]);
 }
 
 // Scores of one chunk and their weights.  q: the operand [mt][D / 32][lane] in
@@ -246,7 +246,12 @@ __device__ __forceinline__ void weigh(Rows<D, MT>& r, uint32_t (&weights)[MT][8]
       for (int mt = 0; mt < MT; ++mt) s[mt][j] = mfma(__builtin_bit_cast(bf16x8, w), b[mt], s[mt][j]);
     }
   }
-  soften<D, MT>(r, weights, s, at, scale_log2);
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    raise<D, MT>(r, mt, s[mt], at, scale_log2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) powers(weights[mt], r.sum[mt], s[mt], i, r.top[mt], scale_log2);
+  }
 }
 
 // Bits `nan` of this lane's 16 tokens: value blocks that held a NaN and were
@@ -791,37 +796,47 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel
     at.masked = at.base < all_first || at.base + kChunk > all_last || !pages_ok;
     const bool whole = !chunk_partial;
     if (at.base < last && at.base + kChunk > first) {  // some row of this wave sees some of it
+      static_assert(MT == 2, "the two row tiles take turns");
       f32x4 s[MT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[mt][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bf16x8 k = __builtin_bit_cast(bf16x8, keys[buffer][j][i][lane]);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) s[mt][j] = mfma(k, q[mt][i], s[mt][j]);
-        }
       uint32_t weights[MT][8];
-      soften<D, MT>(r, weights, s, at, a.scale_log2);
+      // The matrix products of one row tile beside the powers of the other, for
+      // which keys and values are read from shared memory once a tile (8 sequences
+      // of up to 4608 tokens in pieces: 293 -> 284 us; told to interleave them in
+      // fixed patterns the compiler did worse, 297 to 333).
+      auto scores = [&](int mt, int i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          s[mt][j] = mfma(__builtin_bit_cast(bf16x8, keys[buffer][j][i][lane]), q[mt][i],
+                          i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : s[mt][j]);
+      };
+      auto products = [&](int mt, int h, int n0, int n1) {
+        const bf16x8 p = as_bf16x8(weights[mt][4 * h], weights[mt][4 * h + 1], weights[mt][4 * h + 2],
+                                   weights[mt][4 * h + 3]);
+#pragma unroll
+        for (int n = n0; n < n1; ++n)
+          r.acc[mt][n] = mfma(__builtin_bit_cast(bf16x8, values[buffer][h][n][lane]), p, r.acc[mt][n]);
+      };
+      constexpr int kEvery = 4 / (D / 32);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) scores(0, i);
+      raise<D, MT>(r, 0, s[0], at, a.scale_log2);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i % kEvery == 0) scores(1, i / kEvery);
+        powers(weights[0], r.sum[0], s[0], i, r.top[0], a.scale_log2);
+      }
+      raise<D, MT>(r, 1, s[1], at, a.scale_log2);
       if (!whole) {
         const int b = c / (kBlock / (D / 16));
         mark_nan<D, MT>(r, nans[buffer][0][g][b] | nans[buffer][1][g][b] << 8, at);
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int i = 0; i < 4; ++i) {
+        products(0, i >> 1, (i & 1) * (D / 32), ((i & 1) + 1) * (D / 32));
+        powers(weights[1], r.sum[1], s[1], i, r.top[1], a.scale_log2);
+      }
 #pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-          const bf16x8 v = __builtin_bit_cast(bf16x8, values[buffer][h][n][lane]);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-            r.acc[mt][n] = mfma(v,
-                                as_bf16x8(weights[mt][4 * h], weights[mt][4 * h + 1],
-                                          weights[mt][4 * h + 2], weights[mt][4 * h + 3]),
-                                r.acc[mt][n]);
-        }
+      for (int h = 0; h < 2; ++h) products(1, h, 0, D / 16);
     }
     // past the last chunk this makes operands that nobody reads
     const int to = upto(chunk + 1);
