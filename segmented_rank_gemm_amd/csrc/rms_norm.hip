@@ -10,7 +10,7 @@
 // formula.  h w is exact in fp32 (8 by 8 significant bits); it is multiplied by a
 // factor held as the sum of two fp32 numbers, which costs four operations where
 // 64-bit arithmetic takes a multiplication and two conversions at a quarter of
-// the rate (1001 rows of 11008: 20.4 us then, 15.7 now, the borders' care in it).
+// the rate (1001 rows of 11008: 20.4 us then, 14.3 now, the borders' care in it).
 // Only the sum of squares is in 64 bits.
 //
 // Bound by: HBM for long batches (8192 rows of 8192 with residual, sum, bf16 and 8

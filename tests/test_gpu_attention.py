@@ -391,6 +391,28 @@ def test_kv_attention(case):
     c.check()
 
 
+def spread(n, longest, seed):
+    return np.random.default_rng(seed).integers(0, longest, n).tolist()
+
+
+# More sequences than a wave ranks, and launches that just fill the device, in which
+# the order of the sequences turns round half way.
+BATCHES = [
+    (spread(70, 41, 1), [1] * 70, 4, 2, 64, 16, 0),
+    (spread(65, 90, 2), [1, 3] * 32 + [1], 6, 2, 128, 16, 20),
+    (spread(40, 70, 3), [1] * 40, 16, 8, 64, 16, 0),
+    (spread(64, 70, 4), [1] * 64, 8, 8, 64, 32, 0),
+    (spread(33, 70, 5), [2] * 33, 32, 8, 128, 16, 0),
+]
+
+
+@pytest.mark.parametrize("case", BATCHES, ids=[str(i) for i in range(len(BATCHES))])
+def test_kv_attention_batches(case):
+    c = Call(40 + len(case[0]), *case)
+    c.run()
+    c.check()
+
+
 # Many rows over enough (sequence, key head, 128 rows) that operands are shared by a
 # workgroup: lens, queries, q_heads, kv_heads, head_dim, page, window
 MANY = [
