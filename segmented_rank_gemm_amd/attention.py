@@ -55,51 +55,59 @@ _kv_read, _kv_attention = lib().lora_kv_read, lib().lora_kv_attention
 
 
 # The checks below run on every call, and a decode step's calls are as short as
-# they are: each looks at a tensor's type, shape and strides once.
+# they are: each looks at a tensor's type, shape and strides once, and what is
+# wrong is found out only when something is.
 _BF16, _F32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 _I32T, _I64T, _U8 = torch.int32, torch.int64, torch.uint8
 
 
-def _refuse(t, dtype: torch.dtype, shape, name: str) -> None:
+def _refuse(t, dtype: torch.dtype, shape, name: str, layout: str) -> None:
     _dev_ptr(t, dtype, name)  # raises what the rest of the binding raises
-    raise ValueError(f"{name} must be {list(shape)}, is {list(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, is {list(t.shape)}")
+    raise ValueError(f"{name} must {layout}, has strides {t.stride()}")
 
 
 def _matrix(t: torch.Tensor, dtype: torch.dtype, rows: int, width: int, name: str):
     """Address and row stride of a [rows, width] matrix with unit column stride."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or t.shape != (rows, width):
-        _refuse(t, dtype, (rows, width), name)
-    stride, unit = t.stride()
-    if unit != 1 and width > 1:
-        raise ValueError(f"{name} must have unit column stride")
-    # a single row's stride is never used for an address: any value that passes will do
-    return t.data_ptr(), stride if rows > 1 else width
+    try:
+        if t.dtype is dtype and t.is_cuda and t.shape == (rows, width):
+            stride, unit = t.stride()
+            if unit == 1 or width == 1:
+                # a single row's stride is never used for an address: any that passes will do
+                return t.data_ptr(), stride if rows > 1 else width
+    except AttributeError:
+        pass
+    _refuse(t, dtype, (rows, width), name, "have unit column stride")
 
 
 def _heads(t: torch.Tensor, rows: int, heads: int, head_dim: int, name: str):
     """Address and row stride of a bf16 [rows, heads, head_dim] tensor whose heads
     lie one behind another."""
-    if (not isinstance(t, torch.Tensor) or t.dtype != _BF16 or not t.is_cuda
-            or t.shape != (rows, heads, head_dim)):
-        _refuse(t, _BF16, (rows, heads, head_dim), name)
-    stride, between, unit = t.stride()
-    if (unit != 1 and head_dim > 1) or (between != head_dim and heads > 1):
-        raise ValueError(f"{name} must have each row's heads contiguous")
-    return t.data_ptr(), stride if rows > 1 else heads * head_dim
+    try:
+        if t.dtype is _BF16 and t.is_cuda and t.shape == (rows, heads, head_dim):
+            stride, between, unit = t.stride()
+            if (unit == 1 or head_dim == 1) and (between == head_dim or heads == 1):
+                return t.data_ptr(), stride if rows > 1 else heads * head_dim
+    except AttributeError:
+        pass
+    _refuse(t, _BF16, (rows, heads, head_dim), name, "have each row's heads contiguous")
 
 
 def _vector(t: torch.Tensor, dtype: torch.dtype, n: int, name: str) -> int:
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or t.shape != (n,):
-        _refuse(t, dtype, (n,), name)
-    if n > 1 and t.stride(0) != 1:
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.is_cuda and t.shape == (n,) and (n <= 1 or t.stride(0) == 1):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, dtype, (n,), name, "be contiguous")
 
 
 def _dims(t: torch.Tensor, n: int, name: str):
-    if not isinstance(t, torch.Tensor) or t.dim() != n:
+    shape = getattr(t, "shape", ())
+    if len(shape) != n:
         raise ValueError(f"{name} must be a {n}-D tensor")
-    return t.shape
+    return shape
 
 
 def kv_cache_shape(num_pages: int, kv_heads: int, head_dim: int, page_size: int):
@@ -113,9 +121,10 @@ def kv_cache_shape(num_pages: int, kv_heads: int, head_dim: int, page_size: int)
 def _cache(cache: torch.Tensor, head_dim: int) -> Tuple[int, int, int, int]:
     """Address, pages, kv_heads and page size of a cache for this head_dim."""
     ptr = _dev_ptr(cache, _U8, "cache")
-    if cache.dim() != 4 or cache.shape[1] != 2 or not cache.is_contiguous():
+    shape = cache.shape
+    if len(shape) != 4 or shape[1] != 2 or not cache.is_contiguous():
         raise ValueError("cache must be contiguous [num_pages, 2, kv_heads, page_bytes]")
-    pages, _, heads, size = cache.shape
+    pages, _, heads, size = shape
     row = head_dim // 2 + head_dim // 32  # bytes of one token's head
     if row < 1 or size % row:
         raise ValueError(f"cache pages of {size} bytes hold no heads of {head_dim}")

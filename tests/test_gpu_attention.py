@@ -686,3 +686,48 @@ def test_layer_in_a_graph():
         torch.cuda.synchronize()
         for a, b in zip(got, (sums, y, scales, q, out, cache)):
             assert torch.equal(a, b), k
+
+
+def test_binding_refuses_what_does_not_fit():
+    """Tensors of another type, shape or layout are refused before the library is
+    called, by name."""
+    x = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(256, dtype=torch.bfloat16, device="cuda")
+    y8, s = torch.empty(4, 256, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(4, 2, device="cuda")
+    norm = lambda **k: srg.lora_rms_norm(**{**dict(x=x, weight=w, eps=1e-5, y=torch.empty_like(x)), **k})  # noqa: E731
+    for error, name, more in [
+            (TypeError, "x", dict(x=x.float())), (TypeError, "x", dict(x=x.cpu())),
+            (ValueError, "x", dict(x=x[0])), (ValueError, "x", dict(x=x.t().contiguous().t(), weight=w)),
+            (TypeError, "weight", dict(weight=None)), (ValueError, "weight", dict(weight=w[:8])),
+            (ValueError, "weight", dict(weight=torch.ones(512, dtype=torch.bfloat16, device="cuda")[::2])),
+            (ValueError, "y", dict(y=x[:3])), (TypeError, "y8", dict(y8=x, scales=s)),
+            (ValueError, "scales", dict(y8=y8, scales=s[:, 0])), (ValueError, "scales", dict(y8=y8, scales=torch.empty(4, 3, device="cuda"))),
+            (ValueError, "scales", dict(y8=y8, scales=torch.empty(4, 4, device="cuda")[:, :2]))]:
+        with pytest.raises(error, match=name):
+            norm(**more)
+    with pytest.raises(srg.LoraError):
+        norm(y8=y8)                                  # no scales
+    with pytest.raises(srg.LoraError):
+        norm(eps=-1.0)
+    cache = cache_of(4, 2, 128, 16)
+    slots, q = torch.zeros(3, dtype=torch.int64, device="cuda"), torch.empty(3, 4, 128, dtype=torch.bfloat16, device="cuda")
+    qkv = torch.zeros(3, 8 * 128, dtype=torch.bfloat16, device="cuda")
+    append = lambda **k: srg.lora_kv_append(**{**dict(qkv=qkv, positions=None, slots=slots, rope=None, cache=cache,  # noqa: E731
+                                                      q_out=q), **k})
+    for error, name, more in [
+            (ValueError, "qkv", dict(qkv=qkv[:, :-8])), (TypeError, "slots", dict(slots=slots.int())),
+            (ValueError, "cache", dict(cache=cache[..., :-2].contiguous())), (ValueError, "cache", dict(cache=cache[:, :1])),
+            (ValueError, "q_out", dict(q_out=q[0])), (ValueError, "q_out", dict(q_out=q.transpose(1, 2).contiguous().transpose(1, 2))),
+            (TypeError, "positions", dict(rope=srg.rope_table(8, 128)))]:
+        with pytest.raises(error, match=name):
+            append(**more)
+    with pytest.raises(ValueError, match="k_out"):
+        srg.lora_kv_read(slots, cache, q, None)
+    c = Call(50, [20], [1], 4, 2, 64, 16)
+    for error, name, more in [
+            (ValueError, "query_start", {0: c.dev[0][:1]}), (TypeError, "seq_lens", {1: c.dev[1].long()}),
+            (ValueError, "page_table", {2: c.dev[2][0]})]:
+        with pytest.raises(error, match=name):
+            srg.lora_kv_attention(c.q, *[more.get(i, t) for i, t in enumerate(c.dev)], c.cache, c.out, 1.0, None, 1)
+    with pytest.raises(ValueError, match="max_seq_len"):
+        c.run(max_seq_len=1000)
