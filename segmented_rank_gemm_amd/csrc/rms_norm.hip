@@ -7,8 +7,9 @@
 // The row stays in registers between the sum and the outputs, so each input is
 // read once.  Up to its one rounding to bf16 (through fp32) or 8 bits v carries
 // about 46 bits: next to a border between two codes the result is then that of the
-// formula.  h w is exact in fp32 (8 by 8 significant bits); it is multiplied by a
-// factor held as the sum of two fp32 numbers, which costs four operations where
+// formula.  h w is exact in fp32 (8 by 8 significant bits; rows with a product below
+// the normal numbers take the other way); it is multiplied by a factor held as the
+// sum of two fp32 numbers, which costs four operations where
 // 64-bit arithmetic takes a multiplication and two conversions at a quarter of
 // the rate (1001 rows of 11008: 20.4 us then, 14.3 now, the borders' care in it).
 // Only the sum of squares is in 64 bits.
@@ -24,6 +25,8 @@ namespace lora {
 
 constexpr double kE4m3Max = 448.0;
 constexpr float kMinScale = 1.17549435e-38f;  // 2^-126
+constexpr uint32_t kInfinity = 0x7F800000u;
+constexpr int kSubnormal = 0x90;  // of the classes of fp32 numbers: both signs' subnormal ones
 
 struct NormArgs {
   const uint16_t* x;
@@ -141,7 +144,7 @@ struct NormRow {
   __device__ __forceinline__ bool past(int c) const { return at(c) - lane_id() >= chunks; }
 };
 
-// The outputs where h w and its factors stay well inside fp32's range; top: the
+// The outputs where h w, its factors and v stay well inside fp32's range; top: the
 // largest |h w| of the row.
 template <int T, int C>
 __device__ __forceinline__ void emit(const NormArgs& a, const NormRow<T, C>& n, int64_t row, double top) {
@@ -285,6 +288,7 @@ __global__ __launch_bounds__(T) void rms_norm_kernel(NormArgs a) {
   }
   double sum = 0.0;
   uint32_t top_bits = 0;  // of the largest |h w|: integer order, infinity and NaN on top
+  bool subnormal = false;  // some h w has lost bits
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int i = n.at(c);
@@ -302,9 +306,12 @@ __global__ __launch_bounds__(T) void rms_norm_kernel(NormArgs a) {
       const float e = bf16_at(n.h[c], k);
       const double e64 = e;
       sum = fma(e64, e64, sum);
-      top_bits = max(top_bits, __float_as_uint(e * bf16_at(w, k)) & 0x7FFFFFFFu);
+      const float p = e * bf16_at(w, k);
+      top_bits = max(top_bits, __float_as_uint(p) & 0x7FFFFFFFu);
+      subnormal |= __builtin_amdgcn_classf(p, kSubnormal);
     }
   }
+  if (subnormal) top_bits = kInfinity;
   __shared__ double part_sum[(T / kWave)];
   __shared__ uint32_t part_top[(T / kWave)];
   __shared__ double spare[(T / kWave)];
@@ -327,8 +334,10 @@ __global__ __launch_bounds__(T) void rms_norm_kernel(NormArgs a) {
   }
   if (!a.y && !a.y8) return;
   n.r = inverse_root(fma(sum, a.inv_hidden, a.eps));
-  // the same for all threads of the row
-  if (top_bits < 0x7F800000u && n.r >= 0x1p-60 && n.r <= 0x1p10)
+  // The same for all threads of the row.  The last bound keeps v, and the scales with
+  // their inverses, inside fp32's normal numbers, however large the weights.
+  if (top_bits < kInfinity && n.r >= 0x1p-60 && n.r <= 0x1p10 &&
+      __uint_as_float(top_bits) * n.r <= 0x1p120)
     emit<T, C>(a, n, row, __uint_as_float(top_bits));
   else
     emit_wide<T, C>(a, n, row, spare);
