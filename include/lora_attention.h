@@ -136,6 +136,11 @@ lora_status_t lora_kv_read(const int64_t *slots, int32_t num_tokens, int32_t kv_
  * t > place - window where a window is given.  (The queries are the sequence's
  * last tokens, already appended.)  A query that sees nothing gets zeros.
  * Query head h reads key head h / (q_heads / kv_heads).
+ * Scores, their maxima and all sums are fp32; the weights exp(score - maximum) are
+ * rounded to bf16 and divided by the sum of the rounded ones, so that a result is
+ * off by about 2^-8 of the mean of |v_t - out| at most besides its own rounding.  Scores
+ * have to stay inside fp32's range: a row that has some above it is NaN, and one
+ * whose scores are all below it counts as one that sees nothing.
  *
  *   q            bf16 [num_tokens][ldq]: q_heads heads of head_dim.
  *   query_start  int32 [num_seqs + 1]: sequence s has the rows [query_start[s],
