@@ -55,11 +55,12 @@ int32_t page_shift(int32_t page_size) {
   return -1;
 }
 
-lora_status_t cache_ok(const uint8_t* cache, int32_t num_pages, int32_t page_size, int32_t kv_heads,
-                       int32_t head_dim) {
-  if (!cache || !aligned(cache, 16) || num_pages < 1 || page_size < 1 || kv_heads < 1 ||
-      kv_heads > kMaxHeads || head_dim < 1)
+// used: the call reads or writes the cache; its address is not looked at otherwise.
+lora_status_t cache_ok(bool used, const uint8_t* cache, int32_t num_pages, int32_t page_size,
+                       int32_t kv_heads, int32_t head_dim) {
+  if (num_pages < 0 || page_size < 1 || kv_heads < 1 || kv_heads > kMaxHeads || head_dim < 1)
     return LORA_ERR_INVALID_ARGUMENT;
+  if (used && (!cache || !aligned(cache, 16) || num_pages < 1)) return LORA_ERR_INVALID_ARGUMENT;
   if (page_shift(page_size) < 0 || (head_dim != 64 && head_dim != 128)) return LORA_ERR_UNSUPPORTED;
   return LORA_OK;
 }
@@ -112,15 +113,15 @@ lora_status_t lora_kv_append(const uint16_t* qkv, int64_t ldqkv, const int32_t* 
                              hipStream_t stream) {
   if (num_tokens < 0 || num_tokens > kMaxTokens || q_heads < 1 || q_heads > kMaxHeads)
     return LORA_ERR_INVALID_ARGUMENT;
-  const lora_status_t st = cache_ok(cache, num_pages, page_size, kv_heads, head_dim);
+  const lora_status_t st = cache_ok(num_tokens > 0, cache, num_pages, page_size, kv_heads, head_dim);
   if (st == LORA_ERR_INVALID_ARGUMENT) return st;
   if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16 != 0 || interleaved < 0 || interleaved > 1)
     return LORA_ERR_INVALID_ARGUMENT;
-  if (rot_dim > 0 && (!rope || !aligned(rope, 16) || rope_rows < 1)) return LORA_ERR_INVALID_ARGUMENT;
   const int64_t q_width = static_cast<int64_t>(q_heads) * head_dim;
   const int64_t width = q_width + 2 * static_cast<int64_t>(kv_heads) * head_dim;
-  if (num_tokens > 0 && (!rows_ok(qkv, ldqkv, width) || !rows_ok(q_out, ldq, q_width) || !slots ||
-                         (rot_dim > 0 && !positions)))
+  if (num_tokens > 0 && (!rows_ok(qkv, ldqkv, width) || !rows_ok(q_out, ldq, q_width) || !slots))
+    return LORA_ERR_INVALID_ARGUMENT;
+  if (num_tokens > 0 && rot_dim > 0 && (!positions || !rope || !aligned(rope, 16) || rope_rows < 1))
     return LORA_ERR_INVALID_ARGUMENT;
   if (st != LORA_OK) return st;
   if (num_tokens == 0) return LORA_OK;
@@ -136,7 +137,7 @@ lora_status_t lora_kv_read(const int64_t* slots, int32_t num_tokens, int32_t kv_
                            int64_t ldv, hipStream_t stream) {
   if (num_tokens < 0 || num_tokens > kMaxTokens || (num_tokens > 0 && !k_out && !v_out))
     return LORA_ERR_INVALID_ARGUMENT;
-  const lora_status_t st = cache_ok(cache, num_pages, page_size, kv_heads, head_dim);
+  const lora_status_t st = cache_ok(num_tokens > 0, cache, num_pages, page_size, kv_heads, head_dim);
   if (st == LORA_ERR_INVALID_ARGUMENT) return st;
   const int64_t width = static_cast<int64_t>(kv_heads) * head_dim;
   if (num_tokens > 0 && (!slots || (k_out && !rows_ok(k_out, ldk, width)) ||
@@ -171,23 +172,24 @@ lora_status_t lora_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* q
       !attention_sizes_ok(num_seqs, max_query_len, max_seq_len, q_heads, kv_heads) ||
       !isfinite(scale) || window < 0)
     return LORA_ERR_INVALID_ARGUMENT;
-  const lora_status_t st = cache_ok(cache, num_pages, page_size, kv_heads, head_dim);
+  const bool used = num_tokens > 0 && num_seqs > 0;
+  const lora_status_t st = cache_ok(used, cache, num_pages, page_size, kv_heads, head_dim);
   if (st == LORA_ERR_INVALID_ARGUMENT) return st;
-  if (num_seqs > 0 &&
+  if (used &&
       (!query_start || !seq_lens || !page_table ||
        ld_table < (static_cast<int64_t>(max_seq_len) + page_size - 1) / page_size))
     return LORA_ERR_INVALID_ARGUMENT;
   const int64_t width = static_cast<int64_t>(q_heads) * head_dim;
-  if (num_tokens > 0 && (!rows_ok(q, ldq, width) || !rows_ok(out, ldo, width)))
+  if (used && (!rows_ok(q, ldq, width) || !rows_ok(out, ldo, width)))
     return LORA_ERR_INVALID_ARGUMENT;
   if (st != LORA_OK) return st;
   if (static_cast<int64_t>(max_query_len) * (q_heads / kv_heads) > kMaxRows)
     return LORA_ERR_UNSUPPORTED;
+  if (!used) return LORA_OK;
   const int64_t need = lora_kv_attention_workspace_bytes(num_seqs, max_query_len, max_seq_len,
                                                          q_heads, kv_heads, head_dim);
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
     return LORA_ERR_INVALID_ARGUMENT;
-  if (num_tokens == 0 || num_seqs == 0) return LORA_OK;
   return launch_status(lora::launch_kv_attention(
       q, ldq, query_start, seq_lens, page_table, ld_table, cache, num_pages, page_shift(page_size),
       num_tokens, num_seqs, max_query_len, max_seq_len, q_heads, kv_heads, head_dim, scale, window,
