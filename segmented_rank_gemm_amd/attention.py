@@ -103,6 +103,15 @@ def _vector(t: torch.Tensor, dtype: torch.dtype, n: int, name: str) -> int:
     _refuse(t, dtype, (n,), name, "be contiguous")
 
 
+_MOST = 0x7FFFFFFF  # the library's sizes are 32-bit: ctypes would cut others down to that
+
+
+def _fit(**sizes: int) -> None:
+    for name, n in sizes.items():
+        if not -_MOST <= n <= _MOST:
+            raise ValueError(f"{name} {n} does not fit 32 bits")
+
+
 def _dims(t: torch.Tensor, n: int, name: str):
     shape = getattr(t, "shape", ())
     if len(shape) != n:
@@ -222,6 +231,8 @@ def lora_kv_read(slots: torch.Tensor, cache: torch.Tensor, k_out: Optional[torch
 
 def lora_kv_attention_workspace_bytes(num_seqs: int, max_query_len: int, max_seq_len: int,
                                       q_heads: int, kv_heads: int, head_dim: int) -> int:
+    _fit(num_seqs=num_seqs, max_query_len=max_query_len, max_seq_len=max_seq_len, q_heads=q_heads,
+         kv_heads=kv_heads, head_dim=head_dim)
     return int(lib().lora_kv_attention_workspace_bytes(num_seqs, max_query_len, max_seq_len, q_heads,
                                                        kv_heads, head_dim))
 
@@ -255,6 +266,8 @@ def lora_kv_attention(q: torch.Tensor, query_start: torch.Tensor, seq_lens: torc
     elif not 1 <= max_seq_len <= per_seq * page_size:
         raise ValueError(f"max_seq_len {max_seq_len} is not within the page table's "
                          f"{per_seq * page_size} tokens")
+    if not (-_MOST <= window <= _MOST and -_MOST <= max_query_len <= _MOST and max_seq_len <= _MOST):
+        _fit(window=window, max_query_len=max_query_len, max_seq_len=max_seq_len)
     wptr, wbytes = (0, 0) if workspace is None else _flat_dev_bytes(workspace, "workspace")
     status = _kv_attention(
         pq, ldq, _vector(query_start, _I32T, B + 1, "query_start"),

@@ -45,3 +45,14 @@ def test_calls_over_something_need_them():
     assert L.lora_kv_append(*{**APPEND, "num_pages": 0}.values()) == INVALID
     assert L.lora_kv_read(*{**READ, "cache": None}.values()) == INVALID
     assert L.lora_kv_attention(*{**ATTENTION, "cache": None}.values()) == INVALID
+
+
+@pytest.mark.parametrize("sizes", [((1 << 32) + 1, 1, 64, 4, 2, 128), (1, (1 << 32) + 1, 64, 4, 2, 128),
+                                   (1, 1, (1 << 32) + 64, 4, 2, 128), (1, 1, 1 << 31, 4, 2, 128),
+                                   (1, 1, -(1 << 32) + 64, 4, 2, 128), (1, 1, 64, (1 << 32) + 4, 2, 128)])
+def test_sizes_past_the_librarys_integers_are_refused(sizes):
+    """They would arrive as others: (1 << 32) + 64 tokens as 64."""
+    with pytest.raises(ValueError, match="32 bits"):
+        srg.lora_kv_attention_workspace_bytes(*sizes)
+    with pytest.raises(ValueError, match="32 bits"):
+        srg.kv_attention_workspace(*sizes)

@@ -168,3 +168,14 @@ def test_norm_codes_are_rounded_once(hidden, group):
     assert (R.f64(scales) == s).all()
     want, near = nearest_e4m3((v.reshape(256, -1, group) / s[..., None]).reshape(256, hidden))
     assert not ((R.f64(y8) != want) & (near > 2.0 ** -40)).any()
+
+
+@pytest.mark.parametrize("more", [dict(window=(1 << 32) + 5), dict(window=1 << 32), dict(window=5 - (1 << 32)),
+                                  dict(max_query_len=(1 << 32) + 1)])
+def test_attention_refuses_sizes_past_32_bits(more):
+    """A window of 2^32 + 5 would arrive as one of 5."""
+    c = Call(220, [40], [1], 4, 2, 64, 16)
+    call = dict(max_query_len=1, window=0)
+    with pytest.raises(ValueError, match="32 bits"):
+        srg.lora_kv_attention(c.q, *c.dev, c.cache, c.out, c.scale, c.workspace, **{**call, **more})
+    assert (c.out == 3).all()
