@@ -99,9 +99,11 @@ class Step:
                                         scale_b=layer.base_scales, out_dtype=torch.bfloat16))
         srg.lora_fused_step(self.adapter, self.tokens, self.y, layer.lora_a, layer.lora_b, 1.0, self.buf,
                             self.splits, self.qkv, self.meta, self.step_workspace)
-        srg.lora_kv_append(self.qkv, self.positions, self.slots, layer.rope, layer.cache, self.q)
+        srg.lora_kv_append(self.qkv, self.positions, self.slots, layer.rope, layer.cache, self.q,
+                           page_size=cfg.page)
         srg.lora_kv_attention(self.q, self.query_start, self.seq_lens, self.page_table, layer.cache, self.out,
-                              cfg.head_dim ** -0.5, self.attention_workspace, self.max_query_len)
+                              cfg.head_dim ** -0.5, self.attention_workspace, self.max_query_len,
+                              page_size=cfg.page)
 
     def place(self, before, counts, table, adapters) -> None:
         """Tokens of each sequence: counts[s] new ones behind before[s] cached ones."""

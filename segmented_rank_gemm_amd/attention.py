@@ -127,8 +127,10 @@ def kv_cache_shape(num_pages: int, kv_heads: int, head_dim: int, page_size: int)
     return (int(num_pages), 2, int(kv_heads), page_size * (head_dim // 2 + head_dim // 32))
 
 
-def _cache(cache: torch.Tensor, head_dim: int) -> Tuple[int, int, int, int]:
-    """Address, pages, kv_heads and page size of a cache for this head_dim."""
+def _cache(cache: torch.Tensor, head_dim: int, page_size: Optional[int]) -> Tuple[int, int, int, int]:
+    """Address, pages, kv_heads and page size of a cache for this head_dim.  The bytes
+    of a page are a product of the two: heads of 128 in pages of 64 tokens and heads
+    of 64 in pages of 128 have one shape, and only a caller's page_size tells them apart."""
     ptr = _dev_ptr(cache, _U8, "cache")
     shape = cache.shape
     if len(shape) != 4 or shape[1] != 2 or not cache.is_contiguous():
@@ -137,6 +139,9 @@ def _cache(cache: torch.Tensor, head_dim: int) -> Tuple[int, int, int, int]:
     row = head_dim // 2 + head_dim // 32  # bytes of one token's head
     if row < 1 or size % row:
         raise ValueError(f"cache pages of {size} bytes hold no heads of {head_dim}")
+    if page_size is not None and size != page_size * row:
+        raise ValueError(f"cache pages of {size} bytes hold {size // row} heads of {head_dim}, "
+                         f"not page_size {page_size}")
     return ptr, pages, heads, size // row
 
 
@@ -185,14 +190,16 @@ def lora_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float,
 
 def lora_kv_append(qkv: torch.Tensor, positions: Optional[torch.Tensor], slots: torch.Tensor,
                    rope: Optional[torch.Tensor], cache: torch.Tensor, q_out: torch.Tensor,
-                   interleaved: bool = False, stream: Optional[torch.cuda.Stream] = None) -> None:
+                   interleaved: bool = False, stream: Optional[torch.cuda.Stream] = None,
+                   page_size: Optional[int] = None) -> None:
     """qkv: bf16 [tokens, (q_heads + 2 kv_heads) * head_dim]; positions: int32
     [tokens]; slots: int64 [tokens]; rope: fp32 [rows, rot_dim] (rope_table), or
     None for no rotation; cache: uint8 (kv_cache_shape); q_out: bf16 [tokens,
-    q_heads, head_dim]."""
+    q_heads, head_dim]; page_size: the cache's, to be checked (here and below): without
+    it, it is what head_dim makes of the cache's shape, also where that is another's."""
     T, q_heads, head_dim = _dims(q_out, 3, "q_out")
     pq, ldq = _heads(q_out, T, q_heads, head_dim, "q_out")
-    pc, pages, kv_heads, page_size = _cache(cache, head_dim)
+    pc, pages, kv_heads, page_size = _cache(cache, head_dim, page_size)
     px, ldx = _matrix(qkv, _BF16, T, (q_heads + 2 * kv_heads) * head_dim, "qkv")
     rows = rot = pr = pp = 0
     if rope is not None:
@@ -209,14 +216,15 @@ def lora_kv_append(qkv: torch.Tensor, positions: Optional[torch.Tensor], slots: 
 
 
 def lora_kv_read(slots: torch.Tensor, cache: torch.Tensor, k_out: Optional[torch.Tensor],
-                 v_out: Optional[torch.Tensor], stream: Optional[torch.cuda.Stream] = None) -> None:
+                 v_out: Optional[torch.Tensor], stream: Optional[torch.cuda.Stream] = None,
+                 page_size: Optional[int] = None) -> None:
     """What the cache holds at slots (int64 [tokens]); k_out, v_out: bf16 [tokens,
     kv_heads, head_dim], one of them may be None."""
     like = k_out if k_out is not None else v_out
     if like is None:
         raise ValueError("lora_kv_read needs k_out or v_out")
     T, heads, head_dim = _dims(like, 3, "k_out and v_out")
-    pc, pages, kv_heads, page_size = _cache(cache, head_dim)
+    pc, pages, kv_heads, page_size = _cache(cache, head_dim, page_size)
     pk = ldk = pv = ldv = 0
     if k_out is not None:
         pk, ldk = _heads(k_out, T, kv_heads, head_dim, "k_out")
@@ -250,7 +258,8 @@ def lora_kv_attention(q: torch.Tensor, query_start: torch.Tensor, seq_lens: torc
                       page_table: torch.Tensor, cache: torch.Tensor, out: torch.Tensor,
                       scale: float, workspace: Optional[torch.Tensor], max_query_len: int,
                       window: int = 0, max_seq_len: Optional[int] = None,
-                      stream: Optional[torch.cuda.Stream] = None) -> None:
+                      stream: Optional[torch.cuda.Stream] = None,
+                      page_size: Optional[int] = None) -> None:
     """q, out: bf16 [tokens, q_heads, head_dim]; query_start: int32 [num_seqs + 1];
     seq_lens: int32 [num_seqs]; page_table: int32 [num_seqs, pages a sequence];
     max_seq_len: None: all that the page table can hold; workspace: of
@@ -258,7 +267,7 @@ def lora_kv_attention(q: torch.Tensor, query_start: torch.Tensor, seq_lens: torc
     T, q_heads, head_dim = _dims(q, 3, "q")
     pq, ldq = _heads(q, T, q_heads, head_dim, "q")
     po, ldo = _heads(out, T, q_heads, head_dim, "out")
-    pc, pages, kv_heads, page_size = _cache(cache, head_dim)
+    pc, pages, kv_heads, page_size = _cache(cache, head_dim, page_size)
     B, per_seq = _dims(page_table, 2, "page_table")
     pt, ldt = _matrix(page_table, _I32T, B, per_seq, "page_table")
     if max_seq_len is None:

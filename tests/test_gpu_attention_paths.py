@@ -179,3 +179,30 @@ def test_attention_refuses_sizes_past_32_bits(more):
     with pytest.raises(ValueError, match="32 bits"):
         srg.lora_kv_attention(c.q, *c.dev, c.cache, c.out, c.scale, c.workspace, **{**call, **more})
     assert (c.out == 3).all()
+
+
+def test_page_size_tells_caches_of_one_shape_apart():
+    """Heads of 128 in pages of 64 tokens, read as heads of 64 in pages of 128."""
+    shape = srg.kv_cache_shape(6, 2, 128, 64)
+    assert shape == srg.kv_cache_shape(6, 2, 64, 128)
+    cache = torch.zeros(shape, dtype=torch.uint8, device="cuda")
+    slots = torch.arange(3, device="cuda")
+    bf16 = dict(dtype=torch.bfloat16, device="cuda")
+    table, lens = torch.zeros(1, 3, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    for d in (128, 64):
+        q, k, v = torch.ones(3, 4, d, **bf16), torch.empty(3, 2, d, **bf16), torch.empty(3, 2, d, **bf16)
+        out = torch.full((1, 4, d), 3.0, **bf16)
+        calls = [lambda **more: srg.lora_kv_append(torch.ones(3, 8 * d, **bf16), None, slots, None, cache, q, **more),
+                 lambda **more: srg.lora_kv_read(slots, cache, k, v, **more),
+                 lambda **more: srg.lora_kv_attention(q[:1], start, lens, table, cache, out, 1.0, None, 1, **more)]
+        for call in calls:
+            if d == 128:
+                call(page_size=64), call()
+                for wrong in (128, 32, 0):
+                    with pytest.raises(ValueError, match="page_size"):
+                        call(page_size=wrong)
+            else:
+                with pytest.raises(ValueError, match="page_size 64"):
+                    call(page_size=64)
+        assert bool((out == (1 if d == 128 else 3)).all())
