@@ -343,13 +343,13 @@ __global__ __launch_bounds__(T) void rms_norm_kernel(NormArgs a) {
     emit_wide<T, C>(a, n, row, spare);
 }
 
-template <int T>
+// T threads a row, the first of C, More... that holds a thread's chunks.
+template <int T, int C, int... More>
 static void launch(const NormArgs& a, int chunks, int rows, hipStream_t stream) {
-  const dim3 grid(rows), block(T);
-  if (chunks <= 1) hipLaunchKernelGGL((rms_norm_kernel<T, 1>), grid, block, 0, stream, a);
-  else if (chunks <= 2) hipLaunchKernelGGL((rms_norm_kernel<T, 2>), grid, block, 0, stream, a);
-  else if (chunks <= 4) hipLaunchKernelGGL((rms_norm_kernel<T, 4>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((rms_norm_kernel<T, 8>), grid, block, 0, stream, a);
+  if constexpr (sizeof...(More) > 0) {
+    if (chunks > C) return launch<T, More...>(a, chunks, rows, stream);
+  }
+  hipLaunchKernelGGL((rms_norm_kernel<T, C>), dim3(rows), dim3(T), 0, stream, a);
 }
 
 hipError_t launch_rms_norm(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr,
@@ -363,10 +363,10 @@ hipError_t launch_rms_norm(const uint16_t* x, int64_t ldx, const uint16_t* resid
   // waves cost their launch (us, 64 / 256 / 512 / 1024 threads: 8192 rows of 512
   // 10.9 / 16.7 / 27.3 / 52.9; 2048 of 4096 - / 15.9 / 16.9 / 21.5; 16 of 8192
   // - / 6.5 / 5.1 / 5.2; 8192 of 8192 - / 116 / 111 / 117).
-  if (hidden <= 1024) launch<64>(a, (chunks + 63) / 64, num_tokens, stream);
-  else if (hidden <= 4096) launch<256>(a, (chunks + 255) / 256, num_tokens, stream);
-  else if (hidden <= 32768) launch<512>(a, (chunks + 511) / 512, num_tokens, stream);
-  else launch<1024>(a, (chunks + 1023) / 1024, num_tokens, stream);
+  if (hidden <= 1024) launch<64, 1, 2>(a, (chunks + 63) / 64, num_tokens, stream);
+  else if (hidden <= 4096) launch<256, 1, 2>(a, (chunks + 255) / 256, num_tokens, stream);
+  else if (hidden <= 32768) launch<512, 2, 4, 8>(a, (chunks + 511) / 512, num_tokens, stream);
+  else launch<1024, 8>(a, (chunks + 1023) / 1024, num_tokens, stream);
   return hipGetLastError();
 }
 

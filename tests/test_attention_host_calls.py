@@ -1,5 +1,8 @@
 """Host-side checks of the operators around the projections beside their refusals
-(no GPU needed): calls over nothing with no tensors at all."""
+(no GPU needed): calls over nothing with no tensors at all, sizes past the library's
+integers, and the norm's instances in the library."""
+
+import re
 
 import pytest
 
@@ -56,3 +59,16 @@ def test_sizes_past_the_librarys_integers_are_refused(sizes):
         srg.lora_kv_attention_workspace_bytes(*sizes)
     with pytest.raises(ValueError, match="32 bits"):
         srg.kv_attention_workspace(*sizes)
+
+
+def norm_instance(hidden):
+    """(threads a row, chunks of 8 elements a thread) for rows of this length."""
+    threads = next(t for most, t in ((1024, 64), (4096, 256), (32768, 512), (65536, 1024)) if hidden <= most)
+    each = -(-(hidden // 8) // threads)
+    return threads, 1 << (each - 1).bit_length()
+
+
+def test_every_norm_kernel_in_the_library_serves_some_length():
+    names = set(re.findall(rb"rms_norm_kernelILi(\d+)ELi(\d+)E", open(srg.LIB_PATH, "rb").read()))
+    held = {(int(t), int(c)) for t, c in names}
+    assert held == {norm_instance(h) for h in range(8, 65536 + 8, 8)}

@@ -1,5 +1,6 @@
 """The operators around the projections where numbers leave the ordinary range:
-normalised rows past bf16's and fp32's ends, against their 64-bit forms."""
+normalised rows past bf16's and fp32's ends, against their 64-bit forms; and where
+the launch changes with the length."""
 
 import numpy as np
 import pytest
@@ -7,7 +8,7 @@ import torch
 
 import segmented_rank_gemm_amd as srg
 from tests import attention_reference as R
-from tests.test_gpu_attention import nearest_e4m3
+from tests.test_gpu_attention import check_norm, nearest_e4m3, norm_case
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +72,13 @@ def test_rms_norm_of_products_below_the_normal_numbers(hidden, group):
     w[77] = 2.0 ** -120
     v, _ = check_rows(x, w, group)
     assert (np.abs(v) < 2.0 ** -118).mean() > 0.99 and (np.abs(v) > 2.0 ** -126).mean() > 0.3
+
+
+@pytest.mark.parametrize("hidden", [504, 512, 520, 1024, 1032, 2048, 2056, 4096, 4104, 8192, 8200, 16384, 16392, 32768,
+                                    32776])
+def test_rms_norm_where_the_threads_and_their_chunks_change(hidden):
+    x, w, r = norm_case(np.random.default_rng(hidden), 3, hidden, True)
+    sums, y = torch.empty_like(x), torch.empty_like(x)
+    y8, scales = torch.empty(3, hidden, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(3, 1, device="cuda")
+    srg.lora_rms_norm(x, w, 1e-5, residual=r, residual_out=sums, y=y, y8=y8, scales=scales)
+    check_norm(x, w, r, 1e-5, hidden, sums, y, y8, scales)
