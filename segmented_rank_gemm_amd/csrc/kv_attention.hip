@@ -1047,8 +1047,9 @@ hipError_t launch_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* qu
                      fabsf(scale) * 1.44269504f, scale < 0.f ? 0x80008000u : 0u,
                      group, ((1 << 21) + group - 1) / group,
                      p.row_tiles, p.parts, p.part_chunks, p.tile_rows, nullptr, nullptr};
-  // scores of zero times a hidden token's -infinity must stay -infinity
+  // a hidden token's -infinity must stay -infinity, and a score of zero stay zero
   if (a.scale_log2 < 1.17549435e-38f) a.scale_log2 = 1.17549435e-38f;
+  if (a.scale_log2 > 3.402823466e38f) a.scale_log2 = 3.402823466e38f;
   if (p.parts > 1) {
     a.stats = static_cast<float*>(workspace);
     a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + stats_bytes(p));

@@ -8,7 +8,7 @@ import torch
 
 import segmented_rank_gemm_amd as srg
 from tests import attention_reference as R
-from tests.test_gpu_attention import check_norm, nearest_e4m3, norm_case
+from tests.test_gpu_attention import Call, check_norm, nearest_e4m3, norm_case
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +82,16 @@ def test_rms_norm_where_the_threads_and_their_chunks_change(hidden):
     y8, scales = torch.empty(3, hidden, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(3, 1, device="cuda")
     srg.lora_rms_norm(x, w, 1e-5, residual=r, residual_out=sums, y=y, y8=y8, scales=scales)
     check_norm(x, w, r, 1e-5, hidden, sums, y, y8, scales)
+
+
+# ------------------------------------------------------------------ attention
+@pytest.mark.parametrize("scale", [3e38, -3.4e38, 2e38])
+def test_attention_scales_near_the_largest_number(scale):
+    """Scores of zero stay zero whatever the scale: every query takes the mean of the
+    tokens that it sees."""
+    c = Call(19, [90, 200], [3, 40], 4, 2, 64, 16, 50)
+    c.qh = torch.zeros_like(c.qh)
+    c.q.zero_()
+    c.scale = scale
+    c.run()
+    c.check()
