@@ -59,7 +59,8 @@ extern "C" {
  *   x, residual  bf16 [num_tokens][ldx], [ldr]; residual may be NULL.
  *   weight       bf16 [hidden].
  *   eps          >= 0, finite.
- *   hidden       multiple of 8, 8 <= hidden <= 65536.
+ *   hidden       multiple of 8, 8 <= hidden <= 65536; above 32768, num_tokens is
+ *                less than 2^22 (LORA_ERR_UNSUPPORTED otherwise).
  *   residual_out bf16 [num_tokens][ldo]: h; may be NULL; needs a residual.  May be
  *                x or residual itself (same address and stride).
  *   y            bf16 [num_tokens][ldy]; may be NULL; may be x itself.

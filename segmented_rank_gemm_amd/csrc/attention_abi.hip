@@ -34,8 +34,9 @@ hipError_t launch_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* qu
 
 namespace {
 
-constexpr int32_t kMaxTokens = 1 << 22;  // times 1024 threads: a grid dimension
+constexpr int32_t kMaxTokens = 1 << 22;  // times up to 512 threads: a grid dimension
 constexpr int32_t kMaxHidden = 65536;
+constexpr int32_t kHidden512 = 32768;    // longer rows take 1024 threads
 constexpr int32_t kMaxHeads = 1024;
 constexpr int32_t kMaxSeqs = 65535;     // a grid dimension
 constexpr int64_t kMaxRows = 1 << 22;   // queries times heads a key head, of one sequence
@@ -99,6 +100,7 @@ lora_status_t lora_rms_norm(const uint16_t* x, int64_t ldx, const uint16_t* resi
   }
   if (y8 && group != hidden && group != 32 && group != 64 && group != 128 && group != 256)
     return LORA_ERR_UNSUPPORTED;
+  if (num_tokens == kMaxTokens && hidden > kHidden512) return LORA_ERR_UNSUPPORTED;
   if (num_tokens == 0) return LORA_OK;
   return launch_status(lora::launch_rms_norm(x, ldx, residual, ldr, weight, eps, num_tokens, hidden,
                                              residual_out, ldo, y, ldy, y8, ldy8, scales,

@@ -72,3 +72,9 @@ def test_every_norm_kernel_in_the_library_serves_some_length():
     names = set(re.findall(rb"rms_norm_kernelILi(\d+)ELi(\d+)E", open(srg.LIB_PATH, "rb").read()))
     held = {(int(t), int(c)) for t, c in names}
     assert held == {norm_instance(h) for h in range(8, 65536 + 8, 8)}
+
+
+def test_rms_norm_refuses_the_one_grid_that_cannot_be_launched():
+    """2^22 rows of 1024 threads: 2^32, one more than a grid dimension holds."""
+    wide = dict(hidden=32776, ldx=32776, ldr=32776, ldo=32776, ldy=32776, ldy8=32776, group=32776)
+    assert srg.lib().lora_rms_norm(*{**NORM, **wide, "num_tokens": 1 << 22}.values()) == UNSUPPORTED
