@@ -287,7 +287,7 @@ __global__ __launch_bounds__(T) void rms_norm_kernel(NormArgs a) {
     if (a.residual) res[c] = load16(a.residual + row * a.ldr + 8 * i);
   }
   double sum = 0.0;
-  uint32_t top_bits = 0;  // of the largest |h w|: integer order, infinity and NaN on top
+  float top = 0.f;  // the largest |h w|, NaN if one is
   bool subnormal = false;  // some h w has lost bits
 #pragma unroll
   for (int c = 0; c < C; ++c) {
@@ -307,11 +307,12 @@ __global__ __launch_bounds__(T) void rms_norm_kernel(NormArgs a) {
       const double e64 = e;
       sum = fma(e64, e64, sum);
       const float p = e * bf16_at(w, k);
-      top_bits = max(top_bits, __float_as_uint(p) & 0x7FFFFFFFu);
+      top = __builtin_elementwise_maximum(top, fabsf(p));
       subnormal |= __builtin_amdgcn_classf(p, kSubnormal);
     }
   }
-  if (subnormal) top_bits = kInfinity;
+  // its bits: integer order, infinity and NaN on top
+  uint32_t top_bits = subnormal ? kInfinity : __float_as_uint(top) & 0x7FFFFFFFu;
   __shared__ double part_sum[(T / kWave)];
   __shared__ uint32_t part_top[(T / kWave)];
   __shared__ double spare[(T / kWave)];
