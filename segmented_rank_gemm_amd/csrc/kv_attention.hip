@@ -20,14 +20,15 @@
 // are rounded to bf16 for the second product, as the matrix unit takes them, and it
 // is the rounded ones that are summed: what the values are divided by is what they
 // were multiplied by, so that equal values come back as they are (sums of the
-// unrounded ones were off by up to 2^-8 of the result where few tokens are seen; 283
-// against 294 us for the prompts below, the same for single queries).
+// unrounded ones were off by up to 2^-8 of the result where few tokens are seen; 282
+// against 293 us for prompts in pieces, the same for single queries).
 //
 // Bound by: HBM (136 bytes a token and key head at D = 128) as long as the rows of
-// a key head fit one tile (4.5 TB/s at 64 sequences of up to 8192 tokens, where a
-// copy reaches 4.9); for prompts by the vector unit beside the matrix unit (1050
-// TFLOP/s at 8 sequences of 2048 queries over 8192 tokens, where a library product
-// reaches 1340), which one wave uses in turn.
+// a key head fit one tile (4.8 TB/s at 64 sequences of up to 8192 tokens, where this
+// library's copy reaches 5.5); for prompts by the vector unit beside the matrix unit,
+// which one wave uses in turn (1015 TFLOP/s at 8 sequences of 2048 queries over 8192
+// tokens, where a library product reaches 1335; for prompts in pieces vector
+// instructions take 55% of the cycles, the matrix unit 33%, shared memory 27%).
 
 #include "kv_format.hpp"
 
@@ -366,7 +367,8 @@ struct RowOf {
   int query, head;
 };
 __device__ __forceinline__ RowOf row_of(const AttentionArgs& a, int query0, int head0, int row) {
-  // row + head0 < group + 64: the product is exact enough for a division
+  // head0 + row < group + 128 <= 1152 and the inverse is at most 2^-21 too large, so the
+  // product is off by less than 1152 / 2^21 < 1 / group: the quotient is right
   const int n = head0 + row;
   const int q = static_cast<int>(static_cast<uint32_t>(n * a.group_inverse) >> 21);
   return RowOf{query0 + q, n - q * a.group};
@@ -426,10 +428,10 @@ __device__ __forceinline__ int64_t unit_of(const AttentionArgs& a, int seq, int 
 // that short ones fill the gaps at the end.  A compute unit holds two workgroups;
 // where a launch has no more than that, nothing is left for gaps, and those that
 // come second to their unit go shortest first, each beside a long one (64
-// sequences of 17 to 8192 tokens, 8 key heads: as they come 105 us, longest first
-// 72, this 64; the last two with the loop's present loads).  Every wave ranks the
-// sequences for itself; with more of them than lanes, many workgroups a compute
-// unit even the work out and they are taken as they come.
+// sequences of 17 to 8192 tokens, 8 key heads: as they come 73 us, longest first
+// 69, this 62).  Every wave ranks the sequences for itself; with more of them than
+// lanes, many workgroups a compute unit even the work out and they are taken as they
+// come.
 __device__ __forceinline__ int sequence_at(const AttentionArgs& a, int index) {
   const int n = static_cast<int>(gridDim.z);
   if (n == 1 || n > kWave) return index;
@@ -806,8 +808,8 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel
       uint32_t weights[MT][8];
       // The matrix products of one row tile beside the powers of the other, for
       // which keys and values are read from shared memory once a tile (8 sequences
-      // of up to 4608 tokens in pieces: 293 -> 284 us; told to interleave them in
-      // fixed patterns the compiler did worse, 297 to 333).
+      // of up to 4608 tokens in pieces: 3% less time; told to interleave them in
+      // fixed patterns the compiler did worse, by 5 to 17%).
       auto scores = [&](int mt, int i) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -959,8 +961,8 @@ static AttentionPlan attention_plan(int num_seqs, int max_query_len, int64_t max
   // Workgroups of the rows kernel; with fewer than fill the device twice over
   // (their registers), cutting the tokens up as well gains more than sharing the
   // operands (us, split / rows: 1 sequence of 128 queries of 4096 tokens, 8 key
-  // heads of 8, 64 workgroups 44 / 121; 512 queries, 256: 114 / 124; 2048 of 2048,
-  // 1024: 148 / 101).
+  // heads of 8, 64 workgroups 37 / 106; 512 queries, 256: 90 / 108; 8 sequences of
+  // 128, 512: 176 / 155; 2048 of 2048, 1024: 130 / 94).
   const int64_t wide = (rows + kRowWaves * kRowTiles * kTile - 1) / (kRowWaves * kRowTiles * kTile);
   p.many = rows >= kManyRows && wide * num_seqs * kv_heads >= 2 * kCus;
   p.tile_rows = p.many ? kRowWaves * kRowTiles * kTile : mt * kTile;
@@ -972,8 +974,8 @@ static AttentionPlan attention_plan(int num_seqs, int max_query_len, int64_t max
   p.part_chunks = static_cast<int>(chunks);
   if (p.many) return p;
   // About a workgroup a CU (131072 tokens, 8 key heads, one row tile: 256
-  // workgroups 39 us, 1024 45, 2048 58); two for two row tiles where a part is
-  // still many rounds of the waves (128 queries of 32768 tokens 274 -> 216 us).
+  // workgroups 37 us, 1024 42, 2048 56); two for two row tiles where a part is
+  // still many rounds of the waves (128 queries of 32768 tokens 201 -> 174 us).
   // A part is whole rounds of the waves.
   const int waves = split_waves(mt);
   const int64_t most = (chunks + waves - 1) / waves;
@@ -981,7 +983,7 @@ static AttentionPlan attention_plan(int num_seqs, int max_query_len, int64_t max
   if (mt == 2 && most >= 16 * p.most_parts) p.most_parts = (2 * kCus + p.units - 1) / p.units;
   p.most_parts = p.most_parts < most ? p.most_parts : most;
   // One round less is not worth the launch that joins the parts (1000 tokens, 8
-  // key heads: 2 rounds 10.1 us, 2 parts of 1 round 10.7; 2000: 13.5 and 10.9).
+  // key heads: 2 rounds 9.8 us, 2 parts of 1 round 10.3; 600: 8.6 and 9.7).
   if (most - (most + p.most_parts - 1) / p.most_parts < 2) p.most_parts = 1;
   const int64_t rounds = (most + p.most_parts - 1) / p.most_parts;
   p.part_chunks = static_cast<int>(rounds * waves);

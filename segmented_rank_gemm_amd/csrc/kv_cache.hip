@@ -5,9 +5,9 @@
 // neighbouring lanes share a 32-element block and its scale byte.
 //
 // Bound by: HBM and, for the rotation, the 64-bit conversions beside it (4096
-// tokens of 32 and 32 heads of 128: append 40 us, 3.8 TB/s, read 18 us, 4.6 TB/s,
-// where a copy reaches 4.9; 64 tokens of 64 and 8 heads 3.4 and 2.6 us, of which
-// an empty launch is about 2).
+// tokens of 32 and 32 heads of 128: append 39 us, 3.9 TB/s, read 18 us, 4.7 TB/s,
+// where this library's copy reaches 5.5; 64 tokens of 64 and 8 heads 2.9 and 2.0 us,
+// of which an empty launch is 1.9).
 
 #include "kv_format.hpp"
 
@@ -189,7 +189,7 @@ __global__ __launch_bounds__(kKvThreads) void kv_read_kernel(const int64_t* slot
 
 // Workgroups a token: one where the tokens alone fill the device, up to one
 // pass over a token's items where they do not (1 token of 32 and 32 heads: append
-// 5.5 -> 3.5 us, read 3.3 -> 2.7).
+// 4.5 -> 2.4 us, read 2.6 -> 1.9).
 static int groups_of(int num_tokens, int items) {
   const int most = (items + kKvThreads - 1) / kKvThreads;
   const int want = (2 * kCus + num_tokens - 1) / num_tokens;
