@@ -461,3 +461,8 @@ from . import attention as _attention  # noqa: E402  (needs the helpers above)
 from .attention import *  # noqa: E402,F401,F403
 
 __all__ += _attention.__all__
+
+from . import cache as _cache_ops  # noqa: E402
+from .cache import *  # noqa: E402,F401,F403
+
+__all__ += _cache_ops.__all__

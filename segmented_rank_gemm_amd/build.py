@@ -22,7 +22,8 @@ ARCH = "gfx950"
 
 SOURCES = ["lora_abi.hip", "metadata.hip", "metadata_grouped.hip", "shrink.hip", "expand.hip",
            "token_step.hip", "attention_abi.hip", "rms_norm.hip", "kv_cache.hip",
-           "kv_attention.hip"]
+           "kv_attention.hip", "cache_abi.hip", "draft_masks.hip", "kv_mass.hip", "kv_select.hip",
+           "kv_compact.hip"]
 MEASURE_SOURCES = ["stream_copy.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -2,11 +2,7 @@
 // argument checks, then the launch on the caller's stream.  No call allocates,
 // synchronises or keeps state.
 
-#include <hip/hip_runtime.h>
-#include <math.h>
-#include <stdint.h>
-
-#include "lora_attention.h"
+#include "cache_checks.hpp"
 
 namespace lora {
 hipError_t launch_rms_norm(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr,
@@ -23,57 +19,14 @@ hipError_t launch_kv_read(const int64_t* slots, int num_tokens, int kv_heads, in
                           int64_t ldk, uint16_t* v_out, int64_t ldv, hipStream_t stream);
 int64_t kv_attention_workspace_bytes(int num_seqs, int max_query_len, int max_seq_len, int q_heads,
                                      int kv_heads, int head_dim);
-hipError_t launch_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* query_start,
-                               const int32_t* seq_lens, const int32_t* page_table,
-                               int64_t ld_table, const uint8_t* cache, int num_pages,
-                               int page_shift, int num_tokens, int num_seqs, int max_query_len,
-                               int max_seq_len, int q_heads, int kv_heads, int head_dim,
-                               float scale, int window, uint16_t* out, int64_t ldo,
-                               void* workspace, hipStream_t stream);
 }  // namespace lora
+
+using namespace lora;
 
 namespace {
 
-constexpr int32_t kMaxTokens = 1 << 22;  // times up to 512 threads: a grid dimension
 constexpr int32_t kMaxHidden = 65536;
 constexpr int32_t kHidden512 = 32768;    // longer rows take 1024 threads
-constexpr int32_t kMaxHeads = 1024;
-constexpr int32_t kMaxSeqs = 65535;     // a grid dimension
-constexpr int64_t kMaxRows = 1 << 22;   // queries times heads a key head, of one sequence
-constexpr int32_t kMaxSeqLen = 1 << 30;
-
-bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-
-// A bf16 matrix of rows of `width` elements.
-bool rows_ok(const void* p, int64_t ld, int64_t width) {
-  return p && aligned(p, 16) && ld >= width && ld % 8 == 0;
-}
-
-// log2 of a page size, or -1 where the library does not have it.
-int32_t page_shift(int32_t page_size) {
-  for (int32_t s = 4; s <= 8; ++s)
-    if (page_size == 1 << s) return s;
-  return -1;
-}
-
-// used: the call reads or writes the cache; its address is not looked at otherwise.
-lora_status_t cache_ok(bool used, const uint8_t* cache, int32_t num_pages, int32_t page_size,
-                       int32_t kv_heads, int32_t head_dim) {
-  if (num_pages < 0 || page_size < 1 || kv_heads < 1 || kv_heads > kMaxHeads || head_dim < 1)
-    return LORA_ERR_INVALID_ARGUMENT;
-  if (used && (!cache || !aligned(cache, 16) || num_pages < 1)) return LORA_ERR_INVALID_ARGUMENT;
-  if (page_shift(page_size) < 0 || (head_dim != 64 && head_dim != 128)) return LORA_ERR_UNSUPPORTED;
-  return LORA_OK;
-}
-
-lora_status_t launch_status(hipError_t e) { return e == hipSuccess ? LORA_OK : LORA_ERR_LAUNCH; }
-
-bool attention_sizes_ok(int32_t num_seqs, int32_t max_query_len, int32_t max_seq_len,
-                        int32_t q_heads, int32_t kv_heads) {
-  return num_seqs >= 0 && num_seqs <= kMaxSeqs && max_query_len >= 1 &&
-         max_query_len <= kMaxTokens && max_seq_len >= 1 && max_seq_len <= kMaxSeqLen &&
-         kv_heads >= 1 && q_heads >= kv_heads && q_heads <= kMaxHeads && q_heads % kv_heads == 0;
-}
 
 }  // namespace
 
@@ -195,7 +148,7 @@ lora_status_t lora_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* q
   return launch_status(lora::launch_kv_attention(
       q, ldq, query_start, seq_lens, page_table, ld_table, cache, num_pages, page_shift(page_size),
       num_tokens, num_seqs, max_query_len, max_seq_len, q_heads, kv_heads, head_dim, scale, window,
-      out, ldo, workspace, stream));
+      nullptr, 0, out, ldo, nullptr, 0, workspace, stream));
 }
 
 }  // extern "C"

@@ -30,12 +30,10 @@
 // tokens, where a library product reaches 1335; for prompts in pieces vector
 // instructions take 55% of the cycles, the matrix unit 33%, shared memory 27%).
 
-#include "kv_format.hpp"
+#include "kv_attention.hpp"
 
 namespace lora {
 
-constexpr int kChunk = 64;       // tokens of a wave's step
-constexpr int kTile = 16;        // rows of one matrix product
 // Waves that share out the tokens of a tile of mt * 16 rows.  Two workgroups fit
 // a compute unit: four waves a SIMD at 128 registers, or two at 256.
 __host__ __device__ constexpr int split_waves(int mt) { return mt == 1 ? 8 : 4; }
@@ -48,148 +46,60 @@ constexpr float kNoScore = -3.402823466e38f;  // the running maximum before any 
 // two; weights up to 2^8 lose nothing in fp32 sums or bf16 mantissas.
 constexpr float kMaxLag = 8.f;
 
-struct AttentionArgs {
-  const uint16_t* q;
-  const int32_t* query_start;
-  const int32_t* seq_lens;
-  const int32_t* page_table;
-  uint16_t* out;
-  Cache<const uint8_t> cache;
-  int64_t ldq, ldo, ld_table;
-  int num_tokens, max_query_len, max_seq_len, q_heads, window;
-  float scale_log2;   // |scale| * log2(e): the softmax runs in powers of two
-  uint32_t sign;      // scale's sign bits, for q (two bf16)
-  int group;          // query heads a key head
-  int group_inverse;  // ceil(2^21 / group)
-  int row_tiles;      // of 16 * MT rows, for one sequence and key head
-  int parts;          // of one row tile's tokens
-  int part_chunks;
-  int tile_rows;      // 16 * MT
-  // Of parts, by (sequence, row tile, key head), part, row of the tile: the
-  // maximum and the sum, and the outputs relative to that maximum.
-  float* stats;       // [..][2]
-  float* partial;     // [..][D]
-};
-
-__device__ __forceinline__ uint32_t byte_scale(uint32_t w, int j) {
-  // byte j of w as the exponent of a float
-  const uint32_t s = j == 0 ? w << 23 : (j == 1 ? w << 15 : (j == 2 ? w << 7 : w >> 1));
-  return s & 0x7F800000u;
-}
-
-__device__ __forceinline__ bf16x8 as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  const u32x4 v = {a, b, c, d};
-  return __builtin_bit_cast(bf16x8, v);
-}
-
-__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-
-// A lane's part of a chunk's keys: of tokens 4 c + j, the g-th quarter of the head.
-template <int D>
-struct Keys {
-  uint32_t w[4][D / 32];
-  uint32_t scales;  // of the four tokens
-};
-
-// A lane's part of a chunk's values: of tokens 16 g + k, elements from c * D / 16.
-struct Values {
-  uint32_t w[16];
-  u32x4 scales;  // of the sixteen tokens
-};
-
-struct Pages {
-  int k, v;  // of this lane's keys and values; -1: no such page
-};
-
-// One sequence's cache from one key head's point of view.
-template <int D>
-struct Reader {
-  const uint8_t* keys;
-  const uint8_t* values;
-  const int32_t* table;
-  int64_t page_stride;
-  int shift, num_pages, max_seq_len;
-
-  __device__ __forceinline__ int page_at(int token) const {
-    const bool there = token < max_seq_len;
-    const int p = table[(there ? token : max_seq_len - 1) >> shift];
-    return there && p >= 0 && p < num_pages ? p : -1;
-  }
-  __device__ __forceinline__ Pages pages(int base) const {
-    const int lane = lane_id();
-    return Pages{page_at(base + 16 * ((lane & 15) >> 2)), page_at(base + 16 * (lane >> 4))};
-  }
-  // A page that does not exist reads as page 0, which does, and is masked.
-  __device__ __forceinline__ void load(Keys<D>& k, Pages p, int base) const {
-    const int lane = lane_id(), g = lane >> 4;
-    const int at = (base + 4 * (lane & 15)) & ((1 << shift) - 1);
-    const uint8_t* b = keys + (p.k < 0 ? 0 : p.k) * page_stride;
-    const uint8_t* row = b + at * (D / 2) + g * (D / 8);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (D == 128) {
-        const u32x4 w = load16(row + j * (D / 2));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) k.w[j][i] = w[i];
-      } else {
-        const u32x2 w = load8(row + j * (D / 2));
-        k.w[j][0] = w[0];
-        k.w[j][1] = w[1];
-      }
-    }
-    k.scales = *(const LORA_GLOBAL uint32_t*)(b + (((D / 2) + g * (D / 4) / kBlock) << shift) + at);
-  }
-  __device__ __forceinline__ void load(Values& v, Pages p, int base) const {
-    const int lane = lane_id(), c = lane & 15;
-    const int at = (base + 16 * (lane >> 4)) & ((1 << shift) - 1);
-    const uint8_t* b = values + (p.v < 0 ? 0 : p.v) * page_stride;
-    const uint8_t* row = b + at * (D / 2) + c * (D / 32);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      if constexpr (D == 128) v.w[k] = *(const LORA_GLOBAL uint32_t*)(row + k * (D / 2));
-      else v.w[k] = *(const LORA_GLOBAL uint16_t*)(row + k * (D / 2));
-    }
-    v.scales = load16(b + (((D / 2) + c * (D / 16) / kBlock) << shift) + at);
-  }
-};
-
 // The rows of one wave: MT tiles of 16.
-template <int D, int MT>
+template <int D, int MT, int V>
 struct Rows {
   f32x4 acc[MT][D / 16];
   float top[MT], sum[MT];
   int place[MT];  // of row c of the tile: the last token that it sees
 };
-
-// Where a chunk stands: which of its tokens are there at all.
-struct Span {
-  int base;           // the chunk's first token
-  int first, last;    // tokens [first, last) are seen by some row
-  int window;
-  bool masked;        // some row does not see all 64, or a page is missing
-  bool several;       // the rows are more than one query's
-  bool ok;            // the page of this lane's 16 values (and scores) exists
+// Where sums of exponentials are asked for, those of the unrounded ones too: the
+// logarithm of the rounded ones' would be off by up to 2^-8.
+template <int D, int MT>
+struct SumRows {
+  f32x4 acc[MT][D / 16];
+  float top[MT], sum[MT], full[MT];
+  int place[MT];
+};
+template <int D, int MT>
+struct Rows<D, MT, kSums> : SumRows<D, MT> {};
+template <int D, int MT>
+struct Rows<D, MT, kTree> : SumRows<D, MT> {
+  const Draft* drafts[MT];  // of row c of the tile: what it sees
+  int before;
 };
 
-// Which of this lane's 16 tokens (base + 16 g + k, bit k) a row at `place` sees.
-__device__ __forceinline__ uint32_t seen_bits(const Span& at, int place) {
-  const int token = at.base + 16 * (lane_id() >> 4);
-  int hi = place - token, lo = at.window ? hi - at.window + 1 : 0;  // lo..hi of 0..15
-  hi = hi < 15 ? hi : 15;
-  lo = lo > 0 ? lo : 0;
-  return at.ok && hi >= lo ? ((2u << hi) - 1u) & ~((1u << lo) - 1u) : 0u;
+template <int D, int MT, int V>
+__device__ __forceinline__ uint32_t seen_by(const Rows<D, MT, V>& r, int mt, const Span& at) {
+  if constexpr (V == kTree) return seen_bits(at, *r.drafts[mt], r.before);
+  else return seen_bits(at, r.place[mt]);
+}
+
+// Row c of tile mt: what it sees, and nothing summed up yet.
+template <int D, int MT, int V>
+__device__ __forceinline__ void begin(Rows<D, MT, V>& r, int mt, const RowTile& t, int query,
+                                      const Draft* drafts) {
+  if constexpr (V == kTree) {
+    r.drafts[mt] = drafts + (query - t.query0);
+    r.before = t.before;
+  } else {
+    r.place[mt] = t.before + query;
+  }
+  r.top[mt] = kNoScore;
+  r.sum[mt] = 0.f;
+  if constexpr (V != kPlain) r.full[mt] = 0.f;
+#pragma unroll
+  for (int n = 0; n < D / 16; ++n) r.acc[mt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 }
 
 // The first half of the running softmax over one chunk's scores of row tile mt,
 // s[j][i] of token 16 g + 4 i + j: hides what a row does not see and moves the
 // running maximum.
-template <int D, int MT>
-__device__ __forceinline__ void raise(Rows<D, MT>& r, int mt, f32x4 (&s)[4], const Span& at,
+template <int D, int MT, int V>
+__device__ __forceinline__ void raise(Rows<D, MT, V>& r, int mt, f32x4 (&s)[4], const Span& at,
                                       float scale_log2) {
   if (at.masked) {
-    const uint32_t seen = seen_bits(at, r.place[mt]);
+    const uint32_t seen = seen_by(r, mt, at);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -209,6 +119,7 @@ __device__ __forceinline__ void raise(Rows<D, MT>& r, int mt, f32x4 (&s)[4], con
     const float shrink = __builtin_amdgcn_exp2f(r.top[mt] - now);
     r.top[mt] = now;
     r.sum[mt] *= shrink;
+    if constexpr (V != kPlain) r.full[mt] *= shrink;
 #pragma unroll
     for (int n = 0; n < D / 16; ++n)
 #pragma unroll
@@ -218,21 +129,23 @@ __device__ __forceinline__ void raise(Rows<D, MT>& r, int mt, f32x4 (&s)[4], con
 
 // The second half, a quarter of it: the weights of the tokens 16 g + 4 i + j, in
 // bf16 (pairs of tokens 16 g + 2 i, + 1), and the sum of what they were rounded to.
-__device__ __forceinline__ void powers(uint32_t (&weights)[8], float& sum, const f32x4 (&s)[4], int i,
-                                       float top, float scale_log2) {
+template <int D, int MT, int V>
+__device__ __forceinline__ void powers(uint32_t (&weights)[8], Rows<D, MT, V>& r, int mt,
+                                       const f32x4 (&s)[4], int i, float scale_log2) {
   float p[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) p[j] = __builtin_amdgcn_exp2f(fmaf(s[j][i], scale_log2, -top));
+  for (int j = 0; j < 4; ++j) p[j] = __builtin_amdgcn_exp2f(fmaf(s[j][i], scale_log2, -r.top[mt]));
   const uint32_t a = pack_bf16x2(p[0], p[1]), b = pack_bf16x2(p[2], p[3]);
-  sum += (bf16_lo(a) + bf16_hi(a)) + (bf16_lo(b) + bf16_hi(b));
+  r.sum[mt] += (bf16_lo(a) + bf16_hi(a)) + (bf16_lo(b) + bf16_hi(b));
+  if constexpr (V != kPlain) r.full[mt] += (p[0] + p[1]) + (p[2] + p[3]);
   weights[2 * i] = a;
   weights[2 * i + 1] = b;
 }
 
 // Scores of one chunk and their weights.  q: the operand [mt][D / 32][lane] in
 // shared memory.
-template <int D, int MT>
-__device__ __forceinline__ void weigh(Rows<D, MT>& r, uint32_t (&weights)[MT][8], const Keys<D>& k,
+template <int D, int MT, int V>
+__device__ __forceinline__ void weigh(Rows<D, MT, V>& r, uint32_t (&weights)[MT][8], const Keys<D>& k,
                                       const u32x4* q, const Span& at, float scale_log2) {
   f32x4 s[MT][4];
 #pragma unroll
@@ -254,21 +167,21 @@ __device__ __forceinline__ void weigh(Rows<D, MT>& r, uint32_t (&weights)[MT][8]
   }
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    raise<D, MT>(r, mt, s[mt], at, scale_log2);
+    raise(r, mt, s[mt], at, scale_log2);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) powers(weights[mt], r.sum[mt], s[mt], i, r.top[mt], scale_log2);
+    for (int i = 0; i < 4; ++i) powers(weights[mt], r, mt, s[mt], i, scale_log2);
   }
 }
 
 // Bits `nan` of this lane's 16 tokens: value blocks that held a NaN and were
 // taken out.  Marks the outputs that they reach: those for which the sum over
 // these tokens of "seen" is not zero.
-template <int D, int MT>
-__device__ __forceinline__ void mark_nan(Rows<D, MT>& r, uint32_t nan, const Span& at) {
+template <int D, int MT, int V>
+__device__ __forceinline__ void mark_nan(Rows<D, MT, V>& r, uint32_t nan, const Span& at) {
   if (!__any(nan != 0)) return;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    const uint32_t seen = seen_bits(at, r.place[mt]);
+    const uint32_t seen = seen_by(r, mt, at);
     f32x4 hit = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -294,8 +207,8 @@ __device__ __forceinline__ void mark_nan(Rows<D, MT>& r, uint32_t nan, const Spa
 // Values that no row sees may be anything: their weights are zero, and their
 // scales are made so.  A NaN block that some rows see and others do not is
 // taken out too (mark_nan).
-template <int D, int MT>
-__device__ __forceinline__ void mask_values(Rows<D, MT>& r, u32x4& scales, const Span& at) {
+template <int D, int MT, int V>
+__device__ __forceinline__ void mask_values(Rows<D, MT, V>& r, u32x4& scales, const Span& at) {
   uint32_t nan = 0;
   const int token = at.base + 16 * (lane_id() >> 4);
 #pragma unroll
@@ -306,12 +219,12 @@ __device__ __forceinline__ void mask_values(Rows<D, MT>& r, u32x4& scales, const
     if (bad && !none) nan |= 1u << k;
     if (bad || none) scales[k >> 2] &= ~byte;
   }
-  mark_nan<D, MT>(r, nan, at);
+  mark_nan(r, nan, at);
 }
 
 // The weighted values of one chunk.
-template <int D, int MT>
-__device__ __forceinline__ void add_values(Rows<D, MT>& r, const uint32_t (&weights)[MT][8],
+template <int D, int MT, int V>
+__device__ __forceinline__ void add_values(Rows<D, MT, V>& r, const uint32_t (&weights)[MT][8],
                                            const Values& v, const u32x4 scales) {
   // D / 32 elements of the lane at a time: their operands are D / 8 registers
   constexpr int kPairs = D / 64;  // words of two elements
@@ -362,58 +275,6 @@ __device__ __forceinline__ void add_values(Rows<D, MT>& r, const uint32_t (&weig
   }
 }
 
-// Row `row` of a tile whose first row is head `head0` of query `query0`.
-struct RowOf {
-  int query, head;
-};
-__device__ __forceinline__ RowOf row_of(const AttentionArgs& a, int query0, int head0, int row) {
-  // head0 + row < group + 128 <= 1152 and the inverse is at most 2^-21 too large, so the
-  // product is off by less than 1152 / 2^21 < 1 / group: the quotient is right
-  const int n = head0 + row;
-  const int q = static_cast<int>(static_cast<uint32_t>(n * a.group_inverse) >> 21);
-  return RowOf{query0 + q, n - q * a.group};
-}
-
-// One row tile of a sequence: its rows and the tokens that they see.
-struct RowTile {
-  int start;            // the sequence's first row of q
-  int before;           // tokens before its first query (negative: queries that see none)
-  int rows;             // of this tile
-  int query0, head0;    // the query and head (of the group) of its first row
-  int query1;           // the query of its last row
-  int first, last;      // tokens [first, last) are seen by some row,
-  int all_first, all_last;  // and these by all
-  int chunk0, chunk1;   // the chunks that hold them
-};
-
-// False if the tile has no rows in this call.
-__device__ __forceinline__ bool tile_of(const AttentionArgs& a, int seq, int tile, RowTile& t) {
-  t.start = a.query_start[seq];
-  const int end = a.query_start[seq + 1];
-  int length = a.seq_lens[seq];
-  if (t.start < 0 || t.start >= a.num_tokens || end <= t.start) return false;
-  const int queries = end - t.start;
-  int mine = queries < a.max_query_len ? queries : a.max_query_len;  // that this call does
-  mine = mine < a.num_tokens - t.start ? mine : a.num_tokens - t.start;
-  const int row0 = tile * a.tile_rows;
-  t.rows = mine * a.group - row0;
-  if (t.rows <= 0) return false;
-  t.rows = t.rows < a.tile_rows ? t.rows : a.tile_rows;
-  length = length < 0 ? 0 : (length > a.max_seq_len ? a.max_seq_len : length);
-  t.before = length - queries;
-  t.query0 = row0 / a.group;
-  t.head0 = row0 - t.query0 * a.group;
-  t.query1 = row_of(a, t.query0, t.head0, t.rows - 1).query;
-  const int place0 = t.before + t.query0, place1 = t.before + t.query1;
-  t.last = place1 + 1 > 0 ? place1 + 1 : 0;
-  t.first = a.window && place0 >= a.window ? place0 - a.window + 1 : 0;
-  t.all_first = a.window && place1 >= a.window ? place1 - a.window + 1 : 0;
-  t.all_last = place0 + 1;
-  t.chunk0 = t.first / kChunk;
-  t.chunk1 = (t.last + kChunk - 1) / kChunk;
-  return true;
-}
-
 // The parts of a tile that hold anything; 1 also where nothing is seen.
 __device__ __forceinline__ int parts_of(const AttentionArgs& a, const RowTile& t) {
   const int n = (t.chunk1 - t.chunk0 + a.part_chunks - 1) / a.part_chunks;
@@ -424,34 +285,17 @@ __device__ __forceinline__ int64_t unit_of(const AttentionArgs& a, int seq, int 
   return (static_cast<int64_t>(seq) * a.row_tiles + tile) * a.cache.kv_heads + kv_head;
 }
 
-// The sequence that the index'th workgroups of a launch take: longest first, so
-// that short ones fill the gaps at the end.  A compute unit holds two workgroups;
-// where a launch has no more than that, nothing is left for gaps, and those that
-// come second to their unit go shortest first, each beside a long one (64
-// sequences of 17 to 8192 tokens, 8 key heads: as they come 73 us, longest first
-// 69, this 62).  Every wave ranks the sequences for itself; with more of them than
-// lanes, many workgroups a compute unit even the work out and they are taken as they
-// come.
-__device__ __forceinline__ int sequence_at(const AttentionArgs& a, int index) {
-  const int n = static_cast<int>(gridDim.z);
-  if (n == 1 || n > kWave) return index;
-  const int lane = lane_id();
-  int work = -1;
-  if (lane < n) {
-    work = a.seq_lens[lane];
-    work = work < 0 || a.query_start[lane + 1] <= a.query_start[lane] ? 0 : work;
-  }
-  int rank = 0;
-  for (int i = 0; i < n; ++i) {
-    const int other = __builtin_amdgcn_readlane(work, i);
-    rank += other > work || (other == work && i < lane) ? 1 : 0;
-  }
-  int wanted = index;
-  const int each = static_cast<int>(gridDim.x * gridDim.y);  // workgroups of a sequence
-  if (each * n > kCus && each * n <= 2 * kCus && index >= kCus / each)
-    wanted = n - 1 - (index - kCus / each);
-  const unsigned long long hit = __ballot(lane < n && rank == wanted);
-  return __ffsll(static_cast<long long>(hit)) - 1;
+// ln of the sum of a row's exponentials, from the sum relative to the power `top` of
+// two; -infinity for a row that saw nothing.
+__device__ __forceinline__ float log_sum(float top, float full) {
+  return (top + __builtin_amdgcn_logf(full)) * 0.693147181f;
+}
+
+__device__ __forceinline__ void store_lse(const AttentionArgs& a, const RowTile& t, int kv_head, int row,
+                                          float top, float full) {
+  const RowOf at = row_of(a, t.query0, t.head0, row);
+  if (a.lse)
+    a.lse[static_cast<int64_t>(t.start + at.query) * a.ldl + kv_head * a.group + at.head] = log_sum(top, full);
 }
 
 // Four neighbouring outputs of a row, divided by its sum; a row that saw nothing
@@ -465,39 +309,19 @@ __device__ __forceinline__ void store_out(const AttentionArgs& a, const RowTile&
       u32x2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
 }
 
-template <int D>
-__device__ __forceinline__ Reader<D> reader_of(const AttentionArgs& a, int seq, int kv_head) {
-  Reader<D> r;
-  const int64_t block = static_cast<int64_t>(D / 2 + D / kBlock) << a.cache.page_shift;
-  r.keys = a.cache.data + kv_head * block;
-  r.values = r.keys + a.cache.kv_heads * block;
-  r.page_stride = 2 * a.cache.kv_heads * block;
-  r.table = a.page_table + seq * a.ld_table;
-  r.shift = a.cache.page_shift;
-  r.num_pages = a.cache.num_pages;
-  r.max_seq_len = a.max_seq_len;
-  return r;
-}
-
-// Lane (g, c)'s part of the i-th B operand of 16 queries: elements g * D / 4 +
-// 8 i .. + 7 of tile row `row` (c's); rows past the tile's are zero.
-template <int D>
-__device__ __forceinline__ u32x4 query_operand(const AttentionArgs& a, const RowTile& t, int kv_head,
-                                               int row, int i) {
-  u32x4 w = {0, 0, 0, 0};
-  if (row < t.rows) {
-    const RowOf at = row_of(a, t.query0, t.head0, row);
-    w = load16(a.q + static_cast<int64_t>(t.start + at.query) * a.ldq +
-               (kv_head * a.group + at.head) * D + (lane_id() >> 4) * (D / 4) + 8 * i);
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) w[k] ^= a.sign;
-  return w;
+// A part's maximum and sums for one row.
+template <int V>
+__device__ __forceinline__ void store_stats(const AttentionArgs& a, int64_t at, float top, float total,
+                                            float full) {
+  if constexpr (V == kPlain)
+    *(LORA_GLOBAL u32x2*)(a.stats + at * 2) = u32x2{__float_as_uint(top), __float_as_uint(total)};
+  else
+    store16(a.stats + at * 4, u32x4{__float_as_uint(top), __float_as_uint(total), __float_as_uint(full), 0u});
 }
 
 // Few rows: the workgroup's waves share out the tokens of one row tile, and the
 // workgroups of a unit (sequence, key head, row tile) its parts.
-template <int D, int MT>
+template <int D, int MT, int V>
 __global__ __launch_bounds__(split_waves(MT) * kWave, MT == 1 ? 4 : 2) void kv_attention_kernel(AttentionArgs a) {
   constexpr int kWaves = split_waves(MT);
   const int tid = static_cast<int>(threadIdx.x);
@@ -520,7 +344,7 @@ __global__ __launch_bounds__(split_waves(MT) * kWave, MT == 1 ? 4 : 2) void kv_a
   if (!a.window) pages = reader.pages(chunk * kChunk);
 
   RowTile t;
-  if (!tile_of(a, seq, tile, t)) return;
+  if (!tile_of<V>(a, seq, tile, t)) return;
   const int active = parts_of(a, t);
   if (part >= active) return;
   chunk += t.chunk0;
@@ -545,15 +369,12 @@ __global__ __launch_bounds__(split_waves(MT) * kWave, MT == 1 ? 4 : 2) void kv_a
   }
   for (int f = wave; f < MT * (D / 32); f += kWaves)
     q[f][lane] = query_operand<D>(a, t, kv_head, (f / (D / 32)) * kTile + c, f % (D / 32));
-  Rows<D, MT> r;
+  __shared__ Draft drafts[V == kTree ? MT * kTile : 1];
+  if constexpr (V == kTree) stage_drafts(a, t, drafts, MT * kTile, kWaves * kWave);
+  Rows<D, MT, V> r;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    r.place[mt] = t.before + row_of(a, t.query0, t.head0, mt * kTile + c).query;
-    r.top[mt] = kNoScore;
-    r.sum[mt] = 0.f;
-#pragma unroll
-    for (int n = 0; n < D / 16; ++n) r.acc[mt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
+  for (int mt = 0; mt < MT; ++mt)
+    begin(r, mt, t, row_of(a, t.query0, t.head0, mt * kTile + c).query, drafts);
   __syncthreads();
 
   // The next chunk's keys are on their way from the scores on, its values from
@@ -565,16 +386,16 @@ __global__ __launch_bounds__(split_waves(MT) * kWave, MT == 1 ? 4 : 2) void kv_a
     at.first = t.first;
     at.last = t.last;
     at.window = a.window;
-    at.several = t.query1 != t.query0;
+    at.several = V == kTree || t.query1 != t.query0;
     at.ok = pages.v >= 0;
     at.masked = at.base < t.all_first || at.base + kChunk > t.all_last ||
                 !__all(pages.v >= 0 && pages.k >= 0);
     uint32_t weights[MT][8];
-    weigh<D, MT>(r, weights, keys, &q[0][0], at, a.scale_log2);
+    weigh(r, weights, keys, &q[0][0], at, a.scale_log2);
     reader.load(keys, ahead, next * kChunk);
     u32x4 scales = values.scales;
-    if (at.masked) mask_values<D, MT>(r, scales, at);
-    add_values<D, MT>(r, weights, values, scales);
+    if (at.masked) mask_values(r, scales, at);
+    add_values(r, weights, values, scales);
     reader.load(values, ahead, next * kChunk);
     pages = ahead;
     next = after;
@@ -584,12 +405,16 @@ __global__ __launch_bounds__(split_waves(MT) * kWave, MT == 1 ? 4 : 2) void kv_a
   for (int mt = 0; mt < MT; ++mt) {
     r.sum[mt] += __shfl_xor(r.sum[mt], 16);
     r.sum[mt] += __shfl_xor(r.sum[mt], 32);
+    if constexpr (V != kPlain) {
+      r.full[mt] += __shfl_xor(r.full[mt], 16);
+      r.full[mt] += __shfl_xor(r.full[mt], 32);
+    }
   }
 
   // The waves' results, joined in a fixed order.
   // (rows 4 words apart from a multiple of the banks)
   __shared__ float outs[kWaves][kTile][D + 4];
-  __shared__ float tops[kWaves][kTile], sums[kWaves][kTile];
+  __shared__ float tops[kWaves][kTile], sums[kWaves][kTile], fulls[V == kPlain ? 1 : kWaves][kTile];
   constexpr int kLanes = D / 4;  // threads a row, four elements each
   constexpr int kRowsAtOnce = kWaves * kWave / kLanes;
   const int e = (tid % kLanes) * 4;
@@ -601,6 +426,7 @@ __global__ __launch_bounds__(split_waves(MT) * kWave, MT == 1 ? 4 : 2) void kv_a
     if (g == 0) {
       tops[wave][c] = r.top[mt];
       sums[wave][c] = r.sum[mt];
+      if constexpr (V != kPlain) fulls[wave][c] = r.full[mt];
     }
     __syncthreads();
     float top = kNoScore;
@@ -619,22 +445,22 @@ __global__ __launch_bounds__(split_waves(MT) * kWave, MT == 1 ? 4 : 2) void kv_a
       top = kNoScore;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) top = fmaxf(top, tops[w][row]);
-      float total = 0.f;
+      float total = 0.f, full = 0.f;
       f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
         total += sums[w][row] * __builtin_amdgcn_exp2f(tops[w][row] - top);
+        if constexpr (V != kPlain) full += fulls[w][row] * __builtin_amdgcn_exp2f(tops[w][row] - top);
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] += outs[w][row][e + i];
       }
       if (active == 1) {
         store_out(a, t, kv_head, mt * kTile + row, D, e, o, total);
+        if (V != kPlain && e == 0) store_lse(a, t, kv_head, mt * kTile + row, top, full);
       } else {
         const int64_t at = slot + mt * kTile + row;
         store16(a.partial + at * D + e, __builtin_bit_cast(u32x4, o));
-        if (e == 0)
-          *(LORA_GLOBAL u32x2*)(a.stats + at * 2) =
-              u32x2{__float_as_uint(top), __float_as_uint(total)};
+        if (e == 0) store_stats<V>(a, at, top, total, full);
       }
     }
   }
@@ -647,7 +473,7 @@ __global__ __launch_bounds__(split_waves(MT) * kWave, MT == 1 ? 4 : 2) void kv_a
 // matrix unit's lanes take them (16 bytes a lane, so neither side has bank
 // conflicts).  Two buffers and one barrier a chunk; the codes of the next chunk
 // are on their way meanwhile.
-template <int D>
+template <int D, int V>
 __global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel(AttentionArgs a) {
   constexpr int MT = kRowTiles;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
@@ -657,7 +483,7 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel
   // the last rows of a sequence see the most
   const int tile = static_cast<int>(gridDim.y - 1 - blockIdx.y);
   RowTile t;
-  if (!tile_of(a, seq, tile, t)) return;
+  if (!tile_of<V>(a, seq, tile, t)) return;
   const Reader<D> reader = reader_of<D>(a, seq, kv_head);
 
   // This wave's rows, and what they see.
@@ -665,7 +491,14 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel
   const int left = t.rows - row0;
   const int mine = left < 0 ? 0 : (left < MT * kTile ? left : MT * kTile);
   int first = 0, last = 0, all_first = 0, all_last = 0;
-  if (mine > 0) {
+  if (V == kTree) {
+    if (mine > 0) {
+      first = t.first;
+      last = t.last;
+      all_first = t.all_first;
+      all_last = t.all_last;
+    }
+  } else if (mine > 0) {
     const int place0 = t.before + row_of(a, t.query0, t.head0, row0).query;
     const int place1 = t.before + row_of(a, t.query0, t.head0, row0 + mine - 1).query;
     last = place1 + 1;
@@ -673,19 +506,17 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel
     all_first = a.window && place1 >= a.window ? place1 - a.window + 1 : 0;
     all_last = place0 + 1;
   }
+  __shared__ Draft drafts[V == kTree ? kRowWaves * MT * kTile : 1];
+  if constexpr (V == kTree) stage_drafts(a, t, drafts, kRowWaves * MT * kTile, kRowWaves * kWave);  // (a barrier comes below)
   bf16x8 q[MT][D / 32];
-  Rows<D, MT> r;
+  Rows<D, MT, V> r;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     const int row = row0 + mt * kTile + c;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
       q[mt][i] = __builtin_bit_cast(bf16x8, query_operand<D>(a, t, kv_head, row, i));
-    r.place[mt] = t.before + row_of(a, t.query0, t.head0, row).query;
-    r.top[mt] = kNoScore;
-    r.sum[mt] = 0.f;
-#pragma unroll
-    for (int n = 0; n < D / 16; ++n) r.acc[mt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    begin(r, mt, t, row_of(a, t.query0, t.head0, row).query, drafts);
   }
 
   __shared__ u32x4 keys[2][4][D / 32][kWave];    // [buffer][tile j][step i][lane]
@@ -735,7 +566,7 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel
     for (int i = 0; i < D / 32; ++i) keys[buffer][wave][i][lane] = word_to_bf16(kw[i], ks);
     if (partial(base)) {
       // as mask_values, for the tokens that no row of the workgroup sees
-      const bool several = t.query1 != t.query0;
+      const bool several = V == kTree || t.query1 != t.query0;
       uint32_t nan = 0;
       const int token = base + 16 * g + 8 * half;
 #pragma unroll
@@ -798,7 +629,7 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel
     at.first = t.first;
     at.last = t.last;
     at.window = a.window;
-    at.several = t.query1 != t.query0;
+    at.several = V == kTree || t.query1 != t.query0;
     at.ok = lane_ok;
     at.masked = at.base < all_first || at.base + kChunk > all_last || !pages_ok;
     const bool whole = !chunk_partial;
@@ -826,21 +657,21 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel
       constexpr int kEvery = 4 / (D / 32);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) scores(0, i);
-      raise<D, MT>(r, 0, s[0], at, a.scale_log2);
+      raise(r, 0, s[0], at, a.scale_log2);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (i % kEvery == 0) scores(1, i / kEvery);
-        powers(weights[0], r.sum[0], s[0], i, r.top[0], a.scale_log2);
+        powers(weights[0], r, 0, s[0], i, a.scale_log2);
       }
-      raise<D, MT>(r, 1, s[1], at, a.scale_log2);
+      raise(r, 1, s[1], at, a.scale_log2);
       if (!whole) {
         const int b = c / (kBlock / (D / 16));
-        mark_nan<D, MT>(r, nans[buffer][0][g][b] | nans[buffer][1][g][b] << 8, at);
+        mark_nan(r, nans[buffer][0][g][b] | nans[buffer][1][g][b] << 8, at);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         products(0, i >> 1, (i & 1) * (D / 32), ((i & 1) + 1) * (D / 32));
-        powers(weights[1], r.sum[1], s[1], i, r.top[1], a.scale_log2);
+        powers(weights[1], r, 1, s[1], i, a.scale_log2);
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) products(1, h, 0, D / 16);
@@ -860,8 +691,15 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel
     float sum = r.sum[mt];
     sum += __shfl_xor(sum, 16);
     sum += __shfl_xor(sum, 32);
+    float full = 0.f;
+    if constexpr (V != kPlain) {
+      full = r.full[mt];
+      full += __shfl_xor(full, 16);
+      full += __shfl_xor(full, 32);
+    }
     const int row = row0 + mt * kTile + c;
     if (row >= t.rows) continue;
+    if (V != kPlain && g == 0) store_lse(a, t, kv_head, row, r.top[mt], full);
     const RowOf at = row_of(a, t.query0, t.head0, row);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     uint16_t* dst = a.out + static_cast<int64_t>(t.start + at.query) * a.ldo +
@@ -886,7 +724,7 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel
 // parts up by itself (131072 tokens, 8 key heads, 32 parts of 8 rows each: 10 us in
 // the last workgroup to arrive, 4 here).
 constexpr int kJoinThreads = 256;
-template <int D>
+template <int D, int V>
 __global__ __launch_bounds__(kJoinThreads) void kv_attention_join_kernel(AttentionArgs a,
                                                                          int rows_shift) {
   constexpr int kLanes = D / 4, kTeams = kJoinThreads / kLanes;
@@ -900,48 +738,60 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attention_join_kernel(Attenti
   const int tile = index / a.tile_rows;
   const int row = index - tile * a.tile_rows;
   RowTile t;
-  if (!tile_of(a, seq, tile, t)) return;  // the whole workgroup, here and below
+  if (!tile_of<V>(a, seq, tile, t)) return;  // the whole workgroup, here and below
   const int active = parts_of(a, t);
   if (active == 1) return;
-  float top = kNoScore, total = 0.f;
+  float top = kNoScore, total = 0.f, full = 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
   if (row < t.rows) {
     const int64_t slot = unit_of(a, seq, tile, kv_head) * a.parts * a.tile_rows + row;
 #pragma unroll 4
     for (int p = of_row; p < active; p += teams) {
       const int64_t at = slot + static_cast<int64_t>(p) * a.tile_rows;
-      const u32x2 m = load8(a.stats + at * 2);
+      u32x4 m = {0, 0, 0, 0};
+      if constexpr (V == kPlain) {
+        const u32x2 two = load8(a.stats + at * 2);
+        m[0] = two[0];
+        m[1] = two[1];
+      } else {
+        m = load16(a.stats + at * 4);
+      }
       const f32x4 w = __builtin_bit_cast(f32x4, load16(a.partial + at * D + e));
       const float now = fmaxf(top, __uint_as_float(m[0]));
       const float fa = __builtin_amdgcn_exp2f(top - now);
       const float fb = __builtin_amdgcn_exp2f(__uint_as_float(m[0]) - now);
       top = now;
       total = total * fa + __uint_as_float(m[1]) * fb;
+      if constexpr (V != kPlain) full = full * fa + __uint_as_float(m[2]) * fb;
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] = o[i] * fa + w[i] * fb;
     }
   }
   __shared__ f32x4 outs[kTeams][kLanes];
-  __shared__ float tops[kTeams], sums[kTeams];
+  __shared__ float tops[kTeams], sums[kTeams], fulls[kTeams];
   outs[team][tid % kLanes] = o;
   if (e == 0) {
     tops[team] = top;
     sums[team] = total;
+    if constexpr (V != kPlain) fulls[team] = full;
   }
   __syncthreads();
   if (of_row > 0 || row >= t.rows) return;
   top = kNoScore;
   for (int i = team; i < team + teams; ++i) top = fmaxf(top, tops[i]);
   total = 0.f;
+  full = 0.f;
   o = f32x4{0.f, 0.f, 0.f, 0.f};
   for (int i = team; i < team + teams; ++i) {
     const float f = __builtin_amdgcn_exp2f(tops[i] - top);
     total += sums[i] * f;
+    if constexpr (V != kPlain) full += fulls[i] * f;
     const f32x4 w = outs[i][tid % kLanes];
 #pragma unroll
     for (int k = 0; k < 4; ++k) o[k] += w[k] * f;
   }
   store_out(a, t, kv_head, row, D, e, o, total);
+  if (V != kPlain && e == 0) store_lse(a, t, kv_head, row, top, full);
 }
 
 // How a call is cut up: a function of the sizes alone.
@@ -992,35 +842,45 @@ static AttentionPlan attention_plan(int num_seqs, int max_query_len, int64_t max
 }
 
 // Bytes of the parts' maxima and sums, which lie before their outputs.
-static int64_t stats_bytes(const AttentionPlan& p) {
-  return (p.units * p.most_parts * p.tile_rows * 8 + 255) / 256 * 256;
+static int64_t stats_bytes(const AttentionPlan& p, View view) {
+  return (p.units * p.most_parts * p.tile_rows * (view == kPlain ? 8 : 16) + 255) / 256 * 256;
+}
+
+static int64_t workspace_bytes(int num_seqs, int max_query_len, int max_seq_len, int q_heads, int kv_heads,
+                               int head_dim, View view) {
+  if (num_seqs < 1) return 0;
+  const AttentionPlan p = attention_plan(num_seqs, max_query_len, max_seq_len, q_heads, kv_heads);
+  if (p.most_parts <= 1) return 0;
+  return stats_bytes(p, view) + p.units * p.most_parts * p.tile_rows * head_dim * 4;
 }
 
 int64_t kv_attention_workspace_bytes(int num_seqs, int max_query_len, int max_seq_len, int q_heads,
                                      int kv_heads, int head_dim) {
-  if (num_seqs < 1) return 0;
-  const AttentionPlan p = attention_plan(num_seqs, max_query_len, max_seq_len, q_heads, kv_heads);
-  if (p.most_parts <= 1) return 0;
-  return stats_bytes(p) + p.units * p.most_parts * p.tile_rows * head_dim * 4;
+  return workspace_bytes(num_seqs, max_query_len, max_seq_len, q_heads, kv_heads, head_dim, kPlain);
 }
 
-template <int D>
+int64_t kv_tree_attention_workspace_bytes(int num_seqs, int max_query_len, int max_seq_len, int q_heads,
+                                          int kv_heads, int head_dim) {
+  return workspace_bytes(num_seqs, max_query_len, max_seq_len, q_heads, kv_heads, head_dim, kTree);
+}
+
+template <int D, int V>
 static void launch_for(const AttentionArgs& a, const AttentionPlan& p, int num_seqs,
                        hipStream_t stream) {
   const int heads = a.cache.kv_heads;
   const dim3 grid(heads, p.row_tiles * p.parts, num_seqs);
   if (p.many)
-    hipLaunchKernelGGL(kv_attention_rows_kernel<D>, grid, dim3(kRowWaves * kWave), 0, stream, a);
+    hipLaunchKernelGGL((kv_attention_rows_kernel<D, V>), grid, dim3(kRowWaves * kWave), 0, stream, a);
   else if (p.tile_rows == kTile)
-    hipLaunchKernelGGL((kv_attention_kernel<D, 1>), grid, dim3(split_waves(1) * kWave), 0, stream, a);
+    hipLaunchKernelGGL((kv_attention_kernel<D, 1, V>), grid, dim3(split_waves(1) * kWave), 0, stream, a);
   else
-    hipLaunchKernelGGL((kv_attention_kernel<D, 2>), grid, dim3(split_waves(2) * kWave), 0, stream, a);
+    hipLaunchKernelGGL((kv_attention_kernel<D, 2, V>), grid, dim3(split_waves(2) * kWave), 0, stream, a);
   if (p.parts > 1) {
     // of a workgroup's threads, as many a row as its parts keep busy
     int shift = 0;
     while ((kJoinThreads / (D / 4) >> (shift + 1)) >= p.parts) ++shift;
     const int rows = a.max_query_len * a.group;
-    hipLaunchKernelGGL(kv_attention_join_kernel<D>,
+    hipLaunchKernelGGL((kv_attention_join_kernel<D, V>),
                        dim3(heads, (rows + (1 << shift) - 1) >> shift, num_seqs),
                        dim3(kJoinThreads), 0, stream, a, shift);
   }
@@ -1031,8 +891,10 @@ hipError_t launch_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* qu
                                int64_t ld_table, const uint8_t* cache, int num_pages,
                                int page_shift, int num_tokens, int num_seqs, int max_query_len,
                                int max_seq_len, int q_heads, int kv_heads, int head_dim,
-                               float scale, int window, uint16_t* out, int64_t ldo,
-                               void* workspace, hipStream_t stream) {
+                               float scale, int window, const int64_t* masks, int64_t words,
+                               uint16_t* out, int64_t ldo, float* lse, int64_t ldl, void* workspace,
+                               hipStream_t stream) {
+  const View view = masks ? kTree : (lse ? kSums : kPlain);
   const int group = q_heads / kv_heads;
   // A window bounds the tokens that any tile walks; the parts are then fewer
   // than those that the workspace is sized for.
@@ -1048,16 +910,29 @@ hipError_t launch_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* qu
                      ldq, ldo, ld_table, num_tokens, max_query_len, max_seq_len, q_heads, window,
                      fabsf(scale) * 1.44269504f, scale < 0.f ? 0x80008000u : 0u,
                      group, ((1 << 21) + group - 1) / group,
-                     p.row_tiles, p.parts, p.part_chunks, p.tile_rows, nullptr, nullptr};
+                     p.row_tiles, p.parts, p.part_chunks, p.tile_rows, nullptr, nullptr,
+                     masks, words, lse, ldl};
   // a hidden token's -infinity must stay -infinity, and a score of zero stay zero
   if (a.scale_log2 < 1.17549435e-38f) a.scale_log2 = 1.17549435e-38f;
   if (a.scale_log2 > 3.402823466e38f) a.scale_log2 = 3.402823466e38f;
   if (p.parts > 1) {
     a.stats = static_cast<float*>(workspace);
-    a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + stats_bytes(p));
+    a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + stats_bytes(p, view));
   }
-  if (head_dim == 64) launch_for<64>(a, p, num_seqs, stream);
-  else launch_for<128>(a, p, num_seqs, stream);
+  switch (view) {
+    case kPlain:
+      if (head_dim == 64) launch_for<64, kPlain>(a, p, num_seqs, stream);
+      else launch_for<128, kPlain>(a, p, num_seqs, stream);
+      break;
+    case kSums:
+      if (head_dim == 64) launch_for<64, kSums>(a, p, num_seqs, stream);
+      else launch_for<128, kSums>(a, p, num_seqs, stream);
+      break;
+    case kTree:
+      if (head_dim == 64) launch_for<64, kTree>(a, p, num_seqs, stream);
+      else launch_for<128, kTree>(a, p, num_seqs, stream);
+      break;
+  }
   return hipGetLastError();
 }
 
