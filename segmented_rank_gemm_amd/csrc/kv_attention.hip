@@ -75,23 +75,6 @@ __device__ __forceinline__ uint32_t seen_by(const Rows<D, MT, V>& r, int mt, con
   else return seen_bits(at, r.place[mt]);
 }
 
-// Row c of tile mt: what it sees, and nothing summed up yet.
-template <int D, int MT, int V>
-__device__ __forceinline__ void begin(Rows<D, MT, V>& r, int mt, const RowTile& t, int query,
-                                      const Draft* drafts) {
-  if constexpr (V == kTree) {
-    r.drafts[mt] = drafts + (query - t.query0);
-    r.before = t.before;
-  } else {
-    r.place[mt] = t.before + query;
-  }
-  r.top[mt] = kNoScore;
-  r.sum[mt] = 0.f;
-  if constexpr (V != kPlain) r.full[mt] = 0.f;
-#pragma unroll
-  for (int n = 0; n < D / 16; ++n) r.acc[mt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-}
-
 // The first half of the running softmax over one chunk's scores of row tile mt,
 // s[j][i] of token 16 g + 4 i + j: hides what a row does not see and moves the
 // running maximum.
@@ -291,7 +274,7 @@ __device__ __forceinline__ float log_sum(float top, float full) {
   return (top + __builtin_amdgcn_logf(full)) * 0.693147181f;
 }
 
-__device__ __forceinline__ void store_lse(const AttentionArgs& a, const RowTile& t, int kv_head, int row,
+__device__ __forceinline__ void store_lse(const SumArgs& a, const RowTile& t, int kv_head, int row,
                                           float top, float full) {
   const RowOf at = row_of(a, t.query0, t.head0, row);
   if (a.lse)
@@ -322,7 +305,7 @@ __device__ __forceinline__ void store_stats(const AttentionArgs& a, int64_t at, 
 // Few rows: the workgroup's waves share out the tokens of one row tile, and the
 // workgroups of a unit (sequence, key head, row tile) its parts.
 template <int D, int MT, int V>
-__global__ __launch_bounds__(split_waves(MT) * kWave, MT == 1 ? 4 : 2) void kv_attention_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(split_waves(MT) * kWave, MT == 1 ? 4 : 2) void kv_attention_kernel(typename ArgsOf<V>::type a) {
   constexpr int kWaves = split_waves(MT);
   const int tid = static_cast<int>(threadIdx.x);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -373,8 +356,19 @@ __global__ __launch_bounds__(split_waves(MT) * kWave, MT == 1 ? 4 : 2) void kv_a
   if constexpr (V == kTree) stage_drafts(a, t, drafts, MT * kTile, kWaves * kWave);
   Rows<D, MT, V> r;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-    begin(r, mt, t, row_of(a, t.query0, t.head0, mt * kTile + c).query, drafts);
+  for (int mt = 0; mt < MT; ++mt) {
+    if constexpr (V == kTree) {
+      r.drafts[mt] = drafts + (row_of(a, t.query0, t.head0, mt * kTile + c).query - t.query0);
+      r.before = t.before;
+    } else {
+      r.place[mt] = t.before + row_of(a, t.query0, t.head0, mt * kTile + c).query;
+    }
+    r.top[mt] = kNoScore;
+    r.sum[mt] = 0.f;
+    if constexpr (V != kPlain) r.full[mt] = 0.f;
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n) r.acc[mt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
   __syncthreads();
 
   // The next chunk's keys are on their way from the scores on, its values from
@@ -456,7 +450,8 @@ __global__ __launch_bounds__(split_waves(MT) * kWave, MT == 1 ? 4 : 2) void kv_a
       }
       if (active == 1) {
         store_out(a, t, kv_head, mt * kTile + row, D, e, o, total);
-        if (V != kPlain && e == 0) store_lse(a, t, kv_head, mt * kTile + row, top, full);
+        if constexpr (V != kPlain)
+          if (e == 0) store_lse(a, t, kv_head, mt * kTile + row, top, full);
       } else {
         const int64_t at = slot + mt * kTile + row;
         store16(a.partial + at * D + e, __builtin_bit_cast(u32x4, o));
@@ -474,7 +469,7 @@ __global__ __launch_bounds__(split_waves(MT) * kWave, MT == 1 ? 4 : 2) void kv_a
 // conflicts).  Two buffers and one barrier a chunk; the codes of the next chunk
 // are on their way meanwhile.
 template <int D, int V>
-__global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel(typename ArgsOf<V>::type a) {
   constexpr int MT = kRowTiles;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   const int lane = lane_id(), g = lane >> 4, c = lane & 15;
@@ -516,7 +511,17 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
       q[mt][i] = __builtin_bit_cast(bf16x8, query_operand<D>(a, t, kv_head, row, i));
-    begin(r, mt, t, row_of(a, t.query0, t.head0, row).query, drafts);
+    if constexpr (V == kTree) {
+      r.drafts[mt] = drafts + (row_of(a, t.query0, t.head0, row).query - t.query0);
+      r.before = t.before;
+    } else {
+      r.place[mt] = t.before + row_of(a, t.query0, t.head0, row).query;
+    }
+    r.top[mt] = kNoScore;
+    r.sum[mt] = 0.f;
+    if constexpr (V != kPlain) r.full[mt] = 0.f;
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n) r.acc[mt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
   __shared__ u32x4 keys[2][4][D / 32][kWave];    // [buffer][tile j][step i][lane]
@@ -699,7 +704,8 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel
     }
     const int row = row0 + mt * kTile + c;
     if (row >= t.rows) continue;
-    if (V != kPlain && g == 0) store_lse(a, t, kv_head, row, r.top[mt], full);
+    if constexpr (V != kPlain)
+      if (g == 0) store_lse(a, t, kv_head, row, r.top[mt], full);
     const RowOf at = row_of(a, t.query0, t.head0, row);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     uint16_t* dst = a.out + static_cast<int64_t>(t.start + at.query) * a.ldo +
@@ -725,7 +731,7 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel
 // the last workgroup to arrive, 4 here).
 constexpr int kJoinThreads = 256;
 template <int D, int V>
-__global__ __launch_bounds__(kJoinThreads) void kv_attention_join_kernel(AttentionArgs a,
+__global__ __launch_bounds__(kJoinThreads) void kv_attention_join_kernel(typename ArgsOf<V>::type a,
                                                                          int rows_shift) {
   constexpr int kLanes = D / 4, kTeams = kJoinThreads / kLanes;
   const int tid = static_cast<int>(threadIdx.x);
@@ -791,7 +797,8 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attention_join_kernel(Attenti
     for (int k = 0; k < 4; ++k) o[k] += w[k] * f;
   }
   store_out(a, t, kv_head, row, D, e, o, total);
-  if (V != kPlain && e == 0) store_lse(a, t, kv_head, row, top, full);
+  if constexpr (V != kPlain)
+    if (e == 0) store_lse(a, t, kv_head, row, top, full);
 }
 
 // How a call is cut up: a function of the sizes alone.
@@ -865,7 +872,7 @@ int64_t kv_tree_attention_workspace_bytes(int num_seqs, int max_query_len, int m
 }
 
 template <int D, int V>
-static void launch_for(const AttentionArgs& a, const AttentionPlan& p, int num_seqs,
+static void launch_for(const typename ArgsOf<V>::type& a, const AttentionPlan& p, int num_seqs,
                        hipStream_t stream) {
   const int heads = a.cache.kv_heads;
   const dim3 grid(heads, p.row_tiles * p.parts, num_seqs);
@@ -905,12 +912,12 @@ hipError_t launch_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* qu
     longest = longest < seen ? longest : seen;
   }
   const AttentionPlan p = attention_plan(num_seqs, max_query_len, longest, q_heads, kv_heads);
-  AttentionArgs a = {q, query_start, seq_lens, page_table, out,
+  SumArgs a = {{q, query_start, seq_lens, page_table, out,
                      {cache, num_pages, page_shift, kv_heads},
                      ldq, ldo, ld_table, num_tokens, max_query_len, max_seq_len, q_heads, window,
                      fabsf(scale) * 1.44269504f, scale < 0.f ? 0x80008000u : 0u,
                      group, ((1 << 21) + group - 1) / group,
-                     p.row_tiles, p.parts, p.part_chunks, p.tile_rows, nullptr, nullptr,
+                     p.row_tiles, p.parts, p.part_chunks, p.tile_rows, nullptr, nullptr},
                      masks, words, lse, ldl};
   // a hidden token's -infinity must stay -infinity, and a score of zero stay zero
   if (a.scale_log2 < 1.17549435e-38f) a.scale_log2 = 1.17549435e-38f;

@@ -49,11 +49,22 @@ struct AttentionArgs {
   // maximum and the sum, and the outputs relative to that maximum.
   float* stats;       // [..][2], with sums of exponentials [..][4]
   float* partial;     // [..][D]
-  // Of views other than the plain one (see View), where they have them.
+};
+
+// And of the other views; the plain one's kernels are not handed what they do not read.
+struct SumArgs : AttentionArgs {
   const int64_t* masks;  // [num_tokens][words]
   int64_t words;
-  float* lse;            // [num_tokens][ldl]
+  float* lse;            // [num_tokens][ldl]; may be null
   int64_t ldl;
+};
+template <int V>
+struct ArgsOf {
+  using type = SumArgs;
+};
+template <>
+struct ArgsOf<kPlain> {
+  using type = AttentionArgs;
 };
 
 __device__ __forceinline__ uint32_t byte_scale(uint32_t w, int j) {
@@ -224,54 +235,28 @@ __device__ __forceinline__ void see(const AttentionArgs& a, RowTile& t, int leng
   t.chunk1 = (t.last + kChunk - 1) / kChunk;
 }
 
-// A sequence in this call; false if it has no rows in it.
-struct Sequence {
-  int start, queries, length;
-  int mine;  // of its queries, those that this call does
-};
-__device__ __forceinline__ bool sequence_of(const AttentionArgs& a, int seq, Sequence& s) {
-  s.start = a.query_start[seq];
-  const int end = a.query_start[seq + 1];
-  s.length = a.seq_lens[seq];
-  if (s.start < 0 || s.start >= a.num_tokens || end <= s.start) return false;
-  s.queries = end - s.start;
-  s.mine = s.queries < a.max_query_len ? s.queries : a.max_query_len;
-  s.mine = s.mine < a.num_tokens - s.start ? s.mine : a.num_tokens - s.start;
-  s.length = s.length < 0 ? 0 : (s.length > a.max_seq_len ? a.max_seq_len : s.length);
-  return true;
-}
-
-// False if the tile has no rows in this call.
+// False if the tile has no rows in this call.  all: the tile is all of the sequence's rows.
 template <int V = kPlain>
-__device__ __forceinline__ bool tile_of(const AttentionArgs& a, int seq, int tile, RowTile& t) {
-  Sequence s;
-  if (!sequence_of(a, seq, s)) return false;
-  const int row0 = tile * a.tile_rows;
-  t.start = s.start;
-  t.queries = s.queries;
-  t.before = s.length - s.queries;
-  t.rows = s.mine * a.group - row0;
+__device__ __forceinline__ bool tile_of(const AttentionArgs& a, int seq, int tile, RowTile& t,
+                                        bool all = false) {
+  t.start = a.query_start[seq];
+  const int end = a.query_start[seq + 1];
+  int length = a.seq_lens[seq];
+  if (t.start < 0 || t.start >= a.num_tokens || end <= t.start) return false;
+  const int queries = end - t.start;
+  int mine = queries < a.max_query_len ? queries : a.max_query_len;  // that this call does
+  mine = mine < a.num_tokens - t.start ? mine : a.num_tokens - t.start;
+  const int row0 = all ? 0 : tile * a.tile_rows;
+  t.rows = mine * a.group - row0;
   if (t.rows <= 0) return false;
-  t.rows = t.rows < a.tile_rows ? t.rows : a.tile_rows;
+  if (!all) t.rows = t.rows < a.tile_rows ? t.rows : a.tile_rows;
+  length = length < 0 ? 0 : (length > a.max_seq_len ? a.max_seq_len : length);
+  t.before = length - queries;
+  t.queries = queries;
   t.query0 = row0 / a.group;
   t.head0 = row0 - t.query0 * a.group;
-  t.query1 = row_of(a, t.query0, t.head0, t.rows - 1).query;
-  see<V>(a, t, s.length);
-  return true;
-}
-
-// All rows of a sequence as one tile.
-template <int V>
-__device__ __forceinline__ bool whole_sequence(const AttentionArgs& a, int seq, RowTile& t) {
-  Sequence s;
-  if (!sequence_of(a, seq, s)) return false;
-  t.start = s.start;
-  t.queries = s.queries;
-  t.before = s.length - s.queries;
-  t.rows = s.mine * a.group;
-  t.query0 = t.head0 = 0;
-  t.query1 = s.mine - 1;
-  see<V>(a, t, s.length);
+  t.query1 = all ? mine - 1 : row_of(a, t.query0, t.head0, t.rows - 1).query;
+  see<V>(a, t, length);
   return true;
 }
 
@@ -280,7 +265,7 @@ __device__ __forceinline__ bool whole_sequence(const AttentionArgs& a, int seq, 
 // in their order are those before the drafts and then its mask's; with a window it
 // sees the last `window` of them.  A mask's bits of drafts that are not there (past
 // the sequence's, or before its first token) do not count.
-__device__ __forceinline__ void stage_drafts(const AttentionArgs& a, const RowTile& t, Draft* drafts,
+__device__ __forceinline__ void stage_drafts(const SumArgs& a, const RowTile& t, Draft* drafts,
                                              int count, int threads) {
   const int words = static_cast<int>(a.words);
   const int low = t.before < 0 ? -t.before : 0, high = t.queries;

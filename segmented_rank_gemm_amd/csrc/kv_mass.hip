@@ -18,7 +18,7 @@ namespace lora {
 constexpr int kMassWaves = 4;
 
 struct MassArgs {
-  AttentionArgs a;
+  SumArgs a;
   float* mass;
 };
 
@@ -40,12 +40,12 @@ __device__ __forceinline__ float join_group(float (&v)[16]) {
 
 template <int D, int V>
 __global__ __launch_bounds__(kMassWaves * kWave, 2) void kv_mass_kernel(MassArgs m) {
-  const AttentionArgs& a = m.a;
+  const SumArgs& a = m.a;
   const int wave = wave_index(), lane = lane_id(), g = lane >> 4, c = lane & 15;
   const int kv_head = static_cast<int>(blockIdx.x);
   const int seq = sequence_at(a, static_cast<int>(blockIdx.z));
   RowTile t;
-  if (!whole_sequence<V>(a, seq, t)) return;
+  if (!tile_of<V>(a, seq, 0, t, true)) return;
   const Reader<D> reader = reader_of<D>(a, seq, kv_head);
   const int length = t.before + t.queries;
   const int end = (length + kChunk - 1) / kChunk;
@@ -143,12 +143,12 @@ hipError_t launch_kv_attention_mass(const uint16_t* q, int64_t ldq, const float*
   const int group = q_heads / kv_heads;
   if (window >= max_seq_len) window = 0;
   MassArgs m;
-  m.a = AttentionArgs{q, query_start, seq_lens, page_table, nullptr,
+  m.a = SumArgs{{q, query_start, seq_lens, page_table, nullptr,
                       {cache, num_pages, page_shift, kv_heads},
                       ldq, 0, ld_table, num_tokens, max_query_len, max_seq_len, q_heads, window,
                       fabsf(scale) * 1.44269504f, scale < 0.f ? 0x80008000u : 0u,
                       group, ((1 << 21) + group - 1) / group,
-                      1, 1, 0, 0, nullptr, nullptr,
+                      1, 1, 0, 0, nullptr, nullptr},
                       masks, words, const_cast<float*>(lse), ldl};
   m.mass = mass;
   const int64_t chunks = (static_cast<int64_t>(max_seq_len) + kChunk - 1) / kChunk;
