@@ -5,132 +5,366 @@
 // added to what earlier steps left for the tokens before the queries, and put in the
 // place of whatever was there for the queries' own.
 //
-// A wave takes 64 tokens of a key head and keeps their keys in registers as operands
-// of the matrix unit; the rows come by in tiles of 16.  Lane (g, c) of a tile's scores
-// has those of the tokens [16 g, 16 g + 16) for row c, so each lane adds up its
-// sixteen tokens over the tiles, and the sixteen lanes of a group are joined once, at
-// the end.  Every token has one writer: the sums are always taken in the same order.
+// The scores are 16x16 matrix products with the rows on one side (A) and tokens on the
+// other (B): column c of the j-th of a chunk's four products is token 4 c + j, so that
+// lane (g, c) (lane = 16 g + c) gets, for the rows [4 g, 4 g + 4), the scores of four
+// neighbouring tokens.  It adds up its rows, tile after tile, in four registers; the
+// four lanes that share the tokens are joined once, at the end.  Every token has one
+// writer, and its sum is always taken in the same order.
+//
+// Few rows: a wave walks chunks of 64 tokens of a key head, the next one's keys on
+// their way, with the rows in shared memory.  Many: a wave keeps the keys of one chunk
+// in registers, and the rows come by.
 
 #include "kv_attention.hpp"
 
 namespace lora {
 
-constexpr int kMassWaves = 4;
+constexpr int kMassWaves = 8;
+constexpr int kMassThreads = kMassWaves * kWave;
+constexpr int kMostTiles = 4;      // of 16 rows, for the kernel of few
+constexpr int kHalves = 2;         // of the rows, for that of many: waves that share a chunk
+constexpr int kStageTiles = 2;     // tiles of a half that are staged at a time
+constexpr int kStageRows = kHalves * kStageTiles * kTile;
+constexpr float kLog2e = 1.44269504f;
 
 struct MassArgs {
   SumArgs a;
   float* mass;
+  float scale_log2;  // scale * log2(e), with its sign
 };
 
-// This lane's sixteen sums joined with those of its group's other lanes: lane (g, c)
-// is left with the sum of token 16 g + c.  Each step halves the tokens a lane holds.
-__device__ __forceinline__ float join_group(float (&v)[16]) {
-  const int c = lane_id() & 15;
-#pragma unroll
-  for (int half = 8; half >= 1; half >>= 1) {
-    const bool upper = (c & half) != 0;
-#pragma unroll
-    for (int i = 0; i < half; ++i) {
-      const float give = upper ? v[i] : v[i + half], keep = upper ? v[i + half] : v[i];
-      v[i] = keep + __shfl_xor(give, half);
-    }
-  }
-  return v[0];
+// A row's sum as the power that its scores are taken relative to; a row without a sum
+// (or none at all) counts for nothing.
+__device__ __forceinline__ float relative_to(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
+
+// Sums over the four lanes with the same c.
+__device__ __forceinline__ float over_groups(float v) {
+  const uint32_t a = __float_as_uint(v);
+  const auto rows = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  const uint32_t b = __float_as_uint(__uint_as_float(rows[0]) + __uint_as_float(rows[1]));
+  const auto halves = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return __uint_as_float(halves[0]) + __uint_as_float(halves[1]);
 }
 
-template <int D, int V>
-__global__ __launch_bounds__(kMassWaves * kWave, 2) void kv_mass_kernel(MassArgs m) {
+// The chunk's tokens that the rows [4 g, 4 g + 4) of a tile see: bit 4 i + j for row i and
+// token 4 c + j.  Row 0 of the tile is head head0 of query query0; past `rows`, none.
+template <int V>
+__device__ __forceinline__ uint32_t seen_by_rows(const AttentionArgs& a, const RowTile& t, const Draft* drafts,
+                                                 int base, int query0, int head0, int rows) {
+  const int lane = lane_id(), g = lane >> 4;
+  const int token = base + 4 * (lane & 15);
+  uint32_t seen = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 4 * g + i;
+    const int query = row_of(a, query0, head0, row).query;
+    uint32_t bits;
+    if constexpr (V == kTree) {
+      const Draft& d = drafts[row < rows ? query : 0];
+      const int o = token - t.before;
+      bits = bits_between(token, 0, t.before);
+      if (o > -4) {
+        const int w = o >> 5, shift = o & 31;
+        const uint32_t m0 = w >= 0 && w < 2 * kDraftWords ? d.mask[w] : 0u;
+        const uint32_t m1 = w >= -1 && w + 1 < 2 * kDraftWords ? d.mask[w + 1] : 0u;
+        bits |= static_cast<uint32_t>((static_cast<unsigned long long>(m1) << 32 | m0) >> shift);
+      }
+      bits &= bits_between(token, d.from, token + 4);
+    } else {
+      const int place = t.before + query;
+      bits = bits_between(token, a.window ? place - a.window + 1 : 0, place + 1);
+    }
+    seen |= (row < rows ? bits & 15u : 0u) << (4 * i);
+  }
+  return seen;
+}
+
+// exp(scores - sums) of one tile and chunk, s[j][i] of row 4 g + i and token 4 c + j,
+// added up over the rows.
+__device__ __forceinline__ void add_rows(float (&sums)[4], const f32x4 (&s)[4], f32x4 top, float scale_log2) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = __builtin_amdgcn_exp2f(fmaf(s[j][i], scale_log2, -top[i]));
+    sums[j] += (p[0] + p[1]) + (p[2] + p[3]);
+  }
+}
+__device__ __forceinline__ void add_seen_rows(float (&sums)[4], const f32x4 (&s)[4], f32x4 top, float scale_log2,
+                                              uint32_t seen) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[i] = __builtin_amdgcn_exp2f(fmaf(s[j][i], scale_log2, -top[i]));
+      if (!(seen >> (4 * i + j) & 1u)) p[i] = 0.f;
+    }
+    sums[j] += (p[0] + p[1]) + (p[2] + p[3]);
+  }
+}
+
+// Where lane (g, c) finds its part of the keys, and the mass of token 4 c + g, of a chunk.
+template <int D>
+struct MassReader {
+  Reader<D> keys;
+  float* mass;          // of page 0
+  int64_t mass_stride;  // from one page to the next
+
+  __device__ __forceinline__ int page(int base) const { return keys.page_at(base + 16 * ((lane_id() & 15) >> 2)); }
+  __device__ __forceinline__ void load(Keys<D>& k, int page, int base) const { keys.load(k, Pages{page, page}, base); }
+  // (of page 0 where there is none: it is not written)
+  __device__ __forceinline__ float* at(int page, int base) const {
+    const int lane = lane_id();
+    const int in = (base + 4 * (lane & 15) + (lane >> 4)) & ((1 << keys.shift) - 1);
+    return mass + (page < 0 ? 0 : page) * mass_stride + in;
+  }
+};
+template <int D>
+__device__ __forceinline__ MassReader<D> mass_reader_of(const MassArgs& m, int seq, int kv_head) {
+  const int shift = m.a.cache.page_shift;
+  return MassReader<D>{reader_of<D>(m.a, seq, kv_head), m.mass + (static_cast<int64_t>(kv_head) << shift),
+                       static_cast<int64_t>(m.a.cache.kv_heads) << shift};
+}
+
+// Of a lane's joined sums, that of token 4 c + g.
+__device__ __forceinline__ float of_group(const float (&sums)[4]) {
+  const int g = lane_id() >> 4;
+  const float low = g & 1 ? sums[1] : sums[0], high = g & 1 ? sums[3] : sums[2];
+  return g & 2 ? high : low;
+}
+
+// At most T tiles of rows.
+template <int D, int V, int T>
+__global__ __launch_bounds__(kMassThreads, T == 1 ? 4 : 2) void kv_mass_kernel(MassArgs m) {
   const SumArgs& a = m.a;
   const int wave = wave_index(), lane = lane_id(), g = lane >> 4, c = lane & 15;
   const int kv_head = static_cast<int>(blockIdx.x);
   const int seq = sequence_at(a, static_cast<int>(blockIdx.z));
+  const MassReader<D> reader = mass_reader_of<D>(m, seq, kv_head);
+  const int step = kMassWaves * static_cast<int>(gridDim.y);
+  int chunk = static_cast<int>(blockIdx.y) * kMassWaves + wave;
+  int page = -1;
+  if (!a.window) page = reader.page(chunk * kChunk);  // beside the lengths
   RowTile t;
   if (!tile_of<V>(a, seq, 0, t, true)) return;
-  const Reader<D> reader = reader_of<D>(a, seq, kv_head);
   const int length = t.before + t.queries;
   const int end = (length + kChunk - 1) / kChunk;
+  chunk += t.chunk0;
+  if (t.chunk0 + static_cast<int>(blockIdx.y) * kMassWaves >= end) return;  // the whole workgroup
+  if (a.window) page = reader.page(chunk * kChunk);
 
-  __shared__ Draft drafts[V == kTree ? 64 * kDraftWords : 1];
-  if constexpr (V == kTree) {
-    stage_drafts(a, t, drafts, t.query1 + 1, kMassWaves * kWave);
-    __syncthreads();
+  // (loads without conditions: past the last chunk the last one's once more)
+  const auto upto = [&](int at) { return at < end ? at : end - 1; };
+  Keys<D> keys;
+  reader.load(keys, page, upto(chunk) * kChunk);
+  float old = *reader.at(page, upto(chunk) * kChunk);
+  int ahead = reader.page(upto(chunk + step) * kChunk);
+
+  __shared__ u32x4 q[T * (D / 32)][kWave];
+  __shared__ f32x4 tops[T * 4];
+  __shared__ Draft drafts[V == kTree ? T * kTile : 1];
+  for (int f = wave; f < T * (D / 32); f += kMassWaves) {
+    const int row = (f / (D / 32)) * kTile + c;
+    u32x4 w = {0, 0, 0, 0};
+    if (row < t.rows) {
+      const RowOf at = row_of(a, 0, 0, row);
+      w = load16(a.q + static_cast<int64_t>(t.start + at.query) * a.ldq + (kv_head * a.group + at.head) * D +
+                 g * (D / 4) + 8 * (f % (D / 32)));
+    }
+    q[f][lane] = w;
   }
+  for (int row = static_cast<int>(threadIdx.x); row < T * kTile; row += kMassThreads) {
+    float top = INFINITY;
+    if (row < t.rows) {
+      const RowOf at = row_of(a, 0, 0, row);
+      top = relative_to(a.lse[static_cast<int64_t>(t.start + at.query) * a.ldl + kv_head * a.group + at.head]);
+    }
+    reinterpret_cast<float*>(tops)[row] = top;
+  }
+  if constexpr (V == kTree) stage_drafts(a, t, drafts, T * kTile, kMassThreads);
+  __syncthreads();
 
-  const int step = kMassWaves * static_cast<int>(gridDim.y);
-  for (int chunk = t.first / kChunk + static_cast<int>(blockIdx.y) * kMassWaves + wave; chunk < end; chunk += step) {
+  for (; chunk < end; chunk += step) {
     const int base = chunk * kChunk;
-    const Pages pages = reader.pages(base);
-    Keys<D> keys;
-    reader.load(keys, pages, base);
-    bf16x8 k[4][D / 32];
+    f32x4 s[T][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int i = 0; i < D / 32; ++i) {
+      bf16x8 rows[T];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i)
-        k[j][i] = __builtin_bit_cast(bf16x8, word_to_bf16(keys.w[j][i], __uint_as_float(byte_scale(keys.scales, j))));
+      for (int r = 0; r < T; ++r) rows[r] = __builtin_bit_cast(bf16x8, q[r * (D / 32) + i][lane]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bf16x8 k = __builtin_bit_cast(bf16x8, word_to_bf16(keys.w[j][i], __uint_as_float(byte_scale(keys.scales, j))));
+#pragma unroll
+        for (int r = 0; r < T; ++r) s[r][j] = mfma(rows[r], k, i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : s[r][j]);
+      }
+    }
+    // the next chunk's keys and mass, and the page of the one after it
+    const int now = page, next = upto(chunk + step) * kChunk;
+    const float before = old;
+    page = ahead;
+    reader.load(keys, page, next);
+    old = *reader.at(page, next);
+    ahead = reader.page(upto(chunk + 2 * step) * kChunk);
 
-    // The rows that see some of the chunk.
+    float sums[4] = {0.f, 0.f, 0.f, 0.f};
+    const bool masked = base < t.all_first || base + kChunk > t.all_last;
+#pragma unroll
+    for (int r = 0; r < T; ++r) {
+      const f32x4 top = tops[4 * r + g];
+      if (masked) {
+        // (16 r + row < 64 + group: row_of's bound)
+        const uint32_t seen = seen_by_rows<V>(a, t, drafts, base, (r * kTile) / a.group, (r * kTile) % a.group, t.rows - r * kTile);
+        add_seen_rows(sums, s[r], top, m.scale_log2, seen);
+      } else {
+        add_rows(sums, s[r], top, m.scale_log2);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sums[j] = over_groups(sums[j]);
+    const float drawn = of_group(sums);
+    const int token = base + 4 * c + g;
+    if (token < length && now >= 0) *reader.at(now, base) = token >= t.before ? drawn : before + drawn;
+  }
+}
+
+// Any number of rows: each of the workgroup's waves has the keys of one of four chunks,
+// and takes every second pair of row tiles; tiles come by in shared memory, staged as
+// the matrix unit's operands two steps' tiles at a time.
+template <int D, int V>
+__global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs m) {
+  constexpr int kSteps = D / 32;
+  constexpr int kChunks = kMassWaves / kHalves;  // of a workgroup
+  const SumArgs& a = m.a;
+  const int wave = wave_index(), lane = lane_id(), g = lane >> 4, c = lane & 15;
+  const int half = wave / kChunks;
+  const int kv_head = static_cast<int>(blockIdx.x);
+  const int seq = sequence_at(a, static_cast<int>(blockIdx.z));
+  RowTile t;
+  if (!tile_of<V>(a, seq, 0, t, true)) return;
+  const int length = t.before + t.queries;
+  const int end = (length + kChunk - 1) / kChunk;
+  const MassReader<D> reader = mass_reader_of<D>(m, seq, kv_head);
+
+  __shared__ u32x4 q[2][kHalves * kStageTiles][kSteps][kWave];
+  __shared__ float tops[2][kStageRows];
+  __shared__ float joined[kChunks][kWave];
+  __shared__ Draft drafts[V == kTree ? 64 * kDraftWords : 1];
+  if constexpr (V == kTree) stage_drafts(a, t, drafts, t.query1 + 1, kMassThreads);  // (a barrier comes below)
+
+  for (int first = t.chunk0 + static_cast<int>(blockIdx.y) * kChunks; first < end;
+       first += kChunks * static_cast<int>(gridDim.y)) {
+    const int chunk = first + wave % kChunks, base = chunk * kChunk;
+    const bool mine = chunk < end;
+    const int loaded = mine ? base : (end - 1) * kChunk;
+    const int page = reader.page(loaded);
+    Keys<D> keys;
+    reader.load(keys, page, loaded);
+
+    // The rows that see some of these chunks; tiles are counted from the first of them on.
     int from = 0, to = t.rows;
     if constexpr (V != kTree) {
-      const int q0 = base - t.before;  // the first query that sees the chunk's first token
+      const int q0 = first * kChunk - t.before;  // the first query that sees their first token
       from = q0 > t.query1 ? t.rows : (q0 > 0 ? q0 * a.group : 0);
       if (a.window) {
-        const int64_t q1 = static_cast<int64_t>(base) + kChunk - 1 + a.window - t.before;  // and past the last
+        const int64_t q1 = static_cast<int64_t>(first + kChunks) * kChunk - 1 + a.window - t.before;  // past the last
         to = q1 <= 0 ? 0 : (q1 * a.group < to ? static_cast<int>(q1 * a.group) : to);
       }
     }
-    Span at;
-    at.base = base;
-    at.window = a.window;
-    at.ok = pages.v >= 0;
-    float sums[16];
+    const auto stage = [&](int buffer, int row0) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sums[i] = 0.f;
-    for (int row0 = from & ~(kTile - 1); row0 < to; row0 += kTile) {
-      const int query0 = row0 / a.group, head0 = row0 - query0 * a.group;
-      const RowOf row = row_of(a, query0, head0, c);
-      const bool there = row0 + c < t.rows;
-      float lse = -INFINITY;
-      bf16x8 q[D / 32];
-      const int64_t token = t.start + (there ? row.query : 0);
-      const int head = kv_head * a.group + (there ? row.head : 0);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        u32x4 w = load16(a.q + token * a.ldq + head * D + g * (D / 4) + 8 * i);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] ^= a.sign;
-        q[i] = __builtin_bit_cast(bf16x8, w);
+      for (int f = 0; f < kHalves * kStageTiles * kSteps / kMassWaves; ++f) {
+        const int at = f * kMassWaves + wave, tile = at / kSteps, i = at % kSteps;
+        int row = row0 + tile * kTile + c;
+        row = row < t.rows ? row : t.rows - 1;
+        const int query = row / a.group, head = row - query * a.group;
+        load16_to_lds(a.q + static_cast<int64_t>(t.start + query) * a.ldq + (kv_head * a.group + head) * D + g * (D / 4) + 8 * i,
+                      &q[buffer][tile][i][0]);
       }
-      lse = a.lse[token * a.ldl + head];
-      f32x4 s[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) s[j] = mfma(k[j][i], q[i], s[j]);
+      if (wave == 0) {
+        const int row = row0 + lane;
+        const int query = (row < to ? row : t.rows - 1) / a.group, head = (row < to ? row : t.rows - 1) - query * a.group;
+        const float lse = a.lse[static_cast<int64_t>(t.start + query) * a.ldl + kv_head * a.group + head];
+        tops[buffer][lane] = row < to ? relative_to(lse) : INFINITY;
       }
-      const bool counts = there && lse != -INFINITY;
-      uint32_t seen = 0;
-      if constexpr (V == kTree) seen = seen_bits(at, drafts[there ? row.query : 0], t.before);
-      else seen = seen_bits(at, t.before + row.query);
-      if (!counts) seen = 0;
-      const float top = lse * 1.44269504f;
+    };
+    int row0 = from;
+    if (row0 < to) stage(0, row0);
+    bf16x8 k[4][kSteps];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(s[j][i], a.scale_log2, -top));
-          sums[4 * i + j] += seen >> (4 * i + j) & 1u ? p : 0.f;
+      for (int i = 0; i < kSteps; ++i)
+        k[j][i] = __builtin_bit_cast(bf16x8, word_to_bf16(keys.w[j][i], __uint_as_float(byte_scale(keys.scales, j))));
+    float sums[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int buffer = 0; row0 < to; row0 += kStageRows, buffer ^= 1) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's part of the tiles is there
+      __syncthreads();
+      if (row0 + kStageRows < to) stage(buffer ^ 1, row0 + kStageRows);
+      if (!mine) continue;
+#pragma unroll 1
+      for (int n = 0; n < kStageTiles; ++n) {
+        const int tile = half * kStageTiles + n, tile0 = row0 + tile * kTile;
+        if (tile0 >= to) break;
+        f32x4 s[4];
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const bf16x8 rows = __builtin_bit_cast(bf16x8, q[buffer][tile][i][lane]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[j] = mfma(rows, k[j][i], i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : s[j]);
         }
+        const f32x4 top = *reinterpret_cast<const f32x4*>(&tops[buffer][tile * kTile + 4 * g]);
+        const int query0 = tile0 / a.group, last = (tile0 + kTile - 1) / a.group;
+        bool masked;
+        if constexpr (V == kTree) masked = base < t.all_first || base + kChunk > t.all_last;
+        else masked = base + kChunk > t.before + query0 + 1 || (a.window && base <= t.before + last - a.window);
+        if (masked)
+          add_seen_rows(sums, s, top, m.scale_log2,
+                        seen_by_rows<V>(a, t, drafts, base, query0, tile0 - query0 * a.group, to - tile0));
+        else
+          add_rows(sums, s, top, m.scale_log2);
+      }
     }
-    const float drawn = join_group(sums);
-    const int token = base + lane;
-    if (token < length && pages.v >= 0) {
-      float* at_mass = m.mass + ((static_cast<int64_t>(pages.v) * a.cache.kv_heads + kv_head) << reader.shift) +
-                       (token & ((1 << reader.shift) - 1));
-      *at_mass = token >= t.before ? drawn : *at_mass + drawn;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sums[j] = over_groups(sums[j]);
+    const float drawn = of_group(sums);
+    __syncthreads();
+    if (half == 1) joined[wave % kChunks][lane] = drawn;
+    __syncthreads();
+    const int token = base + 4 * c + g;
+    if (half == 0 && mine && token < length && page >= 0) {
+      float* at = reader.at(page, base);
+      const float all = drawn + joined[wave][lane];
+      *at = token >= t.before ? all : *at + all;
     }
   }
+}
+
+template <int D, int V>
+static void launch_mass(const MassArgs& m, int num_seqs, hipStream_t stream) {
+  const int heads = m.a.cache.kv_heads;
+  const int64_t rows = static_cast<int64_t>(m.a.max_query_len) * m.a.group;
+  const int64_t units = static_cast<int64_t>(num_seqs) * heads;
+  // tokens that a sequence's rows see, and its own
+  int64_t longest = m.a.max_seq_len;
+  if (m.a.window) {
+    const int64_t seen = static_cast<int64_t>(m.a.window) + m.a.max_query_len + kChunk;
+    longest = longest < seen ? longest : seen;
+  }
+  const int64_t chunks = (longest + kChunk - 1) / kChunk;
+  const bool few = rows <= kMostTiles * kTile;
+  // As many workgroups as the device holds, and several times that of those whose lengths differ in
+  // rows as well.
+  const int64_t most = few ? (chunks + kMassWaves - 1) / kMassWaves : (chunks * kHalves + kMassWaves - 1) / kMassWaves;
+  int64_t groups = ((few ? 2 : 16) * kCus + units - 1) / units;
+  groups = groups < most ? groups : most;
+  const dim3 grid(heads, static_cast<unsigned>(groups), num_seqs), block(kMassThreads);
+  if (rows <= kTile) hipLaunchKernelGGL((kv_mass_kernel<D, V, 1>), grid, block, 0, stream, m);
+  else if (rows <= 2 * kTile) hipLaunchKernelGGL((kv_mass_kernel<D, V, 2>), grid, block, 0, stream, m);
+  else if (few) hipLaunchKernelGGL((kv_mass_kernel<D, V, kMostTiles>), grid, block, 0, stream, m);
+  else hipLaunchKernelGGL((kv_mass_rows_kernel<D, V>), grid, block, 0, stream, m);
 }
 
 hipError_t launch_kv_attention_mass(const uint16_t* q, int64_t ldq, const float* lse, int64_t ldl,
@@ -144,25 +378,19 @@ hipError_t launch_kv_attention_mass(const uint16_t* q, int64_t ldq, const float*
   if (window >= max_seq_len) window = 0;
   MassArgs m;
   m.a = SumArgs{{q, query_start, seq_lens, page_table, nullptr,
-                      {cache, num_pages, page_shift, kv_heads},
-                      ldq, 0, ld_table, num_tokens, max_query_len, max_seq_len, q_heads, window,
-                      fabsf(scale) * 1.44269504f, scale < 0.f ? 0x80008000u : 0u,
-                      group, ((1 << 21) + group - 1) / group,
-                      1, 1, 0, 0, nullptr, nullptr},
-                      masks, words, const_cast<float*>(lse), ldl};
+                 {cache, num_pages, page_shift, kv_heads},
+                 ldq, 0, ld_table, num_tokens, max_query_len, max_seq_len, q_heads, window,
+                 0.f, 0u, group, ((1 << 21) + group - 1) / group,
+                 1, 1, 0, 0, nullptr, nullptr},
+                masks, words, const_cast<float*>(lse), ldl};
   m.mass = mass;
-  const int64_t chunks = (static_cast<int64_t>(max_seq_len) + kChunk - 1) / kChunk;
-  int64_t groups = (chunks + kMassWaves - 1) / kMassWaves;
-  // enough workgroups to fill the device a few times over; beyond that each takes several chunks
-  const int64_t most = (8 * kCus + static_cast<int64_t>(num_seqs) * kv_heads - 1) / (static_cast<int64_t>(num_seqs) * kv_heads);
-  groups = groups < most ? groups : most;
-  const dim3 grid(kv_heads, static_cast<unsigned>(groups), num_seqs), block(kMassWaves * kWave);
+  m.scale_log2 = fminf(fmaxf(scale * kLog2e, -3.402823466e38f), 3.402823466e38f);
   if (masks) {
-    if (head_dim == 64) hipLaunchKernelGGL((kv_mass_kernel<64, kTree>), grid, block, 0, stream, m);
-    else hipLaunchKernelGGL((kv_mass_kernel<128, kTree>), grid, block, 0, stream, m);
+    if (head_dim == 64) launch_mass<64, kTree>(m, num_seqs, stream);
+    else launch_mass<128, kTree>(m, num_seqs, stream);
   } else {
-    if (head_dim == 64) hipLaunchKernelGGL((kv_mass_kernel<64, kPlain>), grid, block, 0, stream, m);
-    else hipLaunchKernelGGL((kv_mass_kernel<128, kPlain>), grid, block, 0, stream, m);
+    if (head_dim == 64) launch_mass<64, kPlain>(m, num_seqs, stream);
+    else launch_mass<128, kPlain>(m, num_seqs, stream);
   }
   return hipGetLastError();
 }
