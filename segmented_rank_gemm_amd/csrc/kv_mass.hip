@@ -22,10 +22,9 @@ namespace lora {
 
 constexpr int kMassWaves = 8;
 constexpr int kMassThreads = kMassWaves * kWave;
-constexpr int kMostTiles = 4;      // of 16 rows, for the kernel of few
+constexpr int kFewTiles = 8;       // of 16 rows, at most, for the kernel of few
 constexpr int kHalves = 2;         // of the rows, for that of many: waves that share a chunk
-constexpr int kStageTiles = 2;     // tiles of a half that are staged at a time
-constexpr int kStageRows = kHalves * kStageTiles * kTile;
+constexpr int kBuffers = 3;        // of staged tiles: two steps' on their way
 constexpr float kLog2e = 1.44269504f;
 
 struct MassArgs {
@@ -135,9 +134,10 @@ __device__ __forceinline__ float of_group(const float (&sums)[4]) {
   return g & 2 ? high : low;
 }
 
-// At most T tiles of rows.
+// One tile of rows (T = 1), or up to T.
 template <int D, int V, int T>
-__global__ __launch_bounds__(kMassThreads, T == 1 ? 4 : 2) void kv_mass_kernel(MassArgs m) {
+__global__ __launch_bounds__(kMassThreads, 4) void kv_mass_kernel(MassArgs m) {
+  constexpr int kSteps = D / 32;
   const SumArgs& a = m.a;
   const int wave = wave_index(), lane = lane_id(), g = lane >> 4, c = lane & 15;
   const int kv_head = static_cast<int>(blockIdx.x);
@@ -145,37 +145,56 @@ __global__ __launch_bounds__(kMassThreads, T == 1 ? 4 : 2) void kv_mass_kernel(M
   const MassReader<D> reader = mass_reader_of<D>(m, seq, kv_head);
   const int step = kMassWaves * static_cast<int>(gridDim.y);
   int chunk = static_cast<int>(blockIdx.y) * kMassWaves + wave;
-  int page = -1;
-  if (!a.window) page = reader.page(chunk * kChunk);  // beside the lengths
+  int first_page = -1;
+  if (!a.window) first_page = reader.page(chunk * kChunk);  // beside the lengths
   RowTile t;
   if (!tile_of<V>(a, seq, 0, t, true)) return;
   const int length = t.before + t.queries;
   const int end = (length + kChunk - 1) / kChunk;
   chunk += t.chunk0;
   if (t.chunk0 + static_cast<int>(blockIdx.y) * kMassWaves >= end) return;  // the whole workgroup
-  if (a.window) page = reader.page(chunk * kChunk);
+  if (a.window) first_page = reader.page(chunk * kChunk);
 
-  // (loads without conditions: past the last chunk the last one's once more)
-  const auto upto = [&](int at) { return at < end ? at : end - 1; };
-  Keys<D> keys;
-  reader.load(keys, page, upto(chunk) * kChunk);
-  float old = *reader.at(page, upto(chunk) * kChunk);
-  int ahead = reader.page(upto(chunk + step) * kChunk);
+  // What a wave has on its way, with one tile: two chunks' keys, and the mass of their
+  // tokens; with several, whose products take longer, the next chunk's page.  (Loads
+  // without conditions: past the last chunk the last one's once more.)
+  struct Ahead {
+    Keys<D> keys;
+    float mass;
+    int page;
+  };
+  const auto base_of = [&](int at) { return (at < end ? at : end - 1) * kChunk; };
+  const auto fetch = [&](Ahead& x, int page, int at) {
+    x.page = page;
+    reader.load(x.keys, page, base_of(at));
+    x.mass = *reader.at(page, base_of(at));
+  };
+  Ahead ahead[2];
+  int pages[2];  // of the chunks after those
+  fetch(ahead[0], first_page, chunk);
+  if constexpr (T == 1) {
+    fetch(ahead[1], reader.page(base_of(chunk + step)), chunk + step);
+    pages[0] = reader.page(base_of(chunk + 2 * step));
+    pages[1] = reader.page(base_of(chunk + 3 * step));
+  } else {
+    pages[0] = reader.page(base_of(chunk + step));
+  }
 
-  __shared__ u32x4 q[T * (D / 32)][kWave];
+  const int tiles = (t.rows + kTile - 1) / kTile;
+  __shared__ u32x4 q[T * kSteps][kWave];
   __shared__ f32x4 tops[T * 4];
   __shared__ Draft drafts[V == kTree ? T * kTile : 1];
-  for (int f = wave; f < T * (D / 32); f += kMassWaves) {
-    const int row = (f / (D / 32)) * kTile + c;
+  for (int f = wave; f < tiles * kSteps; f += kMassWaves) {
+    const int row = (f / kSteps) * kTile + c;
     u32x4 w = {0, 0, 0, 0};
     if (row < t.rows) {
       const RowOf at = row_of(a, 0, 0, row);
       w = load16(a.q + static_cast<int64_t>(t.start + at.query) * a.ldq + (kv_head * a.group + at.head) * D +
-                 g * (D / 4) + 8 * (f % (D / 32)));
+                 g * (D / 4) + 8 * (f % kSteps));
     }
     q[f][lane] = w;
   }
-  for (int row = static_cast<int>(threadIdx.x); row < T * kTile; row += kMassThreads) {
+  for (int row = static_cast<int>(threadIdx.x); row < tiles * kTile; row += kMassThreads) {
     float top = INFINITY;
     if (row < t.rows) {
       const RowOf at = row_of(a, 0, 0, row);
@@ -183,50 +202,80 @@ __global__ __launch_bounds__(kMassThreads, T == 1 ? 4 : 2) void kv_mass_kernel(M
     }
     reinterpret_cast<float*>(tops)[row] = top;
   }
-  if constexpr (V == kTree) stage_drafts(a, t, drafts, T * kTile, kMassThreads);
+  if constexpr (V == kTree) stage_drafts(a, t, drafts, tiles * kTile, kMassThreads);
   __syncthreads();
 
-  for (; chunk < end; chunk += step) {
-    const int base = chunk * kChunk;
-    f32x4 s[T][4];
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      bf16x8 rows[T];
-#pragma unroll
-      for (int r = 0; r < T; ++r) rows[r] = __builtin_bit_cast(bf16x8, q[r * (D / 32) + i][lane]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bf16x8 k = __builtin_bit_cast(bf16x8, word_to_bf16(keys.w[j][i], __uint_as_float(byte_scale(keys.scales, j))));
-#pragma unroll
-        for (int r = 0; r < T; ++r) s[r][j] = mfma(rows[r], k, i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : s[r][j]);
-      }
+  // Adds up one tile's rows.
+  const auto add = [&](float (&sums)[4], const f32x4 (&s)[4], int base, bool masked, int n) {
+    const f32x4 top = tops[4 * n + g];
+    if (masked) {
+      const int query0 = n * kTile / a.group;
+      add_seen_rows(sums, s, top, m.scale_log2,
+                    seen_by_rows<V>(a, t, drafts, base, query0, n * kTile - query0 * a.group, t.rows - n * kTile));
+    } else {
+      add_rows(sums, s, top, m.scale_log2);
     }
-    // the next chunk's keys and mass, and the page of the one after it
-    const int now = page, next = upto(chunk + step) * kChunk;
-    const float before = old;
-    page = ahead;
-    reader.load(keys, page, next);
-    old = *reader.at(page, next);
-    ahead = reader.page(upto(chunk + 2 * step) * kChunk);
-
-    float sums[4] = {0.f, 0.f, 0.f, 0.f};
-    const bool masked = base < t.all_first || base + kChunk > t.all_last;
-#pragma unroll
-    for (int r = 0; r < T; ++r) {
-      const f32x4 top = tops[4 * r + g];
-      if (masked) {
-        // (16 r + row < 64 + group: row_of's bound)
-        const uint32_t seen = seen_by_rows<V>(a, t, drafts, base, (r * kTile) / a.group, (r * kTile) % a.group, t.rows - r * kTile);
-        add_seen_rows(sums, s[r], top, m.scale_log2, seen);
-      } else {
-        add_rows(sums, s[r], top, m.scale_log2);
-      }
-    }
+  };
+  const auto store = [&](float (&sums)[4], int base, int page, float before) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) sums[j] = over_groups(sums[j]);
     const float drawn = of_group(sums);
     const int token = base + 4 * c + g;
-    if (token < length && now >= 0) *reader.at(now, base) = token >= t.before ? drawn : before + drawn;
+    if (token < length && page >= 0) *reader.at(page, base) = token >= t.before ? drawn : before + drawn;
+  };
+  const auto key = [&](const Keys<D>& keys, int i, int j) {
+    return __builtin_bit_cast(bf16x8, word_to_bf16(keys.w[j][i], __uint_as_float(byte_scale(keys.scales, j))));
+  };
+  if constexpr (T == 1) {
+    const auto take = [&](Ahead& x, int& next_page) {
+      const int base = chunk * kChunk, page = x.page;
+      const float before = x.mass;
+      f32x4 s[4];
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const bf16x8 rows = __builtin_bit_cast(bf16x8, q[i][lane]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          s[j] = mfma(rows, key(x.keys, i, j), i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : s[j]);
+      }
+      fetch(x, next_page, chunk + 2 * step);
+      next_page = reader.page(base_of(chunk + 4 * step));
+      float sums[4] = {0.f, 0.f, 0.f, 0.f};
+      add(sums, s, base, base < t.all_first || base + kChunk > t.all_last, 0);
+      store(sums, base, page, before);
+      chunk += step;
+    };
+    while (chunk < end) {
+      take(ahead[0], pages[0]);
+      if (chunk >= end) break;
+      take(ahead[1], pages[1]);
+    }
+  } else {
+    for (; chunk < end; chunk += step) {
+      const int base = chunk * kChunk, page = ahead[0].page;
+      const float before = ahead[0].mass;
+      bf16x8 k[4][kSteps];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) k[j][i] = key(ahead[0].keys, i, j);
+      float sums[4] = {0.f, 0.f, 0.f, 0.f};
+      const bool masked = base < t.all_first || base + kChunk > t.all_last;
+#pragma unroll 1
+      for (int n = 0; n < tiles; ++n) {
+        f32x4 s[4];
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const bf16x8 rows = __builtin_bit_cast(bf16x8, q[n * kSteps + i][lane]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[j] = mfma(rows, k[j][i], i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : s[j]);
+        }
+        add(sums, s, base, masked, n);
+      }
+      store(sums, base, page, before);
+      fetch(ahead[0], pages[0], chunk + step);
+      pages[0] = reader.page(base_of(chunk + 2 * step));
+    }
   }
 }
 
@@ -237,6 +286,10 @@ template <int D, int V>
 __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs m) {
   constexpr int kSteps = D / 32;
   constexpr int kChunks = kMassWaves / kHalves;  // of a workgroup
+  // Tiles of a half that are staged at a time (beside a tree's masks there is room for one,
+  // if two workgroups are to share a compute unit).
+  constexpr int kStageTiles = V == kTree && D == 128 ? 1 : 2;
+  constexpr int kStageRows = kHalves * kStageTiles * kTile;
   const SumArgs& a = m.a;
   const int wave = wave_index(), lane = lane_id(), g = lane >> 4, c = lane & 15;
   const int half = wave / kChunks;
@@ -248,8 +301,8 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs 
   const int end = (length + kChunk - 1) / kChunk;
   const MassReader<D> reader = mass_reader_of<D>(m, seq, kv_head);
 
-  __shared__ u32x4 q[2][kHalves * kStageTiles][kSteps][kWave];
-  __shared__ float tops[2][kStageRows];
+  __shared__ u32x4 q[kBuffers][kHalves * kStageTiles][kSteps][kWave];
+  __shared__ float tops[kBuffers][kStageRows];
   __shared__ float joined[kChunks][kWave];
   __shared__ Draft drafts[V == kTree ? 64 * kDraftWords : 1];
   if constexpr (V == kTree) stage_drafts(a, t, drafts, t.query1 + 1, kMassThreads);  // (a barrier comes below)
@@ -273,25 +326,39 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs 
         to = q1 <= 0 ? 0 : (q1 * a.group < to ? static_cast<int>(q1 * a.group) : to);
       }
     }
+    // Steps of kStageRows rows, each wave's part of one kLoads loads.  The rows' sums go
+    // by a register of the first wave, a step later than asked for.  (Past the last step
+    // the last row's once more, which nobody reads.)
+    constexpr int kLoads = kHalves * kStageTiles * kSteps / kMassWaves;
+    float lse = 0.f;
+    const auto ask = [&](int row0) {
+      if (wave != 0) return;
+      const int first_row = row0 < t.rows ? row0 : t.rows - 1, left = t.rows - 1 - first_row;
+      const int query0 = first_row / a.group;
+      const RowOf at = row_of(a, query0, first_row - query0 * a.group, lane < left ? lane : left);
+      lse = a.lse[static_cast<int64_t>(t.start + at.query) * a.ldl + kv_head * a.group + at.head];
+    };
+    const auto put = [&](int buffer, int row0) {
+      if (wave == 0 && lane < kStageRows) tops[buffer][lane] = row0 + lane < to ? relative_to(lse) : INFINITY;
+    };
     const auto stage = [&](int buffer, int row0) {
+      const int first_row = row0 < t.rows ? row0 : t.rows - 1, left = t.rows - 1 - first_row;
+      const int query0 = first_row / a.group, head0 = first_row - query0 * a.group;
 #pragma unroll
-      for (int f = 0; f < kHalves * kStageTiles * kSteps / kMassWaves; ++f) {
+      for (int f = 0; f < kLoads; ++f) {
         const int at = f * kMassWaves + wave, tile = at / kSteps, i = at % kSteps;
-        int row = row0 + tile * kTile + c;
-        row = row < t.rows ? row : t.rows - 1;
-        const int query = row / a.group, head = row - query * a.group;
-        load16_to_lds(a.q + static_cast<int64_t>(t.start + query) * a.ldq + (kv_head * a.group + head) * D + g * (D / 4) + 8 * i,
+        const int row = tile * kTile + c;
+        const RowOf of = row_of(a, query0, head0, row < left ? row : left);
+        load16_to_lds(a.q + static_cast<int64_t>(t.start + of.query) * a.ldq + (kv_head * a.group + of.head) * D + g * (D / 4) + 8 * i,
                       &q[buffer][tile][i][0]);
-      }
-      if (wave == 0) {
-        const int row = row0 + lane;
-        const int query = (row < to ? row : t.rows - 1) / a.group, head = (row < to ? row : t.rows - 1) - query * a.group;
-        const float lse = a.lse[static_cast<int64_t>(t.start + query) * a.ldl + kv_head * a.group + head];
-        tops[buffer][lane] = row < to ? relative_to(lse) : INFINITY;
       }
     };
     int row0 = from;
-    if (row0 < to) stage(0, row0);
+    ask(row0);
+    stage(0, row0);
+    put(0, row0);
+    ask(row0 + kStageRows);
+    stage(1, row0 + kStageRows);
     bf16x8 k[4][kSteps];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -299,10 +366,17 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs 
       for (int i = 0; i < kSteps; ++i)
         k[j][i] = __builtin_bit_cast(bf16x8, word_to_bf16(keys.w[j][i], __uint_as_float(byte_scale(keys.scales, j))));
     float sums[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int buffer = 0; row0 < to; row0 += kStageRows, buffer ^= 1) {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's part of the tiles is there
+    for (int buffer = 0; row0 < to; row0 += kStageRows) {
+      const int next = buffer + 1 < kBuffers ? buffer + 1 : 0, after = next + 1 < kBuffers ? next + 1 : 0;
+      put(next, row0 + kStageRows);
+      // this wave's part of this step's tiles is there; the next step's loads may still be out
+      if constexpr (kLoads == 2) asm volatile("s_waitcnt vmcnt(2)" ::: "memory");
+      else asm volatile("s_waitcnt vmcnt(1)" ::: "memory");
       __syncthreads();
-      if (row0 + kStageRows < to) stage(buffer ^ 1, row0 + kStageRows);
+      ask(row0 + 2 * kStageRows);
+      stage(after, row0 + 2 * kStageRows);
+      const int now = buffer;
+      buffer = next;
       if (!mine) continue;
 #pragma unroll 1
       for (int n = 0; n < kStageTiles; ++n) {
@@ -311,11 +385,11 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs 
         f32x4 s[4];
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-          const bf16x8 rows = __builtin_bit_cast(bf16x8, q[buffer][tile][i][lane]);
+          const bf16x8 rows = __builtin_bit_cast(bf16x8, q[now][tile][i][lane]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[j] = mfma(rows, k[j][i], i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : s[j]);
         }
-        const f32x4 top = *reinterpret_cast<const f32x4*>(&tops[buffer][tile * kTile + 4 * g]);
+        const f32x4 top = *reinterpret_cast<const f32x4*>(&tops[now][tile * kTile + 4 * g]);
         const int query0 = tile0 / a.group, last = (tile0 + kTile - 1) / a.group;
         bool masked;
         if constexpr (V == kTree) masked = base < t.all_first || base + kChunk > t.all_last;
@@ -330,6 +404,7 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs 
 #pragma unroll
     for (int j = 0; j < 4; ++j) sums[j] = over_groups(sums[j]);
     const float drawn = of_group(sums);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is on its way to the tiles any more
     __syncthreads();
     if (half == 1) joined[wave % kChunks][lane] = drawn;
     __syncthreads();
@@ -354,7 +429,7 @@ static void launch_mass(const MassArgs& m, int num_seqs, hipStream_t stream) {
     longest = longest < seen ? longest : seen;
   }
   const int64_t chunks = (longest + kChunk - 1) / kChunk;
-  const bool few = rows <= kMostTiles * kTile;
+  const bool few = rows <= kFewTiles * kTile;
   // As many workgroups as the device holds, and several times that of those whose lengths differ in
   // rows as well.
   const int64_t most = few ? (chunks + kMassWaves - 1) / kMassWaves : (chunks * kHalves + kMassWaves - 1) / kMassWaves;
@@ -362,8 +437,7 @@ static void launch_mass(const MassArgs& m, int num_seqs, hipStream_t stream) {
   groups = groups < most ? groups : most;
   const dim3 grid(heads, static_cast<unsigned>(groups), num_seqs), block(kMassThreads);
   if (rows <= kTile) hipLaunchKernelGGL((kv_mass_kernel<D, V, 1>), grid, block, 0, stream, m);
-  else if (rows <= 2 * kTile) hipLaunchKernelGGL((kv_mass_kernel<D, V, 2>), grid, block, 0, stream, m);
-  else if (few) hipLaunchKernelGGL((kv_mass_kernel<D, V, kMostTiles>), grid, block, 0, stream, m);
+  else if (few) hipLaunchKernelGGL((kv_mass_kernel<D, V, kFewTiles>), grid, block, 0, stream, m);
   else hipLaunchKernelGGL((kv_mass_rows_kernel<D, V>), grid, block, 0, stream, m);
 }
 
