@@ -24,14 +24,18 @@ constexpr int kMassWaves = 8;
 constexpr int kMassThreads = kMassWaves * kWave;
 constexpr int kFewTiles = 8;       // of 16 rows, at most, for the kernel of few
 constexpr int kHalves = 2;         // of the rows, for that of many: waves that share a chunk
-constexpr int kBuffers = 3;        // of staged tiles: two steps' on their way
 constexpr float kLog2e = 1.44269504f;
 
 struct MassArgs {
   SumArgs a;
   float* mass;
   float scale_log2;  // scale * log2(e), with its sign
+  uint32_t inverse;  // ceil(2^32 / group): the high half of a product with a row below 2^22 is its query
 };
+
+__device__ __forceinline__ int query_of(const MassArgs& m, int row) {
+  return static_cast<int>(m.a.group == 1 ? static_cast<uint32_t>(row) : __umulhi(static_cast<uint32_t>(row), m.inverse));
+}
 
 // A row's sum as the power that its scores are taken relative to; a row without a sum
 // (or none at all) counts for nothing.
@@ -81,7 +85,7 @@ __device__ __forceinline__ uint32_t seen_by_rows(const AttentionArgs& a, const R
 
 // exp(scores - sums) of one tile and chunk, s[j][i] of row 4 g + i and token 4 c + j,
 // added up over the rows.
-__device__ __forceinline__ void add_rows(float (&sums)[4], const f32x4 (&s)[4], f32x4 top, float scale_log2) {
+__device__ __forceinline__ void add_rows(f32x4& sums, const f32x4 (&s)[4], f32x4 top, float scale_log2) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     float p[4];
@@ -90,7 +94,7 @@ __device__ __forceinline__ void add_rows(float (&sums)[4], const f32x4 (&s)[4], 
     sums[j] += (p[0] + p[1]) + (p[2] + p[3]);
   }
 }
-__device__ __forceinline__ void add_seen_rows(float (&sums)[4], const f32x4 (&s)[4], f32x4 top, float scale_log2,
+__device__ __forceinline__ void add_seen_rows(f32x4& sums, const f32x4 (&s)[4], f32x4 top, float scale_log2,
                                               uint32_t seen) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -128,9 +132,10 @@ __device__ __forceinline__ MassReader<D> mass_reader_of(const MassArgs& m, int s
 }
 
 // Of a lane's joined sums, that of token 4 c + g.
-__device__ __forceinline__ float of_group(const float (&sums)[4]) {
+__device__ __forceinline__ float of_group(const f32x4 sums) {
   const int g = lane_id() >> 4;
-  const float low = g & 1 ? sums[1] : sums[0], high = g & 1 ? sums[3] : sums[2];
+  const float s0 = sums[0], s1 = sums[1], s2 = sums[2], s3 = sums[3];
+  const float low = g & 1 ? s1 : s0, high = g & 1 ? s3 : s2;
   return g & 2 ? high : low;
 }
 
@@ -206,7 +211,7 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_kernel(MassArgs m) {
   __syncthreads();
 
   // Adds up one tile's rows.
-  const auto add = [&](float (&sums)[4], const f32x4 (&s)[4], int base, bool masked, int n) {
+  const auto add = [&](f32x4& sums, const f32x4 (&s)[4], int base, bool masked, int n) {
     const f32x4 top = tops[4 * n + g];
     if (masked) {
       const int query0 = n * kTile / a.group;
@@ -216,7 +221,7 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_kernel(MassArgs m) {
       add_rows(sums, s, top, m.scale_log2);
     }
   };
-  const auto store = [&](float (&sums)[4], int base, int page, float before) {
+  const auto store = [&](f32x4& sums, int base, int page, float before) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) sums[j] = over_groups(sums[j]);
     const float drawn = of_group(sums);
@@ -240,7 +245,7 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_kernel(MassArgs m) {
       }
       fetch(x, next_page, chunk + 2 * step);
       next_page = reader.page(base_of(chunk + 4 * step));
-      float sums[4] = {0.f, 0.f, 0.f, 0.f};
+      f32x4 sums = {0.f, 0.f, 0.f, 0.f};
       add(sums, s, base, base < t.all_first || base + kChunk > t.all_last, 0);
       store(sums, base, page, before);
       chunk += step;
@@ -259,7 +264,7 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_kernel(MassArgs m) {
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) k[j][i] = key(ahead[0].keys, i, j);
-      float sums[4] = {0.f, 0.f, 0.f, 0.f};
+      f32x4 sums = {0.f, 0.f, 0.f, 0.f};
       const bool masked = base < t.all_first || base + kChunk > t.all_last;
 #pragma unroll 1
       for (int n = 0; n < tiles; ++n) {
@@ -301,8 +306,8 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs 
   const int end = (length + kChunk - 1) / kChunk;
   const MassReader<D> reader = mass_reader_of<D>(m, seq, kv_head);
 
-  __shared__ u32x4 q[kBuffers][kHalves * kStageTiles][kSteps][kWave];
-  __shared__ float tops[kBuffers][kStageRows];
+  __shared__ u32x4 q[2][kHalves * kStageTiles][kSteps][kWave];
+  __shared__ float tops[2][kStageRows];
   __shared__ float joined[kChunks][kWave];
   __shared__ Draft drafts[V == kTree ? 64 * kDraftWords : 1];
   if constexpr (V == kTree) stage_drafts(a, t, drafts, t.query1 + 1, kMassThreads);  // (a barrier comes below)
@@ -326,57 +331,50 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs 
         to = q1 <= 0 ? 0 : (q1 * a.group < to ? static_cast<int>(q1 * a.group) : to);
       }
     }
-    // Steps of kStageRows rows, each wave's part of one kLoads loads.  The rows' sums go
-    // by a register of the first wave, a step later than asked for.  (Past the last step
-    // the last row's once more, which nobody reads.)
+    // Steps of kStageRows rows, of whose operands each wave brings kLoads, and the first
+    // one the sums: by registers, since the compiler lets no read of shared memory pass a
+    // load into it.  (Past the last step the last row's once more, which nobody reads.)
     constexpr int kLoads = kHalves * kStageTiles * kSteps / kMassWaves;
+    u32x4 part[kLoads];
     float lse = 0.f;
     const auto ask = [&](int row0) {
-      if (wave != 0) return;
       const int first_row = row0 < t.rows ? row0 : t.rows - 1, left = t.rows - 1 - first_row;
-      const int query0 = first_row / a.group;
-      const RowOf at = row_of(a, query0, first_row - query0 * a.group, lane < left ? lane : left);
-      lse = a.lse[static_cast<int64_t>(t.start + at.query) * a.ldl + kv_head * a.group + at.head];
-    };
-    const auto put = [&](int buffer, int row0) {
-      if (wave == 0 && lane < kStageRows) tops[buffer][lane] = row0 + lane < to ? relative_to(lse) : INFINITY;
-    };
-    const auto stage = [&](int buffer, int row0) {
-      const int first_row = row0 < t.rows ? row0 : t.rows - 1, left = t.rows - 1 - first_row;
-      const int query0 = first_row / a.group, head0 = first_row - query0 * a.group;
+      const int query0 = query_of(m, first_row), head0 = first_row - query0 * a.group;
 #pragma unroll
       for (int f = 0; f < kLoads; ++f) {
-        const int at = f * kMassWaves + wave, tile = at / kSteps, i = at % kSteps;
-        const int row = tile * kTile + c;
+        const int at = f * kMassWaves + wave, row = at / kSteps * kTile + c;
         const RowOf of = row_of(a, query0, head0, row < left ? row : left);
-        load16_to_lds(a.q + static_cast<int64_t>(t.start + of.query) * a.ldq + (kv_head * a.group + of.head) * D + g * (D / 4) + 8 * i,
-                      &q[buffer][tile][i][0]);
+        part[f] = load16(a.q + static_cast<int64_t>(t.start + of.query) * a.ldq + (kv_head * a.group + of.head) * D +
+                         g * (D / 4) + 8 * (at % kSteps));
       }
+      if (wave == 0) {
+        const RowOf of = row_of(a, query0, head0, lane < left ? lane : left);
+        lse = a.lse[static_cast<int64_t>(t.start + of.query) * a.ldl + kv_head * a.group + of.head];
+      }
+    };
+    const auto put = [&](int buffer, int row0) {
+#pragma unroll
+      for (int f = 0; f < kLoads; ++f) {
+        const int at = f * kMassWaves + wave;
+        q[buffer][at / kSteps][at % kSteps][lane] = part[f];
+      }
+      if (wave == 0 && lane < kStageRows) tops[buffer][lane] = row0 + lane < to ? relative_to(lse) : INFINITY;
     };
     int row0 = from;
     ask(row0);
-    stage(0, row0);
     put(0, row0);
     ask(row0 + kStageRows);
-    stage(1, row0 + kStageRows);
     bf16x8 k[4][kSteps];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int i = 0; i < kSteps; ++i)
         k[j][i] = __builtin_bit_cast(bf16x8, word_to_bf16(keys.w[j][i], __uint_as_float(byte_scale(keys.scales, j))));
-    float sums[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int buffer = 0; row0 < to; row0 += kStageRows) {
-      const int next = buffer + 1 < kBuffers ? buffer + 1 : 0, after = next + 1 < kBuffers ? next + 1 : 0;
-      put(next, row0 + kStageRows);
-      // this wave's part of this step's tiles is there; the next step's loads may still be out
-      if constexpr (kLoads == 2) asm volatile("s_waitcnt vmcnt(2)" ::: "memory");
-      else asm volatile("s_waitcnt vmcnt(1)" ::: "memory");
-      __syncthreads();
+    f32x4 sums = {0.f, 0.f, 0.f, 0.f};
+    for (int buffer = 0; row0 < to; row0 += kStageRows, buffer ^= 1) {
+      __syncthreads();  // this step's tiles are there, and the other buffer has been read
+      put(buffer ^ 1, row0 + kStageRows);
       ask(row0 + 2 * kStageRows);
-      stage(after, row0 + 2 * kStageRows);
-      const int now = buffer;
-      buffer = next;
       if (!mine) continue;
 #pragma unroll 1
       for (int n = 0; n < kStageTiles; ++n) {
@@ -385,12 +383,12 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs 
         f32x4 s[4];
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-          const bf16x8 rows = __builtin_bit_cast(bf16x8, q[now][tile][i][lane]);
+          const bf16x8 rows = __builtin_bit_cast(bf16x8, q[buffer][tile][i][lane]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[j] = mfma(rows, k[j][i], i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : s[j]);
         }
-        const f32x4 top = *reinterpret_cast<const f32x4*>(&tops[now][tile * kTile + 4 * g]);
-        const int query0 = tile0 / a.group, last = (tile0 + kTile - 1) / a.group;
+        const f32x4 top = *reinterpret_cast<const f32x4*>(&tops[buffer][tile * kTile + 4 * g]);
+        const int query0 = query_of(m, tile0), last = query_of(m, tile0 + kTile - 1);
         bool masked;
         if constexpr (V == kTree) masked = base < t.all_first || base + kChunk > t.all_last;
         else masked = base + kChunk > t.before + query0 + 1 || (a.window && base <= t.before + last - a.window);
@@ -404,7 +402,6 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs 
 #pragma unroll
     for (int j = 0; j < 4; ++j) sums[j] = over_groups(sums[j]);
     const float drawn = of_group(sums);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is on its way to the tiles any more
     __syncthreads();
     if (half == 1) joined[wave % kChunks][lane] = drawn;
     __syncthreads();
@@ -458,6 +455,7 @@ hipError_t launch_kv_attention_mass(const uint16_t* q, int64_t ldq, const float*
                  1, 1, 0, 0, nullptr, nullptr},
                 masks, words, const_cast<float*>(lse), ldl};
   m.mass = mass;
+  m.inverse = static_cast<uint32_t>(((1ull << 32) + group - 1) / group);
   m.scale_log2 = fminf(fmaxf(scale * kLog2e, -3.402823466e38f), 3.402823466e38f);
   if (masks) {
     if (head_dim == 64) launch_mass<64, kTree>(m, num_seqs, stream);
