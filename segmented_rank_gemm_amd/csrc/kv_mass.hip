@@ -23,7 +23,7 @@ namespace lora {
 constexpr int kMassWaves = 8;
 constexpr int kMassThreads = kMassWaves * kWave;
 constexpr int kFewTiles = 8;       // of 16 rows, at most, for the kernel of few
-constexpr int kHalves = 2;         // of the rows, for that of many: waves that share a chunk
+constexpr int kShares = 4;         // of the rows, for that of many: waves that share a chunk
 constexpr float kLog2e = 1.44269504f;
 
 struct MassArgs {
@@ -290,14 +290,11 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_kernel(MassArgs m) {
 template <int D, int V>
 __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs m) {
   constexpr int kSteps = D / 32;
-  constexpr int kChunks = kMassWaves / kHalves;  // of a workgroup
-  // Tiles of a half that are staged at a time (beside a tree's masks there is room for one,
-  // if two workgroups are to share a compute unit).
-  constexpr int kStageTiles = V == kTree && D == 128 ? 1 : 2;
-  constexpr int kStageRows = kHalves * kStageTiles * kTile;
+  constexpr int kChunks = kMassWaves / kShares;  // of a workgroup
+  constexpr int kStageRows = kShares * kTile;      // a tile for each
   const SumArgs& a = m.a;
   const int wave = wave_index(), lane = lane_id(), g = lane >> 4, c = lane & 15;
-  const int half = wave / kChunks;
+  const int share = wave / kChunks;
   const int kv_head = static_cast<int>(blockIdx.x);
   const int seq = sequence_at(a, static_cast<int>(blockIdx.z));
   RowTile t;
@@ -306,9 +303,9 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs 
   const int end = (length + kChunk - 1) / kChunk;
   const MassReader<D> reader = mass_reader_of<D>(m, seq, kv_head);
 
-  __shared__ u32x4 q[2][kHalves * kStageTiles][kSteps][kWave];
+  __shared__ u32x4 q[2][kShares][kSteps][kWave];
   __shared__ float tops[2][kStageRows];
-  __shared__ float joined[kChunks][kWave];
+  __shared__ float joined[kMassWaves][kWave];
   __shared__ Draft drafts[V == kTree ? 64 * kDraftWords : 1];
   if constexpr (V == kTree) stage_drafts(a, t, drafts, t.query1 + 1, kMassThreads);  // (a barrier comes below)
 
@@ -334,23 +331,36 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs 
     // Steps of kStageRows rows, of whose operands each wave brings kLoads, and the first
     // one the sums: by registers, since the compiler lets no read of shared memory pass a
     // load into it.  (Past the last step the last row's once more, which nobody reads.)
-    constexpr int kLoads = kHalves * kStageTiles * kSteps / kMassWaves;
+    constexpr int kLoads = kShares * kSteps / kMassWaves;
     u32x4 part[kLoads];
     float lse = 0.f;
+    // Where a step is a whole number of queries, its rows lie as far behind those of the
+    // step before as these do; elsewhere, and where rows are missing, they are looked for.
+    const bool whole = kStageRows % a.group == 0;
+    const int64_t queries = kStageRows / a.group;  // (for that case)
+    const uint16_t* at_row[kLoads];
+    const float* at_lse = a.lse;
     const auto ask = [&](int row0) {
-      const int first_row = row0 < t.rows ? row0 : t.rows - 1, left = t.rows - 1 - first_row;
-      const int query0 = query_of(m, first_row), head0 = first_row - query0 * a.group;
+      if (whole && row0 > from && row0 + kStageRows <= t.rows) {
 #pragma unroll
-      for (int f = 0; f < kLoads; ++f) {
-        const int at = f * kMassWaves + wave, row = at / kSteps * kTile + c;
-        const RowOf of = row_of(a, query0, head0, row < left ? row : left);
-        part[f] = load16(a.q + static_cast<int64_t>(t.start + of.query) * a.ldq + (kv_head * a.group + of.head) * D +
-                         g * (D / 4) + 8 * (at % kSteps));
-      }
-      if (wave == 0) {
+        for (int f = 0; f < kLoads; ++f) at_row[f] += queries * a.ldq;
+        at_lse += queries * a.ldl;
+      } else {
+        const int first_row = row0 < t.rows ? row0 : t.rows - 1, left = t.rows - 1 - first_row;
+        const int query0 = query_of(m, first_row), head0 = first_row - query0 * a.group;
+#pragma unroll
+        for (int f = 0; f < kLoads; ++f) {
+          const int at = f * kMassWaves + wave, row = at / kSteps * kTile + c;
+          const RowOf of = row_of(a, query0, head0, row < left ? row : left);
+          at_row[f] = a.q + static_cast<int64_t>(t.start + of.query) * a.ldq + (kv_head * a.group + of.head) * D +
+                      g * (D / 4) + 8 * (at % kSteps);
+        }
         const RowOf of = row_of(a, query0, head0, lane < left ? lane : left);
-        lse = a.lse[static_cast<int64_t>(t.start + of.query) * a.ldl + kv_head * a.group + of.head];
+        at_lse = a.lse + static_cast<int64_t>(t.start + of.query) * a.ldl + kv_head * a.group + of.head;
       }
+#pragma unroll
+      for (int f = 0; f < kLoads; ++f) part[f] = load16(at_row[f]);
+      if (wave == 0) lse = *at_lse;
     };
     const auto put = [&](int buffer, int row0) {
 #pragma unroll
@@ -375,42 +385,40 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs 
       __syncthreads();  // this step's tiles are there, and the other buffer has been read
       put(buffer ^ 1, row0 + kStageRows);
       ask(row0 + 2 * kStageRows);
-      if (!mine) continue;
-#pragma unroll 1
-      for (int n = 0; n < kStageTiles; ++n) {
-        const int tile = half * kStageTiles + n, tile0 = row0 + tile * kTile;
-        if (tile0 >= to) break;
-        f32x4 s[4];
+      const int tile0 = row0 + share * kTile;
+      if (!mine || tile0 >= to) continue;
+      f32x4 s[4];
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-          const bf16x8 rows = __builtin_bit_cast(bf16x8, q[buffer][tile][i][lane]);
+      for (int i = 0; i < kSteps; ++i) {
+        const bf16x8 rows = __builtin_bit_cast(bf16x8, q[buffer][share][i][lane]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[j] = mfma(rows, k[j][i], i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : s[j]);
-        }
-        const f32x4 top = *reinterpret_cast<const f32x4*>(&tops[buffer][tile * kTile + 4 * g]);
-        const int query0 = query_of(m, tile0), last = query_of(m, tile0 + kTile - 1);
-        bool masked;
-        if constexpr (V == kTree) masked = base < t.all_first || base + kChunk > t.all_last;
-        else masked = base + kChunk > t.before + query0 + 1 || (a.window && base <= t.before + last - a.window);
-        if (masked)
-          add_seen_rows(sums, s, top, m.scale_log2,
-                        seen_by_rows<V>(a, t, drafts, base, query0, tile0 - query0 * a.group, to - tile0));
-        else
-          add_rows(sums, s, top, m.scale_log2);
+        for (int j = 0; j < 4; ++j) s[j] = mfma(rows, k[j][i], i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : s[j]);
       }
+      const f32x4 top = *reinterpret_cast<const f32x4*>(&tops[buffer][share * kTile + 4 * g]);
+      const int query0 = query_of(m, tile0), last = query_of(m, tile0 + kTile - 1);
+      bool masked;
+      if constexpr (V == kTree) masked = base < t.all_first || base + kChunk > t.all_last;
+      else masked = base + kChunk > t.before + query0 + 1 || (a.window && base <= t.before + last - a.window);
+      if (masked)
+        add_seen_rows(sums, s, top, m.scale_log2,
+                      seen_by_rows<V>(a, t, drafts, base, query0, tile0 - query0 * a.group, to - tile0));
+      else
+        add_rows(sums, s, top, m.scale_log2);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) sums[j] = over_groups(sums[j]);
     const float drawn = of_group(sums);
-    __syncthreads();
-    if (half == 1) joined[wave % kChunks][lane] = drawn;
+    joined[wave][lane] = drawn;
     __syncthreads();
     const int token = base + 4 * c + g;
-    if (half == 0 && mine && token < length && page >= 0) {
+    if (share == 0 && mine && token < length && page >= 0) {
       float* at = reader.at(page, base);
-      const float all = drawn + joined[wave][lane];
+      float all = drawn;
+#pragma unroll
+      for (int n = 1; n < kShares; ++n) all += joined[n * kChunks + wave][lane];
       *at = token >= t.before ? all : *at + all;
     }
+    __syncthreads();  // the sums have been read
   }
 }
 
@@ -429,7 +437,7 @@ static void launch_mass(const MassArgs& m, int num_seqs, hipStream_t stream) {
   const bool few = rows <= kFewTiles * kTile;
   // As many workgroups as the device holds, and several times that of those whose lengths differ in
   // rows as well.
-  const int64_t most = few ? (chunks + kMassWaves - 1) / kMassWaves : (chunks * kHalves + kMassWaves - 1) / kMassWaves;
+  const int64_t most = few ? (chunks + kMassWaves - 1) / kMassWaves : (chunks * kShares + kMassWaves - 1) / kMassWaves;
   int64_t groups = ((few ? 2 : 16) * kCus + units - 1) / units;
   groups = groups < most ? groups : most;
   const dim3 grid(heads, static_cast<unsigned>(groups), num_seqs), block(kMassThreads);
