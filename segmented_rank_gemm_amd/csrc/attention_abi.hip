@@ -148,7 +148,7 @@ lora_status_t lora_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* q
   return launch_status(lora::launch_kv_attention(
       q, ldq, query_start, seq_lens, page_table, ld_table, cache, num_pages, page_shift(page_size),
       num_tokens, num_seqs, max_query_len, max_seq_len, q_heads, kv_heads, head_dim, scale, window,
-      nullptr, 0, out, ldo, nullptr, 0, workspace, stream));
+      nullptr, 0, false, out, ldo, nullptr, 0, workspace, stream));
 }
 
 }  // extern "C"

@@ -117,7 +117,7 @@ lora_status_t lora_kv_tree_attention(const uint16_t* q, int64_t ldq, const int32
   return launch_status(lora::launch_kv_attention(
       q, ldq, query_start, seq_lens, page_table, ld_table, cache, num_pages, page_shift(page_size),
       num_tokens, num_seqs, max_query_len, max_seq_len, q_heads, kv_heads, head_dim, scale, window, masks,
-      mask_words, out, ldo, lse, ldl, workspace, stream));
+      mask_words, true, out, ldo, lse, ldl, workspace, stream));
 }
 
 lora_status_t lora_kv_attention_mass(const uint16_t* q, int64_t ldq, const float* lse, int64_t ldl,

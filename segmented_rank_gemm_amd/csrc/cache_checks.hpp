@@ -16,8 +16,8 @@ hipError_t launch_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* qu
                                int page_shift, int num_tokens, int num_seqs, int max_query_len,
                                int max_seq_len, int q_heads, int kv_heads, int head_dim,
                                float scale, int window, const int64_t* masks, int64_t words,
-                               uint16_t* out, int64_t ldo, float* lse, int64_t ldl, void* workspace,
-                               hipStream_t stream);
+                               bool sums, uint16_t* out, int64_t ldo, float* lse, int64_t ldl,
+                               void* workspace, hipStream_t stream);
 
 constexpr int32_t kMaxTokens = 1 << 22;  // times up to 512 threads: a grid dimension
 constexpr int32_t kMaxHeads = 1024;

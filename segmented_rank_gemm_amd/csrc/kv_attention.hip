@@ -268,6 +268,27 @@ __device__ __forceinline__ int64_t unit_of(const AttentionArgs& a, int seq, int 
   return (static_cast<int64_t>(seq) * a.row_tiles + tile) * a.cache.kv_heads + kv_head;
 }
 
+// A call's arguments behind a loop that does not need them; of the views with more of
+// them they are loaded once more: kept in registers through it they put others out.
+template <int V>
+struct LateArgs {
+  SumArgs args;
+  __device__ __forceinline__ explicit LateArgs(const SumArgs&) {
+    using Word = const __attribute__((address_space(4))) uint64_t;
+    Word* p = (Word*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    uint64_t words[sizeof(SumArgs) / 8];
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(SumArgs) / 8); ++i) words[i] = p[i];
+    args = __builtin_bit_cast(SumArgs, words);
+  }
+};
+template <>
+struct LateArgs<kPlain> {
+  const AttentionArgs& args;
+  __device__ __forceinline__ explicit LateArgs(const AttentionArgs& a) : args(a) {}
+};
+
 // ln of the sum of a row's exponentials, from the sum relative to the power `top` of
 // two; -infinity for a row that saw nothing.
 __device__ __forceinline__ float log_sum(float top, float full) {
@@ -409,11 +430,13 @@ __global__ __launch_bounds__(split_waves(MT) * kWave, MT == 1 ? 4 : 2) void kv_a
   // (rows 4 words apart from a multiple of the banks)
   __shared__ float outs[kWaves][kTile][D + 4];
   __shared__ float tops[kWaves][kTile], sums[kWaves][kTile], fulls[V == kPlain ? 1 : kWaves][kTile];
+  const LateArgs<V> late(a);
+  const auto& b = late.args;
   constexpr int kLanes = D / 4;  // threads a row, four elements each
   constexpr int kRowsAtOnce = kWaves * kWave / kLanes;
   const int e = (tid % kLanes) * 4;
   const int64_t slot =
-      (unit_of(a, seq, tile, kv_head) * a.parts + part) * (MT * kTile);
+      (unit_of(b, seq, tile, kv_head) * b.parts + part) * (MT * kTile);
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     if (mt > 0) __syncthreads();  // the tile before has been read
@@ -449,13 +472,13 @@ __global__ __launch_bounds__(split_waves(MT) * kWave, MT == 1 ? 4 : 2) void kv_a
         for (int i = 0; i < 4; ++i) o[i] += outs[w][row][e + i];
       }
       if (active == 1) {
-        store_out(a, t, kv_head, mt * kTile + row, D, e, o, total);
+        store_out(b, t, kv_head, mt * kTile + row, D, e, o, total);
         if constexpr (V != kPlain)
-          if (e == 0) store_lse(a, t, kv_head, mt * kTile + row, top, full);
+          if (e == 0) store_lse(b, t, kv_head, mt * kTile + row, top, full);
       } else {
         const int64_t at = slot + mt * kTile + row;
-        store16(a.partial + at * D + e, __builtin_bit_cast(u32x4, o));
-        if (e == 0) store_stats<V>(a, at, top, total, full);
+        store16(b.partial + at * D + e, __builtin_bit_cast(u32x4, o));
+        if (e == 0) store_stats<V>(b, at, top, total, full);
       }
     }
   }
@@ -691,6 +714,8 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel
     ahead = reader.pages(upto(chunk + 3));
     __syncthreads();
   }
+  const LateArgs<V> late(a);
+  const auto& b = late.args;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     float sum = r.sum[mt];
@@ -704,12 +729,13 @@ __global__ __launch_bounds__(kRowWaves * kWave, 2) void kv_attention_rows_kernel
     }
     const int row = row0 + mt * kTile + c;
     if (row >= t.rows) continue;
-    if constexpr (V != kPlain)
-      if (g == 0) store_lse(a, t, kv_head, row, r.top[mt], full);
-    const RowOf at = row_of(a, t.query0, t.head0, row);
+    if constexpr (V != kPlain) {
+      if (g == 0) store_lse(b, t, kv_head, row, r.top[mt], full);
+    }
+    const RowOf at = row_of(b, t.query0, t.head0, row);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint16_t* dst = a.out + static_cast<int64_t>(t.start + at.query) * a.ldo +
-                    (kv_head * a.group + at.head) * D + g * (D / 4);
+    uint16_t* dst = b.out + static_cast<int64_t>(t.start + at.query) * b.ldo +
+                    (kv_head * b.group + at.head) * D + g * (D / 4);
     // lane (g, c) has elements g * D / 4 + i * D / 16 + n of row c
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -810,11 +836,19 @@ struct AttentionPlan {
   int64_t most_parts;  // no fewer than the parts of any smaller max_len
 };
 
-static AttentionPlan attention_plan(int num_seqs, int max_query_len, int64_t max_len, int q_heads,
+// views: of the views with sums.
+static AttentionPlan attention_plan(bool views, int num_seqs, int max_query_len, int64_t max_len, int q_heads,
                                     int kv_heads) {
   AttentionPlan p;
   const int64_t rows = static_cast<int64_t>(max_query_len) * (q_heads / kv_heads);
-  const int mt = rows <= kTile ? 1 : 2;
+  const int64_t chunks = (max_len + kChunk - 1) / kChunk;
+  // One row tile a workgroup also where there are compute units for all of them and
+  // their eight waves are done in a round or two, which four with two tiles are not
+  // (26 rows and 500 tokens, 32 key heads: 12.5 us, two tiles 14.6; but 512 rows and
+  // 32768 tokens, 8 key heads: 174 and 101).  Only for the views that came later: the
+  // plain one's results are those of its tiles.
+  const int64_t narrow = (rows + kTile - 1) / kTile * num_seqs * kv_heads;
+  const int mt = rows <= kTile || (views && narrow <= kCus && chunks <= 2 * split_waves(1)) ? 1 : 2;
   // Workgroups of the rows kernel; with fewer than fill the device twice over
   // (their registers), cutting the tokens up as well gains more than sharing the
   // operands (us, split / rows: 1 sequence of 128 queries of 4096 tokens, 8 key
@@ -827,7 +861,6 @@ static AttentionPlan attention_plan(int num_seqs, int max_query_len, int64_t max
   p.units = static_cast<int64_t>(num_seqs) * kv_heads * p.row_tiles;
   p.parts = 1;
   p.most_parts = 1;
-  const int64_t chunks = (max_len + kChunk - 1) / kChunk;
   p.part_chunks = static_cast<int>(chunks);
   if (p.many) return p;
   // About a workgroup a CU (131072 tokens, 8 key heads, one row tile: 256
@@ -856,7 +889,7 @@ static int64_t stats_bytes(const AttentionPlan& p, View view) {
 static int64_t workspace_bytes(int num_seqs, int max_query_len, int max_seq_len, int q_heads, int kv_heads,
                                int head_dim, View view) {
   if (num_seqs < 1) return 0;
-  const AttentionPlan p = attention_plan(num_seqs, max_query_len, max_seq_len, q_heads, kv_heads);
+  const AttentionPlan p = attention_plan(view != kPlain, num_seqs, max_query_len, max_seq_len, q_heads, kv_heads);
   if (p.most_parts <= 1) return 0;
   return stats_bytes(p, view) + p.units * p.most_parts * p.tile_rows * head_dim * 4;
 }
@@ -899,9 +932,9 @@ hipError_t launch_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* qu
                                int page_shift, int num_tokens, int num_seqs, int max_query_len,
                                int max_seq_len, int q_heads, int kv_heads, int head_dim,
                                float scale, int window, const int64_t* masks, int64_t words,
-                               uint16_t* out, int64_t ldo, float* lse, int64_t ldl, void* workspace,
-                               hipStream_t stream) {
-  const View view = masks ? kTree : (lse ? kSums : kPlain);
+                               bool sums, uint16_t* out, int64_t ldo, float* lse, int64_t ldl,
+                               void* workspace, hipStream_t stream) {
+  const View view = masks ? kTree : (sums ? kSums : kPlain);
   const int group = q_heads / kv_heads;
   // A window bounds the tokens that any tile walks; the parts are then fewer
   // than those that the workspace is sized for.
@@ -911,7 +944,7 @@ hipError_t launch_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* qu
     const int64_t seen = static_cast<int64_t>(window) + max_query_len + kChunk;
     longest = longest < seen ? longest : seen;
   }
-  const AttentionPlan p = attention_plan(num_seqs, max_query_len, longest, q_heads, kv_heads);
+  const AttentionPlan p = attention_plan(view != kPlain, num_seqs, max_query_len, longest, q_heads, kv_heads);
   SumArgs a = {{q, query_start, seq_lens, page_table, out,
                      {cache, num_pages, page_shift, kv_heads},
                      ldq, ldo, ld_table, num_tokens, max_query_len, max_seq_len, q_heads, window,
