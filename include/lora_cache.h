@@ -154,12 +154,12 @@ lora_status_t lora_kv_select(const float *mass, int32_t num_pages, int32_t page_
  *                that take place first + j; NULL: in place.  None of these may be one
  *                that the call reads from, and none may take the tokens of two places.
  *   mass         may be NULL.
- * In place, kept[j] > j moves, kept[j] = j leaves the token where it is, and entries
- * below j are skipped; no page may then stand twice among those that hold the places
- * named.  Entries below 0, and those whose source or destination lies outside its
- * table or on a page outside [0, num_pages), are skipped: their destinations stay as
- * they are.
- * Enqueues one kernel.
+ * Entries below 0, and those whose source or destination lies outside its table or on
+ * a page outside [0, num_pages), are skipped: their destinations stay as they are.
+ * In place the entries before the first one below 0 ascend (what the places named hold
+ * afterwards is open otherwise); kept[j] = j leaves the token where it is.  No page may
+ * then stand twice among those that hold the places named.
+ * Enqueues one kernel, or two for long lists of few key heads in place.
  */
 lora_status_t lora_kv_compact(const int32_t *kept, int32_t num_lists, int32_t max_kept,
                               const int32_t *counts, const int32_t *first,

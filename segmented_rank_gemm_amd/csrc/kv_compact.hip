@@ -1,23 +1,34 @@
 // lora_kv_compact: kept tokens to the places in front, codes, scales and weights:
 //   place first + j  <-  place first + kept[j]
 //
-// A workgroup a (sequence, key head, keys or values) where this is done in place.  It
-// takes the list in blocks from the front: everything a block moves is in registers
-// before any of it is written.  As kept[j] >= j, a block's places lie in front of all
-// that later blocks still have to read, so that every place gets what its source held
-// before the call; and no other workgroup touches these bytes.
 // Into other pages nothing has to be waited for, and the list is shared out.
+// In place a workgroup has a (sequence, key head, keys or values) and takes the list in
+// blocks from the front: everything a block moves is in registers before any of it is
+// written.  As kept[j] >= j, a block's places lie in front of all that later blocks
+// still have to read, so that every place gets what its source held before the call;
+// and no other workgroup touches these bytes.
 //
-// A wave moves 64 tokens at a time, kUnits of them in flight: each lane finds out where
-// one token is and goes, and moves its scale bytes and its weight; the codes are moved
-// by as many lanes a token as it has 16-byte pieces, which ask that lane.
+// Long lists of few key heads leave the device idle that way (2 x 8 workgroups, 65536
+// tokens: 225 us).  Where the tokens lie a thousand places ahead of where they go, and
+// further on always do, the moves are followed from the other end: a place that is no
+// source itself takes its token, whose place takes its own, and so on.  These chains
+// have nothing in common, each step is a thousand places long, and there are as many of
+// them as tokens were left out.  What lies before goes in blocks first, in a launch of
+// its own (that list: 47 us in all).
+//
+// A wave moves 64 tokens at a time, several times that in flight: each lane finds out
+// where one token is and goes, and moves its scale bytes and its weight; the codes are
+// moved by as many lanes a token as it has 16-byte pieces, which ask that lane.
 
 #include "kv_format.hpp"
 
 namespace lora {
 
 constexpr int kCompactThreads = 1024;  // at most
-constexpr int kUnits = 4;
+constexpr int kUnits = 4;              // of 64 tokens in flight
+constexpr int kNearBlock = 1024;       // tokens of a block, where the rest goes by chains
+constexpr int kFar = 1024;             // places that a chain's steps have at least
+constexpr int kChainWaves = 4;
 
 struct CompactArgs {
   const int32_t* kept;
@@ -31,75 +42,115 @@ struct CompactArgs {
   int lists, max_kept, pages, dst_pages;
 };
 
+// One (sequence, key head, keys or values) of a call.
 template <int D>
-__global__ __launch_bounds__(kCompactThreads) void kv_compact_kernel(CompactArgs a) {
-  constexpr int kPieces = D / 32;  // of a token's codes; and its scale bytes
-  constexpr int kAtOnce = kWave / kPieces;
-  const int head = static_cast<int>(blockIdx.x) >> 1, part = static_cast<int>(blockIdx.x) & 1;
-  const int seq = static_cast<int>(blockIdx.y);
-  const int lane = lane_id(), wave = wave_index(), waves = static_cast<int>(blockDim.x) / kWave;
-  const int piece = lane % kPieces;
-  int count = a.counts[seq];
-  count = count < a.max_kept ? count : a.max_kept;
-  const int64_t first = a.first ? a.first[seq] : 0;
-  if (first < 0) return;
-  const int shift = a.cache.page_shift, in = (1 << shift) - 1;
-  const int32_t* kept = a.kept + (static_cast<int64_t>(seq) * a.lists + (a.lists > 1 ? head : 0)) * a.max_kept;
-  const int32_t* table = a.table + seq * a.ld_table;
-  const int32_t* dst_table = a.dst_table ? a.dst_table + seq * a.ld_dst : table;
-  const int64_t places = static_cast<int64_t>(a.pages) << shift;
-  const int64_t dst_places = static_cast<int64_t>(a.dst_table ? a.dst_pages : a.pages) << shift;
-  const bool weights = a.mass && part == 0;
-  const int64_t block_bytes = static_cast<int64_t>(D / 2 + kPieces) << shift;
-  const int64_t page_bytes = 2 * a.cache.kv_heads * block_bytes;
-  uint8_t* mine = a.cache.data + (part * a.cache.kv_heads + head) * block_bytes;  // of page 0
+struct Mover {
+  static constexpr int kPieces = D / 32;  // of a token's codes; and its scale bytes
+  const int32_t* kept;
+  const int32_t* table;
+  const int32_t* dst_table;
+  uint8_t* bytes;       // of page 0
+  float* mass;          // of page 0; null where the weights are not this one's to move
+  int64_t first, places, dst_places, page_bytes, mass_stride;
+  int count, shift, in, num_pages;
 
-  const int tokens = waves * kUnits * kWave;
-  const int step = static_cast<int>(gridDim.z) * tokens;
-  for (int base = static_cast<int>(blockIdx.z) * tokens; base < count; base += step) {
-    int page[kUnits], to_page[kUnits], at[kUnits];  // at: places in the two pages
-    u32x4 codes[kUnits][kPieces];
-    uint8_t scales[kUnits][kPieces];
-    float weight[kUnits];
+  // What a wave holds of 64 tokens.
+  struct Held {
+    u32x4 codes[kPieces];
+    uint8_t scales[kPieces];
+    float weight;
+  };
+
+  __device__ __forceinline__ Mover(const CompactArgs& a, int seq, int head, int part) {
+    count = a.counts[seq];
+    count = count < a.max_kept ? count : a.max_kept;
+    first = a.first ? a.first[seq] : 0;
+    if (first < 0) count = 0;
+    shift = a.cache.page_shift;
+    in = (1 << shift) - 1;
+    num_pages = a.cache.num_pages;
+    kept = a.kept + (static_cast<int64_t>(seq) * a.lists + (a.lists > 1 ? head : 0)) * a.max_kept;
+    table = a.table + seq * a.ld_table;
+    dst_table = a.dst_table ? a.dst_table + seq * a.ld_dst : table;
+    places = static_cast<int64_t>(a.pages) << shift;
+    dst_places = static_cast<int64_t>(a.dst_table ? a.dst_pages : a.pages) << shift;
+    const int64_t block_bytes = static_cast<int64_t>(D / 2 + kPieces) << shift;
+    page_bytes = 2 * a.cache.kv_heads * block_bytes;
+    bytes = a.cache.data + (part * a.cache.kv_heads + head) * block_bytes;
+    mass = a.mass && part == 0 ? a.mass + (static_cast<int64_t>(head) << shift) : nullptr;
+    mass_stride = static_cast<int64_t>(a.cache.kv_heads) << shift;
+  }
+  __device__ __forceinline__ bool has(int page) const { return page >= 0 && page < num_pages; }
+  // at: each lane's token's place in its page.  (Loads without conditions, of a page that
+  // is there: the wait before a use counts the loads behind it.)
+  __device__ __forceinline__ void load(Held& h, int page, int at) const {
+    const int lane = lane_id();
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      const int j = base + (wave * kUnits + u) * kWave + lane;
-      const int number = kept[j < count ? j : count - 1];
-      const int64_t from = first + number, to = first + j;
+    for (int p = 0; p < kPieces; ++p) {
+      const int of = p * (kWave / kPieces) + lane / kPieces;
+      h.codes[p] = load16(bytes + __shfl(page, of) * page_bytes + __shfl(at, of) * (D / 2) + lane % kPieces * 16);
+    }
+    const uint8_t* s = bytes + page * page_bytes + ((D / 2) << shift) + at;
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) h.scales[p] = s[p << shift];
+  }
+  __device__ __forceinline__ void load_weight(Held& h, int page, int at) const {
+    if (mass) h.weight = mass[page * mass_stride + at];
+  }
+  // page: -1 for a token that does not move.
+  __device__ __forceinline__ void store(const Held& h, int page, int at) const {
+    const int lane = lane_id();
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+      const int of = p * (kWave / kPieces) + lane / kPieces;
+      const int to = __shfl(page, of), place = __shfl(at, of);
+      if (to >= 0) store16(bytes + to * page_bytes + place * (D / 2) + lane % kPieces * 16, h.codes[p]);
+    }
+    if (page < 0) return;
+    uint8_t* s = bytes + page * page_bytes + ((D / 2) << shift) + at;
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) s[p << shift] = h.scales[p];
+    if (mass) mass[page * mass_stride + at] = h.weight;
+  }
+};
+
+// U: units of a wave.  Near: only the blocks before the first whose tokens come from far.
+template <int D, int U, bool Near>
+__global__ __launch_bounds__(kCompactThreads) void kv_compact_kernel(CompactArgs a) {
+  const Mover<D> m(a, static_cast<int>(blockIdx.y), static_cast<int>(blockIdx.x) >> 1, static_cast<int>(blockIdx.x) & 1);
+  const int lane = lane_id(), wave = wave_index(), waves = static_cast<int>(blockDim.x) / kWave;
+  const int tokens = waves * U * kWave;
+  const int step = static_cast<int>(gridDim.z) * tokens;
+  for (int base = static_cast<int>(blockIdx.z) * tokens; base < m.count; base += step) {
+    if (Near && m.kept[base] - base >= kFar) break;
+    int page[U], to_page[U], at[U], to_at[U];
+    typename Mover<D>::Held held[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = base + (wave * U + u) * kWave + lane;
+      const int number = m.kept[j < m.count ? j : m.count - 1];
+      const int64_t from = m.first + number, to = m.first + j;
       // in place, a token that stays where it is stays; one from further ahead is skipped
-      const bool moves = j < count && number >= 0 && from < places && to < dst_places && (a.dst_table || number > j);
-      page[u] = moves ? table[from >> shift] : -1;
-      to_page[u] = moves ? dst_table[to >> shift] : -1;
-      at[u] = (static_cast<int>(from) & in) | (static_cast<int>(to) & in) << 16;
+      const bool moves = j < m.count && number >= 0 && from < m.places && to < m.dst_places && (a.dst_table || number > j);
+      page[u] = moves ? m.table[from >> m.shift] : -1;
+      to_page[u] = moves ? m.dst_table[to >> m.shift] : -1;
+      at[u] = static_cast<int>(from) & m.in;
+      to_at[u] = static_cast<int>(to) & m.in;
     }
     bool any = false;
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      const bool moves = page[u] >= 0 && page[u] < a.cache.num_pages && to_page[u] >= 0 && to_page[u] < a.cache.num_pages;
+    for (int u = 0; u < U; ++u) {
+      const bool moves = m.has(page[u]) && m.has(to_page[u]);
       if (!moves) to_page[u] = -1;
-      if (!moves) page[u] = 0;  // which is there, and is not written to
+      if (!moves) page[u] = 0;
       any |= moves;
     }
     any = __any(any);
     if (any) {
-      // (loads without conditions: the wait before a use counts the loads behind it)
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
+      for (int u = 0; u < U; ++u) m.load(held[u], page[u], at[u]);
 #pragma unroll
-        for (int p = 0; p < kPieces; ++p) {
-          const int of = p * kAtOnce + lane / kPieces;
-          const int from = __shfl(at[u], of) & 0xFFFF;
-          codes[u][p] = load16(mine + __shfl(page[u], of) * page_bytes + from * (D / 2) + piece * 16);
-        }
-        const uint8_t* s = mine + page[u] * page_bytes + ((D / 2) << shift) + (at[u] & 0xFFFF);
-#pragma unroll
-        for (int p = 0; p < kPieces; ++p) scales[u][p] = s[p << shift];
-      }
-      if (weights) {
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u)
-          weight[u] = a.mass[((static_cast<int64_t>(page[u]) * a.cache.kv_heads + head) << shift) + (at[u] & 0xFFFF)];
-      }
+      for (int u = 0; u < U; ++u) m.load_weight(held[u], page[u], at[u]);
     }
     if (!a.dst_table) {
       // what this block reads has arrived before any of it is written
@@ -108,21 +159,101 @@ __global__ __launch_bounds__(kCompactThreads) void kv_compact_kernel(CompactArgs
     }
     if (!any) continue;
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-#pragma unroll
-      for (int p = 0; p < kPieces; ++p) {
-        const int of = p * kAtOnce + lane / kPieces;
-        const int to = __shfl(to_page[u], of), place = __shfl(at[u], of) >> 16;
-        if (to >= 0) store16(mine + to * page_bytes + place * (D / 2) + piece * 16, codes[u][p]);
-      }
-      if (to_page[u] < 0) continue;
-      uint8_t* s = mine + to_page[u] * page_bytes + ((D / 2) << shift) + (at[u] >> 16);
-#pragma unroll
-      for (int p = 0; p < kPieces; ++p) s[p << shift] = scales[u][p];
-      if (weights)
-        a.mass[((static_cast<int64_t>(to_page[u]) * a.cache.kv_heads + head) << shift) + (at[u] >> 16)] = weight[u];
+    for (int u = 0; u < U; ++u) m.store(held[u], to_page[u], to_at[u]);
+  }
+}
+
+// The rest of the list, in place, by chains.
+template <int D>
+__global__ __launch_bounds__(kChainWaves * kWave) void kv_compact_chain_kernel(CompactArgs a) {
+  const Mover<D> m(a, static_cast<int>(blockIdx.y), static_cast<int>(blockIdx.x) >> 1, static_cast<int>(blockIdx.x) & 1);
+  const int lane = lane_id(), wave = wave_index();
+  // The first block whose tokens come from far.
+  int from = m.count;
+  for (int base = 0; base < m.count; base += kWave * kNearBlock) {
+    const int64_t j = base + static_cast<int64_t>(lane) * kNearBlock;
+    const unsigned long long far = __ballot(j < m.count && m.kept[j < m.count ? j : 0] - j >= kFar);
+    if (far) {
+      from = base + (__ffsll(static_cast<long long>(far)) - 1) * kNearBlock;
+      break;
     }
   }
+  __shared__ uint32_t sources[kChainWaves][kWave];
+  const int step = static_cast<int>(gridDim.z) * kChainWaves * kWave;
+  for (int start = from + (static_cast<int>(blockIdx.z) * kChainWaves + wave) * kWave; start < m.count; start += step) {
+    // The first entry from `start` on: of 64 even parts the one that it is in, until
+    // they are single entries.
+    int low = from, high = m.count;
+    while (high > low) {
+      const int part = (high - low + kWave - 1) / kWave;
+      const int64_t probe = low + static_cast<int64_t>(lane) * part;
+      const int before = static_cast<int>(__popcll(__ballot(probe < high && m.kept[probe < high ? probe : low] < start)));
+      if (before == 0) break;
+      const int64_t next = low + static_cast<int64_t>(before) * part;
+      low = low + (before - 1) * part + 1;
+      high = next < high ? static_cast<int>(next) : high;
+    }
+    // Which of the 64 places from `start` on are sources: they stand there, ascending.
+    sources[wave][lane] = 0;
+    __builtin_amdgcn_wave_barrier();
+    const int64_t entry = static_cast<int64_t>(low) + lane;
+    const int source = entry < m.count ? m.kept[entry] : -1;
+    if (source >= start && source - start < kWave) sources[wave][source - start] = 1;
+    __builtin_amdgcn_wave_barrier();
+    int place = start + lane;
+    bool active = place < m.count && sources[wave][lane] == 0;
+    __builtin_amdgcn_wave_barrier();
+    // Every step goes ahead, so that each chain ends at the list's.
+    int next = active ? m.kept[place] : 0;
+    int to_page = active && m.first + place < m.places ? m.table[(m.first + place) >> m.shift] : -1;
+    while (__any(active)) {
+      const int64_t at = m.first + next;
+      const bool ahead = active && next > place && at < m.places;
+      int page = ahead ? m.table[at >> m.shift] : -1;
+      const int to_at = static_cast<int>(m.first + place) & m.in;
+      const bool moves = ahead && m.has(page) && m.has(to_page);
+      active = ahead && next < m.count;
+      const int after = active ? m.kept[next] : 0;
+      typename Mover<D>::Held held;
+      const int from_page = moves ? page : 0, from_at = static_cast<int>(at) & m.in;
+      m.load(held, from_page, from_at);
+      m.load_weight(held, from_page, from_at);
+      m.store(held, moves ? to_page : -1, to_at);
+      place = next;
+      next = after;
+      to_page = page;
+    }
+  }
+}
+
+template <int D>
+static void launch_compact(const CompactArgs& a, int num_seqs, hipStream_t stream) {
+  const int64_t units = static_cast<int64_t>(num_seqs) * a.cache.kv_heads * 2;
+  const dim3 grid(2 * a.cache.kv_heads, num_seqs, 1);
+  // By chains where the device has more compute units than half of them could use, and
+  // the list more than a few blocks.
+  if (!a.dst_table && units <= kCus / 4 && a.max_kept > 4 * kNearBlock) {
+    hipLaunchKernelGGL((kv_compact_kernel<D, 1, true>), grid, dim3(kNearBlock), 0, stream, a);
+    const int64_t all = (static_cast<int64_t>(a.max_kept) + kChainWaves * kWave - 1) / (kChainWaves * kWave);
+    int64_t ranges = (16 * kCus + units - 1) / units;
+    ranges = ranges < all ? ranges : all;
+    hipLaunchKernelGGL(kv_compact_chain_kernel<D>, dim3(grid.x, grid.y, static_cast<unsigned>(ranges)),
+                       dim3(kChainWaves * kWave), 0, stream, a);
+    return;
+  }
+  // In place as many waves as the list keeps busy, up to 16; into other pages four, and
+  // as many workgroups as fill the device.
+  const int64_t waves = (static_cast<int64_t>(a.max_kept) + kUnits * kWave - 1) / (kUnits * kWave);
+  const int64_t most = a.dst_table ? 4 : kCompactThreads / kWave;
+  const int threads = static_cast<int>(waves < most ? waves : most) * kWave;
+  int64_t ranges = 1;
+  if (a.dst_table) {
+    const int64_t all = (waves + most - 1) / most;
+    ranges = (8 * kCus + units - 1) / units;
+    ranges = ranges < all ? ranges : all;
+  }
+  hipLaunchKernelGGL((kv_compact_kernel<D, kUnits, false>), dim3(grid.x, grid.y, static_cast<unsigned>(ranges)),
+                     dim3(threads), 0, stream, a);
 }
 
 hipError_t launch_kv_compact(const int32_t* kept, int lists, int max_kept, const int32_t* counts,
@@ -132,20 +263,8 @@ hipError_t launch_kv_compact(const int32_t* kept, int lists, int max_kept, const
                              float* mass, hipStream_t stream) {
   const CompactArgs a = {kept, counts, first, page_table, dst_table, ld_table, ld_dst,
                          {cache, num_pages, page_shift, kv_heads}, mass, lists, max_kept, pages, dst_pages};
-  // In place as many waves as the list keeps busy, up to 16; into other pages four, and
-  // as many workgroups as fill the device.
-  const int64_t waves = (static_cast<int64_t>(max_kept) + kUnits * kWave - 1) / (kUnits * kWave);
-  const int64_t most = dst_table ? 4 : kCompactThreads / kWave;
-  const int threads = static_cast<int>(waves < most ? waves : most) * kWave;
-  int64_t ranges = 1;
-  if (dst_table) {
-    const int64_t units = static_cast<int64_t>(num_seqs) * kv_heads * 2, all = (waves + most - 1) / most;
-    ranges = (8 * kCus + units - 1) / units;
-    ranges = ranges < all ? ranges : all;
-  }
-  const dim3 grid(2 * kv_heads, num_seqs, static_cast<unsigned>(ranges));
-  if (head_dim == 64) hipLaunchKernelGGL(kv_compact_kernel<64>, grid, dim3(threads), 0, stream, a);
-  else hipLaunchKernelGGL(kv_compact_kernel<128>, grid, dim3(threads), 0, stream, a);
+  if (head_dim == 64) launch_compact<64>(a, num_seqs, stream);
+  else launch_compact<128>(a, num_seqs, stream);
   return hipGetLastError();
 }
 

@@ -143,17 +143,19 @@ def compact(places, mass, kept, counts, first, table, dst_table):
     dst = table if dst_table is None else dst_table
     for s in range(len(counts)):
         base = 0 if first is None else int(first[s])
+        n = max(0, min(int(counts[s]), kept.shape[2]))
+        if base < 0:
+            continue
         for h in range(kv):
-            for j in range(min(int(counts[s]), kept.shape[2])):
-                k = int(kept[s, h if kept.shape[1] > 1 else 0, j])
-                src, to = base + k, base + j
-                if base < 0 or k < 0 or (dst_table is None and k < j):
-                    continue
-                if src >= table.shape[1] * page or to >= dst.shape[1] * page:
-                    continue
-                a, b = int(table[s, src // page]), int(dst[s, to // page])
-                if not (0 <= a < pages and 0 <= b < pages):
-                    continue
-                new_places[b, :, h, to % page] = places[a, :, h, src % page]
-                new_mass[b, h, to % page] = mass[a, h, src % page]
+            k = kept[s, h if kept.shape[1] > 1 else 0, :n].astype(np.int64)
+            j = np.arange(n)
+            ok = (k >= 0) & (base + k < table.shape[1] * page) & (base + j < dst.shape[1] * page)
+            if dst_table is None:
+                ok &= k > j
+            src, to = (base + k)[ok], (base + j)[ok]
+            a, b = table[s, src // page], dst[s, to // page]
+            there = (a >= 0) & (a < pages) & (b >= 0) & (b < pages)
+            a, b, src, to = a[there], b[there], src[there] % page, to[there] % page
+            new_places[b, :, h, to] = places[a, :, h, src]
+            new_mass[b, h, to] = mass[a, h, src]
     return new_places, new_mass

@@ -419,23 +419,68 @@ def test_compact_without_mass():
     Moves(2, 2, 2, 40, 2, 128, 16, 90).check(mass=False)
 
 
-@pytest.mark.parametrize("new_pages", [False, True])
-def test_compact_of_any_list(new_pages):
-    """Numbers out of order, twice, far ahead; entries that are skipped; pages and starts that
-    are not there."""
-    for seed in range(4):
-        m = Moves(seed, 4, 2, 60, 2, 128 if seed % 2 else 64, 16, 3000, first=[0, 3, 2900, 5], new_pages=new_pages)
-        rng = np.random.default_rng(seed)
-        ahead = np.arange(60) + rng.integers(-4, 2800, m.kept.shape)
-        ahead[rng.random(m.kept.shape) < 0.1] = -1
-        ahead[rng.random(m.kept.shape) < 0.05] = 2 ** 31 - 1
-        same = rng.random(m.kept.shape) < 0.2
-        m.kept = np.where(same, np.arange(60), ahead).astype(np.int32)
-        m.table[1, 1], m.table[1, 20] = -1, m.pages
-        m.first[3] = -5
-        if m.dst is not None:
-            m.dst[2, -3] = m.pages
-        m.check()
+def spoil(m):
+    """Pages and starts that are not there."""
+    m.table[1, 1], m.table[1, m.table.shape[1] // 2] = -1, m.pages
+    m.first[3] = -5
+    if m.dst is not None:
+        m.dst[2, -3] = m.pages
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_compact_of_any_list_into_new_pages(seed):
+    """Numbers out of order, twice, behind; entries that are skipped."""
+    m = Moves(seed, 4, 2, 60, 2, 128 if seed % 2 else 64, 16, 3000, first=[0, 3, 2900, 5], new_pages=True)
+    rng = np.random.default_rng(seed)
+    m.kept = rng.integers(0, 2900, m.kept.shape).astype(np.int32)
+    m.kept[rng.random(m.kept.shape) < 0.1] = -1
+    m.kept[rng.random(m.kept.shape) < 0.05] = 2 ** 31 - 1
+    spoil(m)
+    m.check()
+
+
+@pytest.mark.parametrize("n", [60, 5000])
+@pytest.mark.parametrize("seed", range(2))
+def test_compact_in_place_skips_what_is_not_there(seed, n):
+    """Ascending lists with entries below 0 behind and numbers far past the table's places."""
+    m = Moves(seed, 4, 2, n, 2, 128 if seed % 2 else 64, 16, 3 * n, first=[0, 3, 2 * n - 100, 5])
+    rng = np.random.default_rng(seed)
+    m.kept = np.sort(np.stack([[rng.permutation(4 * n)[:n] for _ in range(2)] for _ in range(4)]), axis=-1).astype(np.int32)
+    m.kept[1, 0, -7:] = -1
+    m.kept[2, 1, -1] = 2 ** 31 - 1
+    spoil(m)
+    m.check()
+
+
+def runs(*parts):
+    """Ascending numbers: of (length, kept of each so many) parts one behind another."""
+    out, at = [], 0
+    for length, one_of in parts:
+        out += range(at, at + length, one_of)
+        at += length
+    return np.array(out, dtype=np.int32)
+
+
+@pytest.mark.parametrize("parts", [
+    [(11000, 1)],                                  # all stay
+    [(1, 1), (5000, 5000), (6000, 1)],             # 5000 out at once, then all behind come far
+    [(3000, 1), (1500, 1500), (7000, 1)],          # the far ones start inside a block
+    [(1024, 1), (3000, 2), (9000, 2)], [(4000, 4), (30000, 6)], [(2048, 1), (1024, 1024), (6000, 1), (100, 100), (500, 1)],
+    [(6000, 1), (40, 40), (2000, 1)],              # never far
+    [(1023, 1), (1100, 1100), (4200, 1)], [(200000, 40)],
+])
+@pytest.mark.parametrize("d,lists", [(64, 1), (128, 2)])
+def test_compact_of_long_lists_in_place(parts, d, lists):
+    kept = runs(*parts)
+    n = len(kept)
+    assert n > 4096
+    m = Moves(n, 2, lists, n, 2, d, 64, int(kept[-1]) + 3, first=[0, 2])
+    m.kept[:] = kept
+    rng = np.random.default_rng(n)
+    if lists == 2:  # another list for the other head: random gaps
+        m.kept[:, 1] = np.sort(rng.permutation(max(int(kept[-1]), n + 1))[:n])
+    m.counts = [n, n - 333]
+    m.check()
 
 
 def test_compact_of_a_long_list_with_one_token_out():
