@@ -114,70 +114,97 @@ struct Mover {
   }
 };
 
-// U: units of a wave.  Near: only the blocks before the first whose tokens come from far.
-template <int D, int U, bool Near>
+// The list's entries from `base` on, as many as the workgroup's waves take with U units each.
+template <int D, int U>
+__device__ __forceinline__ void move_block(const Mover<D>& m, bool in_place, int base) {
+  const int lane = lane_id(), wave = wave_index();
+  int page[U], to_page[U], at[U], to_at[U];
+  typename Mover<D>::Held held[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int j = base + (wave * U + u) * kWave + lane;
+    const int number = m.kept[j < m.count ? j : m.count - 1];
+    const int64_t from = m.first + number, to = m.first + j;
+    // in place, a token that stays where it is stays; one from further ahead is skipped
+    const bool moves = j < m.count && number >= 0 && from < m.places && to < m.dst_places && (!in_place || number > j);
+    page[u] = moves ? m.table[from >> m.shift] : -1;
+    to_page[u] = moves ? m.dst_table[to >> m.shift] : -1;
+    at[u] = static_cast<int>(from) & m.in;
+    to_at[u] = static_cast<int>(to) & m.in;
+  }
+  bool any = false;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const bool moves = m.has(page[u]) && m.has(to_page[u]);
+    if (!moves) to_page[u] = -1;
+    if (!moves) page[u] = 0;
+    any |= moves;
+  }
+  any = __any(any);
+  if (any) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) m.load(held[u], page[u], at[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) m.load_weight(held[u], page[u], at[u]);
+  }
+  if (in_place) {
+    // what this block reads has arrived before any of it is written
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+  }
+  if (!any) return;
+#pragma unroll
+  for (int u = 0; u < U; ++u) m.store(held[u], to_page[u], to_at[u]);
+}
+
+template <int D>
+__device__ __forceinline__ Mover<D> mover_of(const CompactArgs& a) {
+  return Mover<D>(a, static_cast<int>(blockIdx.y), static_cast<int>(blockIdx.x) >> 1, static_cast<int>(blockIdx.x) & 1);
+}
+
+// U: units of a wave.
+template <int D, int U>
 __global__ __launch_bounds__(kCompactThreads) void kv_compact_kernel(CompactArgs a) {
-  const Mover<D> m(a, static_cast<int>(blockIdx.y), static_cast<int>(blockIdx.x) >> 1, static_cast<int>(blockIdx.x) & 1);
-  const int lane = lane_id(), wave = wave_index(), waves = static_cast<int>(blockDim.x) / kWave;
-  const int tokens = waves * U * kWave;
+  const Mover<D> m = mover_of<D>(a);
+  const int tokens = static_cast<int>(blockDim.x) * U;
   const int step = static_cast<int>(gridDim.z) * tokens;
-  for (int base = static_cast<int>(blockIdx.z) * tokens; base < m.count; base += step) {
-    if (Near && m.kept[base] - base >= kFar) break;
-    int page[U], to_page[U], at[U], to_at[U];
-    typename Mover<D>::Held held[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = base + (wave * U + u) * kWave + lane;
-      const int number = m.kept[j < m.count ? j : m.count - 1];
-      const int64_t from = m.first + number, to = m.first + j;
-      // in place, a token that stays where it is stays; one from further ahead is skipped
-      const bool moves = j < m.count && number >= 0 && from < m.places && to < m.dst_places && (a.dst_table || number > j);
-      page[u] = moves ? m.table[from >> m.shift] : -1;
-      to_page[u] = moves ? m.dst_table[to >> m.shift] : -1;
-      at[u] = static_cast<int>(from) & m.in;
-      to_at[u] = static_cast<int>(to) & m.in;
+  for (int base = static_cast<int>(blockIdx.z) * tokens; base < m.count; base += step)
+    move_block<D, U>(m, !a.dst_table, base);
+}
+
+// The first block of the list whose tokens come from far (the list's end if none does).
+template <int D>
+__device__ __forceinline__ int first_far(const Mover<D>& m) {
+  for (int base = 0; base < m.count; base += kWave * kNearBlock) {
+    const int64_t j = base + static_cast<int64_t>(lane_id()) * kNearBlock;
+    const unsigned long long far = __ballot(j < m.count && m.kept[j < m.count ? j : 0] - j >= kFar);
+    if (far) return base + (__ffsll(static_cast<long long>(far)) - 1) * kNearBlock;
+  }
+  return m.count;
+}
+
+// In place, the blocks before it: several at a time as long as there are as many.
+template <int D>
+__global__ __launch_bounds__(kNearBlock) void kv_compact_near_kernel(CompactArgs a) {
+  const Mover<D> m = mover_of<D>(a);
+  const int end = first_far(m);
+  for (int base = 0; base < end;) {
+    if (end == m.count || end - base >= kUnits * kNearBlock) {
+      move_block<D, kUnits>(m, true, base);
+      base += kUnits * kNearBlock;
+    } else {
+      move_block<D, 1>(m, true, base);
+      base += kNearBlock;
     }
-    bool any = false;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool moves = m.has(page[u]) && m.has(to_page[u]);
-      if (!moves) to_page[u] = -1;
-      if (!moves) page[u] = 0;
-      any |= moves;
-    }
-    any = __any(any);
-    if (any) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) m.load(held[u], page[u], at[u]);
-#pragma unroll
-      for (int u = 0; u < U; ++u) m.load_weight(held[u], page[u], at[u]);
-    }
-    if (!a.dst_table) {
-      // what this block reads has arrived before any of it is written
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
-    }
-    if (!any) continue;
-#pragma unroll
-    for (int u = 0; u < U; ++u) m.store(held[u], to_page[u], to_at[u]);
   }
 }
 
 // The rest of the list, in place, by chains.
 template <int D>
 __global__ __launch_bounds__(kChainWaves * kWave) void kv_compact_chain_kernel(CompactArgs a) {
-  const Mover<D> m(a, static_cast<int>(blockIdx.y), static_cast<int>(blockIdx.x) >> 1, static_cast<int>(blockIdx.x) & 1);
+  const Mover<D> m = mover_of<D>(a);
   const int lane = lane_id(), wave = wave_index();
-  // The first block whose tokens come from far.
-  int from = m.count;
-  for (int base = 0; base < m.count; base += kWave * kNearBlock) {
-    const int64_t j = base + static_cast<int64_t>(lane) * kNearBlock;
-    const unsigned long long far = __ballot(j < m.count && m.kept[j < m.count ? j : 0] - j >= kFar);
-    if (far) {
-      from = base + (__ffsll(static_cast<long long>(far)) - 1) * kNearBlock;
-      break;
-    }
-  }
+  const int from = first_far(m);
   __shared__ uint32_t sources[kChainWaves][kWave];
   const int step = static_cast<int>(gridDim.z) * kChainWaves * kWave;
   for (int start = from + (static_cast<int>(blockIdx.z) * kChainWaves + wave) * kWave; start < m.count; start += step) {
@@ -233,12 +260,18 @@ static void launch_compact(const CompactArgs& a, int num_seqs, hipStream_t strea
   // By chains where the device has more compute units than half of them could use, and
   // the list more than a few blocks.
   if (!a.dst_table && units <= kCus / 4 && a.max_kept > 4 * kNearBlock) {
-    hipLaunchKernelGGL((kv_compact_kernel<D, 1, true>), grid, dim3(kNearBlock), 0, stream, a);
+    hipLaunchKernelGGL(kv_compact_near_kernel<D>, grid, dim3(kNearBlock), 0, stream, a);
     const int64_t all = (static_cast<int64_t>(a.max_kept) + kChainWaves * kWave - 1) / (kChainWaves * kWave);
     int64_t ranges = (16 * kCus + units - 1) / units;
     ranges = ranges < all ? ranges : all;
     hipLaunchKernelGGL(kv_compact_chain_kernel<D>, dim3(grid.x, grid.y, static_cast<unsigned>(ranges)),
                        dim3(kChainWaves * kWave), 0, stream, a);
+    return;
+  }
+  // A few accepted drafts: a wave's lanes hold a list, and wait for no others' loads.
+  if (a.max_kept <= kNearBlock) {
+    const int threads = (a.max_kept + kWave - 1) / kWave * kWave;
+    hipLaunchKernelGGL((kv_compact_kernel<D, 1>), grid, dim3(threads), 0, stream, a);
     return;
   }
   // In place as many waves as the list keeps busy, up to 16; into other pages four, and
@@ -252,7 +285,7 @@ static void launch_compact(const CompactArgs& a, int num_seqs, hipStream_t strea
     ranges = (8 * kCus + units - 1) / units;
     ranges = ranges < all ? ranges : all;
   }
-  hipLaunchKernelGGL((kv_compact_kernel<D, kUnits, false>), dim3(grid.x, grid.y, static_cast<unsigned>(ranges)),
+  hipLaunchKernelGGL((kv_compact_kernel<D, kUnits>), dim3(grid.x, grid.y, static_cast<unsigned>(ranges)),
                      dim3(threads), 0, stream, a);
 }
 
