@@ -50,6 +50,18 @@ _draft_masks, _tree_attention = lib().lora_draft_masks, lib().lora_kv_tree_atten
 _attention_mass, _select, _compact = lib().lora_kv_attention_mass, lib().lora_kv_select, lib().lora_kv_compact
 
 
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _stream_for(t: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> int:
+    """The stream's handle; refuses a call whose tensors are on another device than it."""
+    device = _current_device() if stream is None else stream.device_index
+    if t.get_device() != device:
+        raise ValueError(f"the tensors are on device {t.get_device()}, the stream is device {device}'s")
+    return _stream_handle(stream)
+
+
 def kv_mass_shape(num_pages: int, kv_heads: int, page_size: int):
     """Shape of the fp32 mass beside a cache: [num_pages, kv_heads, page_size]."""
     if page_size not in SUPPORTED_PAGE_SIZES:
@@ -86,7 +98,7 @@ def lora_draft_masks(parents: torch.Tensor, query_start: torch.Tensor, masks: Op
     pp = _vector(positions, _I32T, T, "positions") if positions is not None else 0
     pf = _vector(first_positions, _I32T, B, "first_positions") if first_positions is not None else 0
     status = _draft_masks(_vector(parents, _I32T, T, "parents"), _vector(query_start, _I32T, B + 1, "query_start"),
-                          T, B, pm, words, pf, pp, _stream_handle(stream))
+                          T, B, pm, words, pf, pp, _stream_for(parents, stream))
     if status:
         raise LoraError("lora_draft_masks", status)
 
@@ -143,7 +155,7 @@ def lora_kv_tree_attention(q: torch.Tensor, query_start: torch.Tensor, seq_lens:
     wptr, wbytes = (0, 0) if workspace is None else _flat_dev_bytes(workspace, "workspace")
     status = _tree_attention(
         pq, ldq, ps, pn, pt, ldt, pc, pages, page_size, T, B, max_query_len, max_seq_len, q_heads, kv_heads,
-        head_dim, scale, window, pm, words, po, ldo, pl, ldl, wptr, wbytes, _stream_handle(stream))
+        head_dim, scale, window, pm, words, po, ldo, pl, ldl, wptr, wbytes, _stream_for(q, stream))
     if status:
         raise LoraError("lora_kv_tree_attention", status)
 
@@ -166,7 +178,7 @@ def lora_kv_attention_mass(q: torch.Tensor, lse: torch.Tensor, query_start: torc
     status = _attention_mass(
         pq, ldq, pl, ldl, ps, pn, pt, ldt, pc, pages, page_size, T, B, max_query_len, max_seq_len, q_heads,
         kv_heads, head_dim, scale, window, pm, words, _whole(mass, _F32, (pages, kv_heads, page_size), "mass"),
-        _stream_handle(stream))
+        _stream_for(q, stream))
     if status:
         raise LoraError("lora_kv_attention_mass", status)
 
@@ -184,7 +196,7 @@ def lora_kv_select(mass: torch.Tensor, seq_lens: torch.Tensor, page_table: torch
     status = _select(
         _whole(mass, _F32, (pages, kv_heads, page_size), "mass"), pages, page_size, pn, pt, ldt, B, kv_heads,
         max_seq_len, sinks, recent, _whole(kept, _I32T, (B, kv_heads, budget), "kept"), budget,
-        _vector(new_lens, _I32T, B, "new_lens"), _stream_handle(stream))
+        _vector(new_lens, _I32T, B, "new_lens"), _stream_for(mass, stream))
     if status:
         raise LoraError("lora_kv_select", status)
 
@@ -212,6 +224,6 @@ def lora_kv_compact(kept: torch.Tensor, counts: torch.Tensor, page_table: torch.
     pf = _vector(first, _I32T, B, "first") if first is not None else 0
     status = _compact(
         _whole(kept, _I32T, (B, lists, n), "kept"), lists, n, _vector(counts, _I32T, B, "counts"), pf, pt, ldt,
-        per_seq, pd, ldd, per_dst, pc, pages, page_size, B, kv_heads, head_dim, pm, _stream_handle(stream))
+        per_seq, pd, ldd, per_dst, pc, pages, page_size, B, kv_heads, head_dim, pm, _stream_for(cache, stream))
     if status:
         raise LoraError("lora_kv_compact", status)
