@@ -12,9 +12,16 @@
 // four lanes that share the tokens are joined once, at the end.  Every token has one
 // writer, and its sum is always taken in the same order.
 //
-// Few rows: a wave walks chunks of 64 tokens of a key head, the next one's keys on
+// Few rows: a wave walks chunks of 64 tokens of a key head, the next ones' keys on
 // their way, with the rows in shared memory.  Many: a wave keeps the keys of one chunk
 // in registers, and the rows come by.
+//
+// Bound by: HBM with one tile of rows (64 sequences of up to 8192 tokens, 8 key heads of
+// 128: 39.5 us, 4.1 TB/s where a copy reaches 5.0 to 5.5); with many rows by the
+// instructions that the units take in turn (8 sequences in pieces of 129 to 512 queries, 8
+// key heads of 8: 155 us, 790 TFLOP/s; vector instructions 51% of the cycles, of which the
+// exponentials, their arguments and sums are 48 of 89 a tile and chunk, the matrix unit
+// 31%).
 
 #include "kv_attention.hpp"
 
@@ -22,7 +29,11 @@ namespace lora {
 
 constexpr int kMassWaves = 8;
 constexpr int kMassThreads = kMassWaves * kWave;
-constexpr int kFewTiles = 8;       // of 16 rows, at most, for the kernel of few
+// Tiles of 16 rows, at most, for the kernel of few: as many as two workgroups a compute
+// unit have room for in shared memory, beside a tree's masks (us, this kernel / that of
+// many: 16 sequences of 4096 tokens, 8 key heads: 32 rows 15 / 64, 128 rows 28 / 81, 256
+// rows 46 / 97; one of 32768: 128 rows 18 / 36).
+__host__ __device__ constexpr int few_tiles(int V) { return V == kTree ? 14 : 16; }
 constexpr int kShares = 4;         // of the rows, for that of many: waves that share a chunk
 constexpr float kLog2e = 1.44269504f;
 
@@ -434,15 +445,16 @@ static void launch_mass(const MassArgs& m, int num_seqs, hipStream_t stream) {
     longest = longest < seen ? longest : seen;
   }
   const int64_t chunks = (longest + kChunk - 1) / kChunk;
-  const bool few = rows <= kFewTiles * kTile;
-  // As many workgroups as the device holds, and several times that of those whose lengths differ in
-  // rows as well.
+  const bool few = rows <= few_tiles(V) * kTile;
+  // Of few rows as many workgroups as the device holds (64 sequences of up to 8192 tokens:
+  // 40 us, with twice as many 46), of many, whose work differs in the rows as well, several
+  // times that.
   const int64_t most = few ? (chunks + kMassWaves - 1) / kMassWaves : (chunks * kShares + kMassWaves - 1) / kMassWaves;
   int64_t groups = ((few ? 2 : 16) * kCus + units - 1) / units;
   groups = groups < most ? groups : most;
   const dim3 grid(heads, static_cast<unsigned>(groups), num_seqs), block(kMassThreads);
   if (rows <= kTile) hipLaunchKernelGGL((kv_mass_kernel<D, V, 1>), grid, block, 0, stream, m);
-  else if (few) hipLaunchKernelGGL((kv_mass_kernel<D, V, kFewTiles>), grid, block, 0, stream, m);
+  else if (few) hipLaunchKernelGGL((kv_mass_kernel<D, V, few_tiles(V)>), grid, block, 0, stream, m);
   else hipLaunchKernelGGL((kv_mass_rows_kernel<D, V>), grid, block, 0, stream, m);
 }
 
