@@ -130,13 +130,18 @@ lora_status_t lora_kv_attention_mass(const uint16_t *q, int64_t ldq, const float
  *   kept         int32 [num_seqs][kv_heads][budget], contiguous: the tokens' numbers,
  *                ascending; -1 past the last.
  *   new_lens     int32 [num_seqs]: how many each key head keeps; not seq_lens itself.
- * Enqueues one kernel.
+ *   workspace    of lora_kv_select_workspace_bytes(...), 256-byte aligned, free for
+ *                reuse when the call's kernels have finished; may be NULL where that is 0.
+ * Enqueues one kernel, or four for long sequences.
  */
+int64_t lora_kv_select_workspace_bytes(int32_t num_seqs, int32_t kv_heads, int32_t max_seq_len);
+
 lora_status_t lora_kv_select(const float *mass, int32_t num_pages, int32_t page_size,
                              const int32_t *seq_lens, const int32_t *page_table, int64_t ld_table,
                              int32_t num_seqs, int32_t kv_heads, int32_t max_seq_len,
                              int32_t sinks, int32_t recent, int32_t *kept, int32_t budget,
-                             int32_t *new_lens, hipStream_t stream);
+                             int32_t *new_lens, void *workspace, int64_t workspace_bytes,
+                             hipStream_t stream);
 
 /*
  * lora_kv_compact - moves cached tokens (keys, values, and their mass) to the places

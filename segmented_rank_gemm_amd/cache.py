@@ -20,7 +20,8 @@ from .attention import (_F32, _I32, _I32T, _I64, _I64T, _MOST, _VP, SUPPORTED_PA
 
 __all__ = [
     "lora_draft_masks", "lora_kv_tree_attention", "lora_kv_tree_attention_workspace_bytes",
-    "kv_tree_attention_workspace", "lora_kv_attention_mass", "lora_kv_select", "lora_kv_compact",
+    "kv_tree_attention_workspace", "lora_kv_attention_mass", "lora_kv_select",
+    "lora_kv_select_workspace_bytes", "kv_select_workspace", "lora_kv_compact",
     "kv_mass_shape", "LORA_MAX_MASK_WORDS",
 ]
 
@@ -37,7 +38,9 @@ def _declare(L: ctypes.CDLL) -> None:
     L.lora_kv_tree_attention.argtypes = [_VP, _I64, *step, _VP, _I64, _VP, _I64, _VP, _I64, _VP]
     L.lora_kv_attention_mass.argtypes = [_VP, _I64, _VP, _I64, *step, _VP, _VP]
     L.lora_kv_select.argtypes = [_VP, _I32, _I32, _VP, _VP, _I64, _I32, _I32, _I32, _I32, _I32, _VP, _I32,
-                                 _VP, _VP]
+                                 _VP, _VP, _I64, _VP]
+    L.lora_kv_select_workspace_bytes.argtypes = [_I32] * 3
+    L.lora_kv_select_workspace_bytes.restype = _I64
     L.lora_kv_compact.argtypes = [_VP, _I32, _I32, _VP, _VP, _VP, _I64, _I32, _VP, _I64, _I32, _VP, _I32,
                                   _I32, _I32, _I32, _I32, _VP, _VP]
     for f in (L.lora_draft_masks, L.lora_kv_tree_attention, L.lora_kv_attention_mass, L.lora_kv_select,
@@ -48,6 +51,7 @@ def _declare(L: ctypes.CDLL) -> None:
 _declare(lib())
 _draft_masks, _tree_attention = lib().lora_draft_masks, lib().lora_kv_tree_attention
 _attention_mass, _select, _compact = lib().lora_kv_attention_mass, lib().lora_kv_select, lib().lora_kv_compact
+_select_bytes = lib().lora_kv_select_workspace_bytes
 
 
 def _current_device() -> int:
@@ -183,20 +187,40 @@ def lora_kv_attention_mass(q: torch.Tensor, lse: torch.Tensor, query_start: torc
         raise LoraError("lora_kv_attention_mass", status)
 
 
+def lora_kv_select_workspace_bytes(num_seqs: int, kv_heads: int, max_seq_len: int) -> int:
+    _fit(num_seqs=num_seqs, kv_heads=kv_heads, max_seq_len=max_seq_len)
+    return int(lib().lora_kv_select_workspace_bytes(num_seqs, kv_heads, max_seq_len))
+
+
+def kv_select_workspace(num_seqs: int, kv_heads: int, max_seq_len: int, device="cuda") -> Optional[torch.Tensor]:
+    """A workspace for lora_kv_select, reused call after call (one stream at a time);
+    None where the sizes need none."""
+    n = lora_kv_select_workspace_bytes(num_seqs, kv_heads, max_seq_len)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
 def lora_kv_select(mass: torch.Tensor, seq_lens: torch.Tensor, page_table: torch.Tensor, sinks: int, recent: int,
                    kept: torch.Tensor, new_lens: torch.Tensor, max_seq_len: Optional[int] = None,
-                   stream: Optional[torch.cuda.Stream] = None) -> None:
+                   stream: Optional[torch.cuda.Stream] = None, workspace: Optional[torch.Tensor] = None) -> None:
     """mass: fp32 (kv_mass_shape); kept: int32 [num_seqs, kv_heads, budget], each key
     head's tokens, ascending, -1 past the last; new_lens: int32 [num_seqs].  Kept are the
-    first sinks tokens, the last recent and the heaviest of the others."""
+    first sinks tokens, the last recent and the heaviest of the others; workspace: of
+    kv_select_workspace for these sizes, or None: one from torch's allocator."""
     pages, kv_heads, page_size = _dims(mass, 3, "mass")
     budget = _dims(kept, 3, "kept")[2]
     B, max_seq_len, _, pn, pt, ldt = _step(None, seq_lens, page_table, page_size, max_seq_len, 1, 0)
     _fit(sinks=sinks, recent=recent, budget=budget, pages=pages)
+    handle = _stream_for(mass, stream)
+    if workspace is None and max_seq_len > 0:
+        need = _select_bytes(B, kv_heads, max_seq_len)
+        if need:
+            with torch.cuda.stream(stream):  # whose later work alone may be given it again
+                workspace = torch.empty(need, dtype=torch.uint8, device=mass.device)
+    wptr, wbytes = (0, 0) if workspace is None else _flat_dev_bytes(workspace, "workspace")
     status = _select(
         _whole(mass, _F32, (pages, kv_heads, page_size), "mass"), pages, page_size, pn, pt, ldt, B, kv_heads,
         max_seq_len, sinks, recent, _whole(kept, _I32T, (B, kv_heads, budget), "kept"), budget,
-        _vector(new_lens, _I32T, B, "new_lens"), _stream_for(mass, stream))
+        _vector(new_lens, _I32T, B, "new_lens"), wptr, wbytes, handle)
     if status:
         raise LoraError("lora_kv_select", status)
 

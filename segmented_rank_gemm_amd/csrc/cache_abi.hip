@@ -21,7 +21,8 @@ hipError_t launch_kv_attention_mass(const uint16_t* q, int64_t ldq, const float*
 hipError_t launch_kv_select(const float* mass, int num_pages, int page_shift, const int32_t* seq_lens,
                             const int32_t* page_table, int64_t ld_table, int num_seqs, int kv_heads,
                             int max_seq_len, int sinks, int recent, int32_t* kept, int budget,
-                            int32_t* new_lens, hipStream_t stream);
+                            int32_t* new_lens, void* workspace, hipStream_t stream);
+int64_t kv_select_workspace_bytes(int num_seqs, int kv_heads, int max_seq_len);
 hipError_t launch_kv_compact(const int32_t* kept, int lists, int max_kept, const int32_t* counts,
                              const int32_t* first, const int32_t* page_table, int64_t ld_table, int pages,
                              const int32_t* dst_table, int64_t ld_dst, int dst_pages, uint8_t* cache,
@@ -141,10 +142,18 @@ lora_status_t lora_kv_attention_mass(const uint16_t* q, int64_t ldq, const float
       mask_words, mass, stream));
 }
 
+int64_t lora_kv_select_workspace_bytes(int32_t num_seqs, int32_t kv_heads, int32_t max_seq_len) {
+  if (num_seqs < 0 || num_seqs > kMaxSeqs || kv_heads < 1 || kv_heads > kMaxHeads || max_seq_len < 1 ||
+      max_seq_len > kMaxSeqLen)
+    return 0;
+  return lora::kv_select_workspace_bytes(num_seqs, kv_heads, max_seq_len);
+}
+
 lora_status_t lora_kv_select(const float* mass, int32_t num_pages, int32_t page_size, const int32_t* seq_lens,
                              const int32_t* page_table, int64_t ld_table, int32_t num_seqs, int32_t kv_heads,
                              int32_t max_seq_len, int32_t sinks, int32_t recent, int32_t* kept,
-                             int32_t budget, int32_t* new_lens, hipStream_t stream) {
+                             int32_t budget, int32_t* new_lens, void* workspace, int64_t workspace_bytes,
+                             hipStream_t stream) {
   if (num_seqs < 0 || num_seqs > kMaxSeqs || kv_heads < 1 || kv_heads > kMaxHeads || max_seq_len < 1 ||
       max_seq_len > kMaxSeqLen || sinks < 0 || recent < 0 || budget < 1 || budget > kMaxBudget ||
       static_cast<int64_t>(sinks) + recent > budget || num_pages < 0 || page_size < 1)
@@ -155,9 +164,12 @@ lora_status_t lora_kv_select(const float* mass, int32_t num_pages, int32_t page_
     return LORA_ERR_INVALID_ARGUMENT;
   if (page_shift(page_size) < 0) return LORA_ERR_UNSUPPORTED;
   if (num_seqs == 0) return LORA_OK;
+  const int64_t need = lora_kv_select_workspace_bytes(num_seqs, kv_heads, max_seq_len);
+  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
+    return LORA_ERR_INVALID_ARGUMENT;
   return launch_status(lora::launch_kv_select(mass, num_pages, page_shift(page_size), seq_lens, page_table,
                                               ld_table, num_seqs, kv_heads, max_seq_len, sinks, recent, kept,
-                                              budget, new_lens, stream));
+                                              budget, new_lens, workspace, stream));
 }
 
 lora_status_t lora_kv_compact(const int32_t* kept, int32_t num_lists, int32_t max_kept, const int32_t* counts,

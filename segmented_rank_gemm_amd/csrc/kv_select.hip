@@ -12,6 +12,16 @@
 // Longer sequences are read once for the first digit, once for those that share it with
 // the last one kept, which go on from shared memory, and once to write.
 //
+// A compute unit takes 15 us to read 131072 weights into a histogram, so a few long lists
+// are cut into pieces of 8192 tokens, a workgroup each, and the digits into launches: each
+// of them joins the histograms that the one before left (which also say how many are kept
+// before the piece), and reads the piece again from the caches.
+//
+// Bound by: the histogram's additions in shared memory and the steps that follow from each
+// other (64 sequences of 4097 to 8192 tokens, 8 key heads: 16.4 us, the 21 MB at 1.3 TB/s,
+// vector instructions 27% of the time; 21 us with 4 waves, 19.9 us with 16); of one
+// sequence of 131072 tokens, the four launches' latencies (21 us; whole 58 us).
+//
 // Non-negative numbers compare as their bits do.  Where there are others (NaNs, which
 // count as -infinity, and pages that do not exist, which weigh as much, among them),
 // which the first reading finds out, the bits are turned into ones that do.
@@ -35,6 +45,36 @@ struct SelectArgs {
   int32_t* kept;
   int32_t* new_lens;
   int num_pages, page_shift, kv_heads, max_seq_len, sinks, recent, budget;
+  uint32_t* work;  // of the pieces; NULL without
+};
+
+// A list in pieces: its stages are launches, between which each piece leaves its part of
+// the digit's histogram (two bins a word), and what it knows.
+constexpr int kPieceVectors = 2;                            // of a thread
+constexpr int kPiece = kPieceVectors * kManyWaves * kVector;  // tokens
+constexpr int kMostPieces = 128, kMostLists = 32;
+constexpr int kWhole = -1, kLastStage = 3;  // stages 0, 1 and 2 count a digit; the last one writes
+struct Known {
+  uint32_t prefix, known, need;  // the border
+  uint32_t keeps, equals;        // before the piece, of those above the border and at it
+  uint32_t done, unused[2];      // nothing is left to be found
+};
+struct Pieces {
+  uint32_t* counts;  // of the list's first piece
+  Known* known;
+  int number;
+
+  static __host__ __device__ constexpr int64_t words(int pieces) {
+    return pieces * static_cast<int64_t>(2 * (kBins / 2) + sizeof(Known) / sizeof(uint32_t));
+  }
+  __device__ __forceinline__ Pieces(const SelectArgs& a, int64_t list) : number((a.max_seq_len + kPiece - 1) / kPiece) {
+    counts = a.work + list * words(number);
+    known = reinterpret_cast<Known*>(counts + number * kBins);
+  }
+  // two histograms take turns: one is read while the next one is written
+  __device__ __forceinline__ uint32_t* counts_of(int piece, int stage) const {
+    return counts + (2 * piece + (stage & 1)) * (kBins / 2);
+  }
 };
 
 constexpr uint32_t kInfinity = 0x7F800000u, kNegative = 0x80000000u;
@@ -115,7 +155,7 @@ struct Border {
 struct Finder {
   uint32_t bins[kBins];
   uint32_t above[kManyWaves];
-  uint32_t digit, need, count;
+  uint32_t digit, need, count, equals;
 };
 
 template <int WAVES>
@@ -187,30 +227,74 @@ __device__ __forceinline__ void run_of(const Source& s, int begin, int end, bool
   }
 }
 
+// The digit at `shift` from the pieces' histograms of `stage`, of a list of n tokens; and
+// what lies before this piece.
+template <int WAVES>
+__device__ __forceinline__ void join_pieces(Finder& f, Border& b, Known& k, const Pieces& pieces, int piece,
+                                            int n, int stage, int shift, int bits) {
+  static_assert(WAVES * kWave * 2 == kBins, "a word a thread");
+  const int tid = static_cast<int>(threadIdx.x);
+  const int number = (n + kPiece - 1) / kPiece;
+  uint32_t all[2] = {0, 0}, before[2] = {0, 0};
+#pragma unroll 8
+  for (int p = 0; p < number; ++p) {
+    const uint32_t two = pieces.counts_of(p, stage)[tid];
+    if (p == piece) {
+      before[0] = all[0];
+      before[1] = all[1];
+    }
+    all[0] += two & 0xFFFFu;
+    all[1] += two >> 16;
+  }
+  f.bins[2 * tid] = all[0];
+  f.bins[2 * tid + 1] = all[1];
+  const uint32_t same = find_digit<WAVES>(f, b, shift, bits);
+  const uint32_t digit = f.digit, first = 2u * static_cast<uint32_t>(tid);
+  uint32_t above = (first > digit ? before[0] : 0u) + (first + 1 > digit ? before[1] : 0u);
+#pragma unroll
+  for (int d = 1; d < kWave; d *= 2) above += __shfl_xor(above, d);
+  if (lane_id() == 0) f.above[wave_index()] = above;
+  if (digit >> 1 == static_cast<uint32_t>(tid)) f.equals = before[digit & 1];
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) k.keeps += f.above[w];
+  k.equals = f.equals;
+  k.done = same == b.need;
+}
+
 // R: vectors of a thread that are kept in registers; 0: sequences that do not fit.
-template <int R, int WAVES>
+// STAGE: of a list in pieces, of which the workgroup has one; kWhole: it has the list.
+template <int R, int WAVES, int STAGE = kWhole>
 __global__ __launch_bounds__(WAVES * kWave) void kv_select_kernel(SelectArgs a) {
+  static_assert(STAGE == kWhole || (R == kPieceVectors && WAVES == kManyWaves), "a piece");
   const int head = static_cast<int>(blockIdx.x), seq = static_cast<int>(blockIdx.y);
+  const int piece = STAGE == kWhole ? 0 : static_cast<int>(blockIdx.z), start = piece * kPiece;
   const int tid = static_cast<int>(threadIdx.x), wave = wave_index(), lane = lane_id();
   const Source source = source_of(a, seq, head);
   Weights<R ? R : 1> own;
   if constexpr (R > 0) {  // beside the length
     uint32_t pages[R];
-    look_up(source, wave * R * kVector, pages);
+    look_up(source, start + wave * R * kVector, pages);
     own.load(source, pages);
   }
   int n = a.seq_lens[seq];
   n = n < 0 ? 0 : (n < a.max_seq_len ? n : a.max_seq_len);
   int32_t* kept = a.kept + (static_cast<int64_t>(seq) * a.kv_heads + head) * a.budget;
-  if (head == 0 && tid == 0) a.new_lens[seq] = n < a.budget ? n : a.budget;
-  if (n <= a.budget) {
-    for (int i = tid; i < a.budget; i += WAVES * kWave) kept[i] = i < n ? i : -1;
+  if constexpr (STAGE == kWhole || STAGE == kLastStage) {
+    if (head == 0 && piece == 0 && tid == 0) a.new_lens[seq] = n < a.budget ? n : a.budget;
+    if (n <= a.budget) {
+      const int step = (STAGE == kWhole ? 1 : static_cast<int>(gridDim.z)) * WAVES * kWave;
+      for (int i = piece * WAVES * kWave + tid; i < a.budget; i += step) kept[i] = i < n ? i : -1;
+      return;
+    }
+  } else if (n <= a.budget) {
     return;
   }
+  if (STAGE != kWhole && start >= n) return;
   const int low = a.sinks, high = n - a.recent;  // those between are weighed
   // This wave's run.
   const int length = R ? R * kVector : (n + WAVES * kVector - 1) / (WAVES * kVector) * kVector;
-  const int begin = wave * length < n ? wave * length : n;
+  const int at = start + wave * length, begin = at < n ? at : n;
   const int end = begin + length < n ? begin + length : n;
   bool turned = false;
   const auto all = [&](const auto& visit) {
@@ -239,7 +323,38 @@ __global__ __launch_bounds__(WAVES * kWave) void kv_select_kernel(SelectArgs a) 
   Border b = {0, 0, static_cast<uint32_t>(a.budget - a.sinks - a.recent)};
   uint32_t above = 0, mine = 0;  // of the run, above the first digit; of this thread's, that share it
   bool gathered = false;
-  if (b.need == 0) {
+  Known k = {};
+  if constexpr (STAGE != kWhole) {
+    // digits of 11, 11 and 10 bits, as below
+    constexpr int kShift[] = {21, 10, 0}, kBits[] = {11, 11, 10};
+    const Pieces pieces(a, static_cast<int64_t>(seq) * a.kv_heads + head);
+    if constexpr (STAGE > 1) {
+      k = pieces.known[piece];
+      b = {k.prefix, k.known, k.need};
+    } else if (b.need == 0) {
+      b.prefix = b.known = 0xFFFFFFFFu;
+      k.done = 1;
+    }
+    if constexpr (STAGE > 0) {
+      if (!k.done) join_pieces<WAVES>(f, b, k, pieces, piece, n, STAGE - 1, kShift[STAGE - 1], kBits[STAGE - 1]);
+      if (STAGE < kLastStage && tid == 0)
+        pieces.known[piece] = {b.prefix, b.known, b.need, k.keeps, k.equals, k.done, {0, 0}};
+    }
+    own.check_pages();
+    own.order();
+    if constexpr (STAGE < kLastStage) {
+      if (k.done) return;
+      clear_bins<WAVES>(f);
+      all([&](int first, const u32x4& w) {
+        weighed(first, w, [&](uint32_t x, bool in) {
+          if (in && b.shares(x)) atomicAdd(&f.bins[x >> kShift[STAGE] & ((1u << kBits[STAGE]) - 1)], 1u);
+        });
+      });
+      __syncthreads();
+      pieces.counts_of(piece, STAGE)[tid] = f.bins[2 * tid] | f.bins[2 * tid + 1] << 16;
+      return;
+    }
+  } else if (b.need == 0) {
     b.prefix = b.known = 0xFFFFFFFFu;  // none is above, and none of the equal ones is taken
   } else {
     clear_bins<WAVES>(f);
@@ -371,6 +486,10 @@ __global__ __launch_bounds__(WAVES * kWave) void kv_select_kernel(SelectArgs a) 
     k0 += __shfl_xor(k0, d);
     e0 += __shfl_xor(e0, d);
   }
+  if constexpr (STAGE != kWhole) {
+    k0 += k.keeps + static_cast<uint32_t>((low < start ? low : start) + (start > high ? start - high : 0));
+    e0 += k.equals;
+  }
   k0 = __builtin_amdgcn_readfirstlane(k0);  // kept, and equal, before the vector
   e0 = __builtin_amdgcn_readfirstlane(e0);
 
@@ -412,13 +531,40 @@ __global__ __launch_bounds__(WAVES * kWave) void kv_select_kernel(SelectArgs a) 
   });
 }
 
+// Pieces of each list; 0: it is left whole.  Pieces use the compute units that a few whole
+// lists leave idle, but their four launches read the weights four times, and every piece
+// all histograms.  us in pieces / whole, by lists:
+//   65536 tokens    8: 19 / 34    32: 21 / 35    128: 61 / 37
+//   131072 tokens   8: 21 / 58    16: 22 / 59     64: 67 / 62
+//   262144 tokens   8: 25 / 106                   64: 142 / 111
+//   524288 tokens   8: 50 / 200   32: 181 / 206
+//   1048576 tokens  1: 47 / 377    8: 134 / 390
+// and 3 pieces 17 / 17 for 8 lists, 20 / 19 for 32.
+static int pieces_of(int num_seqs, int kv_heads, int max_seq_len) {
+  const int pieces = (max_seq_len - 1) / kPiece + 1;
+  return pieces > 3 && pieces <= kMostPieces && static_cast<int64_t>(num_seqs) * kv_heads <= kMostLists ? pieces : 0;
+}
+
+int64_t kv_select_workspace_bytes(int num_seqs, int kv_heads, int max_seq_len) {
+  return static_cast<int64_t>(num_seqs) * kv_heads * Pieces::words(pieces_of(num_seqs, kv_heads, max_seq_len)) *
+         static_cast<int64_t>(sizeof(uint32_t));
+}
+
 hipError_t launch_kv_select(const float* mass, int num_pages, int page_shift, const int32_t* seq_lens,
                             const int32_t* page_table, int64_t ld_table, int num_seqs, int kv_heads,
                             int max_seq_len, int sinks, int recent, int32_t* kept, int budget,
-                            int32_t* new_lens, hipStream_t stream) {
+                            int32_t* new_lens, void* workspace, hipStream_t stream) {
   const SelectArgs a = {mass, seq_lens, page_table, ld_table, kept, new_lens, num_pages, page_shift,
-                        kv_heads, max_seq_len, sinks, recent, budget};
+                        kv_heads, max_seq_len, sinks, recent, budget, static_cast<uint32_t*>(workspace)};
   const dim3 grid(kv_heads, num_seqs), few(kFewWaves * kWave), many(kManyWaves * kWave);
+  if (const int pieces = pieces_of(num_seqs, kv_heads, max_seq_len)) {
+    const dim3 parts(kv_heads, num_seqs, pieces);
+    hipLaunchKernelGGL((kv_select_kernel<kPieceVectors, kManyWaves, 0>), parts, many, 0, stream, a);
+    hipLaunchKernelGGL((kv_select_kernel<kPieceVectors, kManyWaves, 1>), parts, many, 0, stream, a);
+    hipLaunchKernelGGL((kv_select_kernel<kPieceVectors, kManyWaves, 2>), parts, many, 0, stream, a);
+    hipLaunchKernelGGL((kv_select_kernel<kPieceVectors, kManyWaves, kLastStage>), parts, many, 0, stream, a);
+    return hipGetLastError();
+  }
   constexpr int kFit = kFewWaves * kVector;  // tokens of a vector a thread
   if (max_seq_len <= kFit) hipLaunchKernelGGL((kv_select_kernel<1, kFewWaves>), grid, few, 0, stream, a);
   else if (max_seq_len <= 2 * kFit) hipLaunchKernelGGL((kv_select_kernel<2, kFewWaves>), grid, few, 0, stream, a);

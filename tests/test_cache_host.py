@@ -22,7 +22,7 @@ def test_header_entry_points_are_exported_and_bound():
     text = re.sub(r"/\*.*?\*/", "", open(os.path.join(INCLUDE, "lora_cache.h")).read(), flags=re.S)
     names = sorted(set(re.findall(r"\b(lora_[a-z_]+)\s*\(", text)))
     assert names == ["lora_draft_masks", "lora_kv_attention_mass", "lora_kv_compact", "lora_kv_select",
-                     "lora_kv_tree_attention", "lora_kv_tree_attention_workspace_bytes"]
+                     "lora_kv_select_workspace_bytes", "lora_kv_tree_attention", "lora_kv_tree_attention_workspace_bytes"]
     L = ctypes.CDLL(srg.LIB_PATH)
     for n in names:
         assert hasattr(L, n) and hasattr(srg, n) and n in srg.__all__, n
@@ -104,7 +104,10 @@ def test_attention_mass_refuses(change, status):
 
 
 SELECT = dict(mass=FAKE, num_pages=3, page_size=16, seq_lens=FAKE, page_table=FAKE, ld_table=4, num_seqs=2, kv_heads=2,
-              max_seq_len=64, sinks=2, recent=3, kept=FAKE, budget=10, new_lens=FAKE + 64, stream=None)
+              max_seq_len=64, sinks=2, recent=3, kept=FAKE, budget=10, new_lens=FAKE + 64, workspace=None,
+              workspace_bytes=0, stream=None)
+LONG = dict(ld_table=2048, max_seq_len=32768)  # in pieces
+
 
 
 @pytest.mark.parametrize("change,status", [
@@ -116,9 +119,23 @@ SELECT = dict(mass=FAKE, num_pages=3, page_size=16, seq_lens=FAKE, page_table=FA
     (dict(max_seq_len=(1 << 30) + 1), INVALID), (dict(sinks=-1), INVALID), (dict(recent=-1), INVALID),
     (dict(sinks=8), INVALID), (dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1), INVALID), (dict(kept=None), INVALID),
     (dict(budget=0), INVALID), (dict(budget=(1 << 30) + 1), INVALID), (dict(new_lens=None), INVALID),
-    (dict(new_lens=FAKE), INVALID)])
+    (dict(new_lens=FAKE), INVALID), (dict(LONG), INVALID), (dict(LONG, workspace=FAKE, workspace_bytes=100), INVALID),
+    (dict(LONG, workspace=FAKE + 16, workspace_bytes=1 << 30), INVALID), (dict(LONG, workspace_bytes=1 << 30), INVALID)])
 def test_select_refuses(change, status):
     assert srg.lib().lora_kv_select(*{**SELECT, **change}.values()) == status
+
+
+def test_select_workspace():
+    size = srg.lora_kv_select_workspace_bytes
+    assert size(2, 2, 64) == size(64, 8, 131072) == size(0, 8, 131072) == size(1, 8, 1 << 30) == 0
+    for seqs, heads, most in ((0, 0, 131072), (-1, 8, 131072), (1, 8, 0), (1, 8, -5), (1, 1025, 131072), (65536, 1, 131072)):
+        assert size(seqs, heads, most) == 0
+    # two histograms of 2048 counts of 16 bits a piece of 8192 tokens, and 32 bytes
+    for seqs, heads, pieces in ((1, 8, 4), (4, 8, 16), (32, 1, 128)):
+        for most in ((pieces - 1) * 8192 + 1, pieces * 8192):
+            assert size(seqs, heads, most) == seqs * heads * pieces * (2 * 4096 + 32)
+    assert srg.kv_select_workspace(64, 8, 8192, device="cpu") is None
+    assert srg.kv_select_workspace(1, 8, 131072, device="cpu").numel() == size(1, 8, 131072)
 
 
 COMPACT = dict(kept=FAKE, num_lists=2, max_kept=5, counts=FAKE, first=FAKE, page_table=FAKE, ld_table=4, table_pages=4,

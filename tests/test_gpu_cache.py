@@ -354,6 +354,27 @@ def test_select(lens, kv, page, sinks, recent, budget, kind):
     check_selected(mass, lens, table, sinks, recent, budget)
 
 
+@pytest.mark.parametrize("lens,kv,page,sinks,recent,budget", [
+    ([24577], 1, 64, 0, 0, 1), ([32768], 2, 16, 0, 0, 32767), ([32769, 100, 8192, 8193], 2, 64, 9000, 9000, 20000),
+    ([0, 40000, 16385], 3, 32, 4, 512, 16384), ([131072], 1, 256, 0, 70000, 70001), ([131072], 2, 64, 20000, 0, 20000),
+    ([30000], 1, 64, 4, 4, 60000), ([131071], 8, 64, 4, 512, 65536)])
+@pytest.mark.parametrize("kind", ["spread", "ties", "special", "one digit", "equal"])
+def test_select_in_pieces(lens, kv, page, sinks, recent, budget, kind):
+    rng = np.random.default_rng(sum(lens))
+    make = {"spread": lambda shape: np.exp(3 * rng.standard_normal(shape)),
+            "ties": lambda shape: rng.integers(0, 3, shape).astype(float),
+            "special": lambda shape: rng.choice(
+                [np.nan, np.inf, -np.inf, 0.0, -0.0, 1.0, -1.0, 1e-45, -1e-45, 3e38], shape),
+            "one digit": lambda shape: 1 + 2.0 ** -23 * rng.integers(0, 5000, shape),
+            "equal": lambda shape: np.full(shape, 0.5)}[kind]
+    mass, table = paged(rng, lens, kv, page, make)
+    most = table.shape[1] * page
+    assert srg.lora_kv_select_workspace_bytes(len(lens), kv, most) > 0
+    check_selected(mass, lens, table, sinks, recent, budget)
+    ws = srg.kv_select_workspace(len(lens), kv, most).random_()  # whatever it held
+    check_selected(mass, lens, table, sinks, recent, budget, workspace=ws)
+
+
 def test_select_of_neighbours_in_every_bit():
     """Weights that differ in one bit, at every place of the number."""
     rng = np.random.default_rng(2)
@@ -371,6 +392,10 @@ def test_select_with_bad_pages_and_a_length_past_the_most():
     table[0, 1], table[2, 0], table[2, 5] = -1, mass.shape[0], 2 ** 31 - 1
     check_selected(mass, [100, -3, 90], table, 3, 4, 40)
     check_selected(mass, [100, 2 ** 31 - 1, 90], table, 3, 4, 40, most=64, max_seq_len=64)
+    mass, table = paged(rng, [50000, 16], 2, 16, lambda shape: rng.standard_normal(shape))
+    table[0, 1:3000:7], table[0, 40], table[0, 41] = -1, mass.shape[0], 2 ** 31 - 1
+    check_selected(mass, [50000, -3], table, 3, 4, 30000)
+    check_selected(mass, [2 ** 31 - 1, 0], table, 3, 4, 30000, most=40000, max_seq_len=40000)
 
 
 # ------------------------------------------------------------------ compact

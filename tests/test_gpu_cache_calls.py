@@ -87,6 +87,46 @@ def test_a_step_captured_and_replayed():
             assert torch.equal(a, b), seed
 
 
+def test_a_long_choice_captured_on_streams_and_with_a_workspace():
+    """A list in pieces, with a workspace of its own, the caller's, and a graph's; two at
+    once on two streams."""
+    kv, page, n = 4, 64, 60000
+    pages = -(-n // page)
+    table = torch.randperm(pages, device="cuda").int()[None]
+    mass, other = (torch.zeros(srg.kv_mass_shape(pages, kv, page), device="cuda").exponential_() for _ in range(2))
+    lens, new = ints([n]), torch.zeros(1, dtype=torch.int32, device="cuda")
+    kept = lambda: torch.zeros(1, kv, 20000, dtype=torch.int32, device="cuda")  # noqa: E731
+    assert srg.lora_kv_select_workspace_bytes(1, kv, pages * page) > 0
+
+    def want(mass, length):
+        by_head = mass[table[0].long()].transpose(0, 1).reshape(kv, -1)[:, :length].cpu().numpy()
+        return [C.select(by_head[h].tolist(), length, 4, 100, 20000) for h in range(kv)]
+
+    captured, graph = kept(), torch.cuda.CUDAGraph()
+    srg.lora_kv_select(mass, lens, table, 4, 100, captured, new)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        srg.lora_kv_select(mass, lens, table, 4, 100, captured, new)
+    for length in (n, 50001, 41000):
+        lens.fill_(length)
+        mass.exponential_()
+        graph.replay()
+        eager = kept()
+        srg.lora_kv_select(mass, lens, table, 4, 100, eager, new, workspace=srg.kv_select_workspace(1, kv, pages * page))
+        assert captured[0].tolist() == want(mass, length) and torch.equal(captured, eager)
+    streams, lists = [torch.cuda.Stream() for _ in range(2)], [kept(), kept()]
+    news = [torch.zeros_like(new), torch.zeros_like(new)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for stream, m, k, count in zip(streams, (mass, other), lists, news):
+            srg.lora_kv_select(m, lens, table, 4, 100, k, count, stream=stream)
+    torch.cuda.synchronize()
+    for m, k in zip((mass, other), lists):
+        assert k[0].tolist() == want(m, 41000)
+    with pytest.raises(srg.LoraError):
+        srg.lora_kv_select(mass, lens, table, 4, 100, captured, new, workspace=torch.empty(1000, dtype=torch.uint8, device="cuda"))
+
+
 def test_on_another_stream():
     s = Buffers()
     cache, side = s.cache.clone(), torch.cuda.Stream()
