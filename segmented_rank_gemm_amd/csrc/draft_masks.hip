@@ -7,7 +7,8 @@
 // steps as the tree is deep.  Parents lie before their children (others are taken for
 // roots), so that every climb ends.
 //
-// Bound by latency: two dependent loads, the climb and the stores.
+// Bound by latency: two dependent loads, the climb and the stores (1 sequence of 26 drafts
+// 2.0 us, 16 of 32 4.7 us, an empty launch 1.9).
 
 #include "kv_attention.hpp"
 

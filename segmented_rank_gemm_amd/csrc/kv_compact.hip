@@ -14,11 +14,16 @@
 // source itself takes its token, whose place takes its own, and so on.  These chains
 // have nothing in common, each step is a thousand places long, and there are as many of
 // them as tokens were left out.  What lies before goes in blocks first, in a launch of
-// its own (that list: 47 us in all).
+// its own (that list: 71 us in all).
 //
 // A wave moves 64 tokens at a time, several times that in flight: each lane finds out
 // where one token is and goes, and moves its scale bytes and its weight; the codes are
 // moved by as many lanes a token as it has 16-byte pieces, which ask that lane.
+//
+// Bound by: HBM's lines of 128 bytes, of which a token's codes are 64 and its scale bytes
+// one each (16 sequences of up to 8192 tokens, half of them into new pages, heads of 128,
+// with the mass: 42 us, the 149 MB that have to move at 3.6 TB/s, 175 MB as counted at
+// 4.2; chains, whose neighbours go different ways: 71 us, 242 MB as counted).
 
 #include "kv_format.hpp"
 
@@ -258,7 +263,10 @@ static void launch_compact(const CompactArgs& a, int num_seqs, hipStream_t strea
   const int64_t units = static_cast<int64_t>(num_seqs) * a.cache.kv_heads * 2;
   const dim3 grid(2 * a.cache.kv_heads, num_seqs, 1);
   // By chains where the device has more compute units than half of them could use, and
-  // the list more than a few blocks.
+  // the list more than a few blocks (us, chains / blocks, heads of 128: 5000 entries of
+  // one sequence 14.2 / 14.0, 16384 of 32768 tokens 21 / 39.5, 65536 of 131072 71 / 225;
+  // 16384 of 4 sequences, 64 units, 112 / 114).  A list that leaves out next to nothing
+  // has few chains (16 tokens of 65552: 151 / 119).
   if (!a.dst_table && units <= kCus / 4 && a.max_kept > 4 * kNearBlock) {
     hipLaunchKernelGGL(kv_compact_near_kernel<D>, grid, dim3(kNearBlock), 0, stream, a);
     const int64_t all = (static_cast<int64_t>(a.max_kept) + kChainWaves * kWave - 1) / (kChainWaves * kWave);
@@ -268,7 +276,8 @@ static void launch_compact(const CompactArgs& a, int num_seqs, hipStream_t strea
                        dim3(kChainWaves * kWave), 0, stream, a);
     return;
   }
-  // A few accepted drafts: a wave's lanes hold a list, and wait for no others' loads.
+  // A few accepted drafts: a wave's lanes hold a list, and wait for no others' loads
+  // (64 sequences of 6: 3.0 us, with four times as many in flight 4.5).
   if (a.max_kept <= kNearBlock) {
     const int threads = (a.max_kept + kWave - 1) / kWave * kWave;
     hipLaunchKernelGGL((kv_compact_kernel<D, 1>), grid, dim3(threads), 0, stream, a);
