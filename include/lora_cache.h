@@ -161,9 +161,9 @@ lora_status_t lora_kv_select(const float *mass, int32_t num_pages, int32_t page_
  *   mass         may be NULL.
  * Entries below 0, and those whose source or destination lies outside its table or on
  * a page outside [0, num_pages), are skipped: their destinations stay as they are.
- * In place the entries before the first one below 0 ascend (what the places named hold
- * afterwards is open otherwise); kept[j] = j leaves the token where it is.  No page may
- * then stand twice among those that hold the places named.
+ * In place the entries ascend, those below 0 behind all others (what the places named
+ * hold afterwards is open otherwise); kept[j] = j leaves the token where it is.  No page
+ * may then stand twice among those that hold the places named.
  * Enqueues one kernel, or two for long lists of few key heads in place.
  */
 lora_status_t lora_kv_compact(const int32_t *kept, int32_t num_lists, int32_t max_kept,

@@ -214,12 +214,13 @@ __global__ __launch_bounds__(kChainWaves * kWave) void kv_compact_chain_kernel(C
   const int step = static_cast<int>(gridDim.z) * kChainWaves * kWave;
   for (int start = from + (static_cast<int>(blockIdx.z) * kChainWaves + wave) * kWave; start < m.count; start += step) {
     // The first entry from `start` on: of 64 even parts the one that it is in, until
-    // they are single entries.
+    // they are single entries.  (Those below 0, behind all others, count as large.)
     int low = from, high = m.count;
     while (high > low) {
       const int part = (high - low + kWave - 1) / kWave;
       const int64_t probe = low + static_cast<int64_t>(lane) * part;
-      const int before = static_cast<int>(__popcll(__ballot(probe < high && m.kept[probe < high ? probe : low] < start)));
+      const uint32_t entry = static_cast<uint32_t>(m.kept[probe < high ? probe : low]);
+      const int before = static_cast<int>(__popcll(__ballot(probe < high && entry < static_cast<uint32_t>(start))));
       if (before == 0) break;
       const int64_t next = low + static_cast<int64_t>(before) * part;
       low = low + (before - 1) * part + 1;

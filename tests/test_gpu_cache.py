@@ -508,6 +508,18 @@ def test_compact_of_long_lists_in_place(parts, d, lists):
     m.check()
 
 
+@pytest.mark.parametrize("d,n,tail", [(64, 9000, 3000), (128, 9000, 8900), (64, 20000, 64), (64, 20000, 9999), (64, 4097, 1)])
+def test_compact_of_long_lists_in_place_with_entries_below_0_behind(d, n, tail):
+    m = Moves(n, 2, 2, n, 2, d, 64, 2 * n + 5, first=[0, 3])
+    rng = np.random.default_rng(n)
+    for s in range(2):
+        for h in range(2):
+            m.kept[s, h] = np.sort(rng.permutation(2 * n)[:n])
+            m.kept[s, h, n - tail:] = rng.choice([-1, -7, -2 ** 31], tail)
+    m.counts = [n, n]
+    m.check()
+
+
 def test_compact_of_a_long_list_with_one_token_out():
     m = Moves(4, 1, 1, 5000, 1, 64, 64, 5001)
     m.kept[:] = np.delete(np.arange(5001), 77)
