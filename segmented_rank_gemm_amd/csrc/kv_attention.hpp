@@ -235,6 +235,11 @@ __device__ __forceinline__ void see(const AttentionArgs& a, RowTile& t, int leng
   t.chunk1 = (t.last + kChunk - 1) / kChunk;
 }
 
+// Queries of a sequence that count, where all its tokens are walked: so many that those of
+// a call see none of 2^30 tokens, and few enough that places and their differences do not
+// pass 2^31.
+constexpr int kMostQueries = (1 << 30) + (1 << 22);
+
 // False if the tile has no rows in this call.  all: the tile is all of the sequence's rows.
 template <int V = kPlain>
 __device__ __forceinline__ bool tile_of(const AttentionArgs& a, int seq, int tile, RowTile& t,
@@ -243,7 +248,8 @@ __device__ __forceinline__ bool tile_of(const AttentionArgs& a, int seq, int til
   const int end = a.query_start[seq + 1];
   int length = a.seq_lens[seq];
   if (t.start < 0 || t.start >= a.num_tokens || end <= t.start) return false;
-  const int queries = end - t.start;
+  int queries = end - t.start;
+  if (V == kTree || all) queries = queries < kMostQueries ? queries : kMostQueries;
   int mine = queries < a.max_query_len ? queries : a.max_query_len;  // that this call does
   mine = mine < a.num_tokens - t.start ? mine : a.num_tokens - t.start;
   const int row0 = all ? 0 : tile * a.tile_rows;

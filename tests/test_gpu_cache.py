@@ -265,6 +265,20 @@ def test_padded_batch():
         check(mass, after, slack, "mass")
 
 
+@pytest.mark.parametrize("end", [2 ** 31 - 1, 2 ** 31 - 20, 2 ** 30 + 60, 2 ** 30, 1000])
+@pytest.mark.parametrize("bits", ["tree", None])
+def test_more_queries_than_tokens(end, bits):
+    """A sequence whose rows go on past all: of a length far below, they see nothing."""
+    s = Step(12, [60, 300], [5, 40], 4, 2, 64, 16, bits=bits)
+    s.start, s.max_q = [0, 5, end], 40
+    out, lse = s.attend()
+    assert (out[5:] == 0).all() and (lse[5:] == -torch.inf).all()
+    mass = torch.ones(s.pages, s.kv, s.page, device="cuda")
+    s.draw(mass, torch.where(lse == -torch.inf, 1.0, lse))
+    for t in range(300):
+        assert (mass[s.table[1][t // 16], :, t % 16] == 0).all(), t
+
+
 def test_strides_and_scales():
     s = Step(10, [70, 90], [9, 12], 8, 2, 64, 16)
     out, lse = s.attend()
