@@ -356,7 +356,9 @@ def paged(rng, lens, kv, page, weights):
 @pytest.mark.parametrize("lens,kv,page,sinks,recent,budget", [
     ([1, 2, 0, 3], 1, 16, 0, 0, 1), ([40, 17, 33, 5], 2, 16, 2, 5, 17), ([40, 17, 33], 2, 32, 0, 17, 17),
     ([40, 17, 33], 2, 16, 17, 0, 17), ([40, 18], 1, 16, 0, 0, 17), ([4095, 4096, 4097, 8193], 2, 64, 4, 100, 1000),
-    ([9000, 100], 3, 256, 1, 4000, 5001), ([20000], 2, 128, 0, 1, 19999), ([70001], 1, 64, 4, 512, 30000)])
+    ([9000, 100], 3, 256, 1, 4000, 5001), ([20000], 2, 128, 0, 1, 19999), ([70001], 1, 64, 4, 512, 30000),
+    # more long lists than are cut into pieces
+    ([70001, 50, 40000, 32769] + [10, 0, 30001] * 10, 1, 64, 4, 512, 30000)])
 @pytest.mark.parametrize("kind", ["spread", "ties", "special"])
 def test_select(lens, kv, page, sinks, recent, budget, kind):
     rng = np.random.default_rng(sum(lens))
@@ -387,6 +389,17 @@ def test_select_in_pieces(lens, kv, page, sinks, recent, budget, kind):
     check_selected(mass, lens, table, sinks, recent, budget)
     ws = srg.kv_select_workspace(len(lens), kv, most).random_()  # whatever it held
     check_selected(mass, lens, table, sinks, recent, budget, workspace=ws)
+
+
+def test_select_in_as_many_pieces_as_there_are():
+    rng = np.random.default_rng(128)
+    mass, table = paged(rng, [128 * 8192 - 5], 1, 256, lambda shape: rng.standard_normal(shape))
+    assert srg.lora_kv_select_workspace_bytes(1, 1, table.shape[1] * 256) > 0
+    check_selected(mass, [128 * 8192 - 5], table, 5, 300, 600000)
+    # one more page of the table, and the list is left whole
+    table = np.concatenate([table, np.full((1, 1), -1, dtype=np.int32)], axis=1)
+    assert srg.lora_kv_select_workspace_bytes(1, 1, table.shape[1] * 256) == 0
+    check_selected(mass, [128 * 8192 + 100], table, 5, 300, 600000)
 
 
 def test_select_of_neighbours_in_every_bit():
