@@ -18,9 +18,10 @@
 // before the piece), and reads the piece again from the caches.
 //
 // Bound by: the histogram's additions in shared memory and the steps that follow from each
-// other (64 sequences of 4097 to 8192 tokens, 8 key heads: 16.4 us, the 21 MB at 1.3 TB/s,
-// vector instructions 27% of the time; 21 us with 4 waves, 19.9 us with 16); of one
-// sequence of 131072 tokens, the four launches' latencies (21 us; whole 58 us).
+// other (64 sequences of 4097 to 8192 tokens, 8 key heads: 13.9 us, the 21 MB at 1.5 TB/s:
+// up to the first histogram's end 6, then the digits 4, counting and writing 4; with 16
+// waves 15.4); of one sequence of 131072 tokens, the four launches' latencies (21 us;
+// whole 58 us).
 //
 // Non-negative numbers compare as their bits do.  Where there are others (NaNs, which
 // count as -infinity, and pages that do not exist, which weigh as much, among them),
@@ -143,6 +144,18 @@ struct Weights {
       for (int i = 0; i < 4; ++i) w[r][i] = order_of(w[r][i]);
   }
 };
+
+// Sums over the lanes below.
+__device__ __forceinline__ uint32_t sum_below(uint32_t v) {
+  int x = __builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x138, 0xF, 0xF, false);  // the lane below's
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // within 16 lanes, 1, 2, 4 and 8 below
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // the last lane's of the 16 below,
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);  // and of the 32
+  return static_cast<uint32_t>(x);
+}
 
 // What has been found of the last one kept: its digits so far (prefix, under known), and
 // how many of those with these digits are kept.
@@ -425,8 +438,14 @@ __global__ __launch_bounds__(WAVES * kWave) void kv_select_kernel(SelectArgs a) 
   // How many of the run are kept, and how many equal the last one that is (as far as its
   // digits were looked for).
   const uint32_t top = b.top(), bottom = b.prefix, need = b.need;
-  // The lanes with a weight that is kept, and with one that is equal to the last one that
-  // is, by the weight's place in the vector.
+  // In registers (vector by vector, as below, it took 2.5 of 16.4 us more and spilled
+  // scalars): this lane's that are kept, and that are equal to the last one that is, as
+  // bits, and how many of each vector are so in the lanes below (at most 252), as bytes.
+  uint32_t kept_bits = 0, equal_bits = 0, kept_below = 0, equal_below = 0;
+  uint32_t kept_of[R ? R : 1] = {}, equal_of[R ? R : 1] = {};  // of the wave's vectors
+  bool some_equal = false;
+  // Elsewhere, vector by vector: the lanes with a weight that is kept, and with one that is
+  // equal to the last one that is, by the weight's place in the vector.
   struct Lanes {
     unsigned long long keep[4], equal[4];
   };
@@ -449,7 +468,48 @@ __global__ __launch_bounds__(WAVES * kWave) void kv_select_kernel(SelectArgs a) 
     return l;
   };
   uint32_t keeps = 0, equals = 0;
-  if (gathered) {
+  if constexpr (R > 0) {
+    uint32_t kept_own = 0, equal_own = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int first = begin + r * kVector, token = first + 4 * lane;
+      const bool inside = first >= low && first + kVector <= high;
+      uint32_t k = 0, e = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = own.w[r][i];
+        k |= (w > top ? 1u : 0u) << i;
+        e |= (w >= bottom ? 1u : 0u) << i;
+      }
+      if (!inside) {
+        uint32_t in = 0, there = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          in |= (token + i >= low && token + i < high ? 1u : 0u) << i;
+          there |= (token + i < n ? 1u : 0u) << i;
+        }
+        k = (k & in) | (there & ~in);
+        e = (e & in) | k;
+      }
+      e &= ~k;
+      kept_bits |= k << (4 * r);
+      equal_bits |= e << (4 * r);
+      kept_own |= static_cast<uint32_t>(__popc(k)) << (8 * r);
+      equal_own |= static_cast<uint32_t>(__popc(e)) << (8 * r);
+    }
+    kept_below = sum_below(kept_own);
+    some_equal = __any(equal_own != 0);
+    if (some_equal) equal_below = sum_below(equal_own);
+    const uint32_t k1 = __builtin_amdgcn_readlane(kept_below, kWave - 1), k2 = __builtin_amdgcn_readlane(kept_own, kWave - 1);
+    const uint32_t e1 = __builtin_amdgcn_readlane(equal_below, kWave - 1), e2 = __builtin_amdgcn_readlane(equal_own, kWave - 1);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      kept_of[r] = (k1 >> (8 * r) & 255u) + (k2 >> (8 * r) & 255u);
+      equal_of[r] = (e1 >> (8 * r) & 255u) + (e2 >> (8 * r) & 255u);
+      keeps += kept_of[r];
+      equals += equal_of[r];
+    }
+  } else if (gathered) {
     uint32_t k = 0, e = 0;
     for (uint32_t i = 0; i < mine; ++i) {
       const uint32_t x = shared[i][tid];
@@ -497,6 +557,31 @@ __global__ __launch_bounds__(WAVES * kWave) void kv_select_kernel(SelectArgs a) 
   const auto put = [&](uint32_t at, int token) {
     if (at < static_cast<uint32_t>(a.budget)) kept[at] = token;
   };
+  if constexpr (R > 0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int token = begin + r * kVector + 4 * lane;
+      uint32_t k = k0 + (kept_below >> (8 * r) & 255u);
+      if (!some_equal) {
+        k += e0 < need ? e0 : need;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (kept_bits >> (4 * r + i) & 1u) put(k++, token + i);
+      } else {
+        uint32_t e = e0 + (equal_below >> (8 * r) & 255u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool keep = kept_bits >> (4 * r + i) & 1u, equal = equal_bits >> (4 * r + i) & 1u;
+          if (keep || (equal && e < need)) put(k + (e < need ? e : need), token + i);
+          k += keep ? 1u : 0u;
+          e += equal ? 1u : 0u;
+        }
+      }
+      k0 += kept_of[r];
+      e0 += equal_of[r];
+    }
+    return;
+  }
   all([&](int first, const u32x4& w) {
     const Lanes l = lanes_of(first, w);
     const int token = first + 4 * lane;
@@ -534,11 +619,11 @@ __global__ __launch_bounds__(WAVES * kWave) void kv_select_kernel(SelectArgs a) 
 // Pieces of each list; 0: it is left whole.  Pieces use the compute units that a few whole
 // lists leave idle, but their four launches read the weights four times, and every piece
 // all histograms.  us in pieces / whole, by lists:
-//   65536 tokens    8: 19 / 34    32: 21 / 35    128: 61 / 37
+//   65536 tokens    8: 16 / 34    32: 21 / 35    128: 61 / 37
 //   131072 tokens   8: 21 / 58    16: 22 / 59     64: 67 / 62
 //   262144 tokens   8: 25 / 106                   64: 142 / 111
-//   524288 tokens   8: 50 / 200   32: 181 / 206
-//   1048576 tokens  1: 47 / 377    8: 134 / 390
+//   524288 tokens   8: 48 / 200   32: 161 / 206
+//   1048576 tokens  1: 35 / 384    8: 123 / 390
 // and 3 pieces 17 / 17 for 8 lists, 20 / 19 for 32.
 static int pieces_of(int num_seqs, int kv_heads, int max_seq_len) {
   const int pieces = (max_seq_len - 1) / kPiece + 1;
