@@ -851,12 +851,22 @@ static AttentionPlan attention_plan(bool views, int num_seqs, int max_query_len,
   const int64_t rows = static_cast<int64_t>(max_query_len) * (q_heads / kv_heads);
   const int64_t chunks = (max_len + kChunk - 1) / kChunk;
   // One row tile a workgroup also where there are compute units for all of them and
-  // their eight waves are done in a round or two, which four with two tiles are not
-  // (26 rows and 500 tokens, 32 key heads: 12.5 us, two tiles 14.6; but 512 rows and
-  // 32768 tokens, 8 key heads: 174 and 101).  Only for the views that came later: the
-  // plain one's results are those of its tiles.
-  const int64_t narrow = (rows + kTile - 1) / kTile * num_seqs * kv_heads;
-  const int mt = rows <= kTile || (views && narrow <= kCus && chunks <= 2 * split_waves(1)) ? 1 : 2;
+  // their eight waves are done in up to three rounds, which four with two tiles are not
+  // (us, one tile / two: 26 rows and 500 tokens, 32 key heads 12.5 / 14.6; 64 rows, 64
+  // key heads of sequences, 1536 tokens 17 / 19, 2600 22.6 / 23.4, 4096 32 / 29; 512 rows
+  // and 32768 tokens, 8 key heads 174 / 101), and where pairs of tiles are more than the
+  // units but single ones no more than two each (78 rows, 96 key heads of sequences, 480
+  // tiles in 288 pairs, heads of 64: 500 tokens 13.1 / 13.4, 1024 15.4 / 17.6, 4096 33 /
+  // 43; but 512 tiles in 256 pairs, heads of 128, 1024 tokens 20.3 / 17.3).  Where a call
+  // with a window has one tile, and the workspace is sized for two and longer walks, it is
+  // large enough: at most 3 parts of 16 rows, or a workgroup a compute unit, against at
+  // least 7 of 32, or as many workgroups.
+  // Only for the views that came later: the plain one's results are those of its tiles.
+  const int64_t heads = static_cast<int64_t>(num_seqs) * kv_heads;
+  const int64_t narrow = (rows + kTile - 1) / kTile * heads, pairs = (rows + 2 * kTile - 1) / (2 * kTile) * heads;
+  const bool one = (narrow <= kCus && chunks <= 3 * split_waves(1)) ||
+                   (narrow <= 2 * kCus && pairs > kCus && chunks <= 8 * split_waves(1));
+  const int mt = rows <= kTile || (views && one) ? 1 : 2;
   // Workgroups of the rows kernel; with fewer than fill the device twice over
   // (their registers), cutting the tokens up as well gains more than sharing the
   // operands (us, split / rows: 1 sequence of 128 queries of 4096 tokens, 8 key

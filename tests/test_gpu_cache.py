@@ -279,6 +279,22 @@ def test_more_queries_than_tokens(end, bits):
         assert (mass[s.table[1][t // 16], :, t % 16] == 0).all(), t
 
 
+@pytest.mark.parametrize("d,lens,queries,hq,kv,window", [
+    (128, [1536], [26], 32, 32, 0),                                # one row tile a workgroup, in parts
+    (128, [3000], [26], 32, 32, 1400),                             # with a window, and room for longer walks
+    (64, [2000, 1537, 40], [20, 26, 3], 16, 16, 1300),
+    (64, [700] * 20 + [1500, 3, 0, 1100], [13] * 22 + [1, 4], 24, 4, 0),     # single tiles of 288 pairs
+    (64, [700] * 20 + [2500, 3, 0, 1100], [13] * 22 + [1, 4], 24, 4, 1024),
+])
+@pytest.mark.parametrize("bits", ["tree", None])
+def test_one_row_tile_a_workgroup(d, lens, queries, hq, kv, window, bits):
+    s = Step(13, lens, queries, hq, kv, d, 64, bits=bits, window=window)
+    out, lse = s.attend()
+    want = s.want()
+    check(out, want["out"], want["out_slack"], "out")
+    check(lse, want["lse"], want["lse_slack"], "lse")
+
+
 def test_strides_and_scales():
     s = Step(10, [70, 90], [9, 12], 8, 2, 64, 16)
     out, lse = s.attend()
