@@ -63,7 +63,8 @@ lora_status_t lora_draft_masks(const int32_t *parents, const int32_t *query_star
  * t < length - queries and the drafts t = length - queries + j >= 0 whose bit j is set
  * in row i of masks (bits from `queries` on do not count; a token does not see itself
  * unless its own bit is set); with a window, the last `window` of those.  Without masks
- * they are lora_kv_attention's.  A query that sees nothing gets zeros and -infinity.
+ * they are lora_kv_attention's.  (Queries past max_query_len have no rows here, but are
+ * drafts that others may see.)  A query that sees nothing gets zeros and -infinity.
  * out is computed as by lora_kv_attention; lse from the unrounded weights, in fp32.
  *
  *   masks        int64 [num_tokens][mask_words], contiguous; may be NULL.

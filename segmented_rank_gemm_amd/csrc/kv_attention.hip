@@ -954,12 +954,13 @@ hipError_t launch_kv_attention(const uint16_t* q, int64_t ldq, const int32_t* qu
                                void* workspace, hipStream_t stream) {
   const View view = masks ? kTree : (sums ? kSums : kPlain);
   const int group = q_heads / kv_heads;
-  // A window bounds the tokens that any tile walks; the parts are then fewer
+  // A window bounds the tokens that any tile walks, beside the step's own ones (of a
+  // tree as many as masks have bits, also past max_query_len); the parts are then fewer
   // than those that the workspace is sized for.
   if (window >= max_seq_len) window = 0;
   int64_t longest = max_seq_len;
   if (window) {
-    const int64_t seen = static_cast<int64_t>(window) + max_query_len + kChunk;
+    const int64_t seen = window + (masks ? 64 * words : max_query_len) + kChunk;
     longest = longest < seen ? longest : seen;
   }
   const AttentionPlan p = attention_plan(view != kPlain, num_seqs, max_query_len, longest, q_heads, kv_heads);

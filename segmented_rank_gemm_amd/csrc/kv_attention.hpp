@@ -215,14 +215,17 @@ struct RowTile {
 // The tokens that some row of the tile sees, and those that all see, for a sequence of
 // `length` tokens.
 template <int V>
-__device__ __forceinline__ void see(const AttentionArgs& a, RowTile& t, int length) {
+__device__ __forceinline__ void see(const typename ArgsOf<V>::type& a, RowTile& t, int length) {
   if constexpr (V == kTree) {
-    // A row sees from 0 to all `queries` of the drafts, and with a window so many
-    // fewer of the tokens before them.
+    // A row sees from 0 to all of the drafts that its mask has bits for, and with a
+    // window so many fewer of the tokens before them.  (A sequence may have more queries
+    // than those; the call is cut up for as many drafts as there are bits.)
     const int text = t.before > 0 ? t.before : 0;
-    t.last = length;
+    const int bits = t.before + 64 * static_cast<int>(a.words);
+    const int last = bits < length ? bits : length;
+    t.last = last > 0 ? last : 0;
     t.first = a.window && text > a.window ? text - a.window : 0;
-    t.all_first = a.window && t.before + t.queries > a.window ? length - a.window : 0;
+    t.all_first = a.window && last > a.window ? last - a.window : 0;
     t.all_last = t.before;
   } else {
     const int place0 = t.before + t.query0, place1 = t.before + t.query1;
@@ -242,7 +245,7 @@ constexpr int kMostQueries = (1 << 30) + (1 << 22);
 
 // False if the tile has no rows in this call.  all: the tile is all of the sequence's rows.
 template <int V = kPlain>
-__device__ __forceinline__ bool tile_of(const AttentionArgs& a, int seq, int tile, RowTile& t,
+__device__ __forceinline__ bool tile_of(const typename ArgsOf<V>::type& a, int seq, int tile, RowTile& t,
                                         bool all = false) {
   t.start = a.query_start[seq];
   const int end = a.query_start[seq + 1];

@@ -295,6 +295,31 @@ def test_one_row_tile_a_workgroup(d, lens, queries, hq, kv, window, bits):
     check(lse, want["lse"], want["lse_slack"], "lse")
 
 
+@pytest.mark.parametrize("lens,queries,last,most,words,hq,kv,d,window", [
+    ([2000], [16], 1000, 16, 1, 1, 1, 64, 64),                       # tiles of 16 rows, one part
+    ([3000, 2500], [300, 1], 512, 1, 8, 2, 2, 128, 100),             # 512 drafts, of which some count
+    ([3000, 2500], [300, 130], 700, 13, 2, 4, 4, 64, 1300),          # several parts
+    ([4500, 5500], [200, 20], 190, 20, 3, 4, 2, 128, 2500),          # tiles of 32 rows, several parts
+    ([4500, 5500], [200, 20], 2 ** 31 - 1, 20, 3, 4, 2, 64, 2500),
+    ([6000], [64], 5000, 64, 2, 8, 1, 128, 400),
+    ([2100 + 7 * b for b in range(24)], [1] * 20 + [70, 3, 200, 2], 900, 32, 1, 16, 16, 64, 90),   # of 32, one part
+    ([1500 + 7 * b for b in range(8)], [1, 2, 3, 70, 0, 1, 2, 2], 600, 32, 1, 256, 32, 64, 90),    # of 128
+])
+def test_more_queries_than_the_call_takes_in_a_window(lens, queries, last, most, words, hq, kv, d, window):
+    """Drafts from max_query_len on have no rows, and are seen where masks have bits for them."""
+    s = Step(14, lens, queries, hq, kv, d, 64, bits="any", words=words, window=window)
+    s.start[-1], s.max_q = s.start[-2] + last if last < 2 ** 31 - 1 else last, most
+    out, lse = s.attend()
+    want = s.want(max_query_len=most)
+    assert (~np.isnan(want["lse"])).any()
+    check(lse, want["lse"], want["lse_slack"], "lse")
+    check(out, want["out"], want["out_slack"], "out")
+    mass = torch.ones(s.pages, s.kv, s.page, device="cuda")
+    s.draw(mass, torch.where(lse.isnan(), 0.0, lse))
+    after, slack = C.mass_after(np.ones(mass.shape), s.want(max_query_len=most, lse_in=R.f64(lse)))
+    check(mass, after, slack, "mass")
+
+
 def test_strides_and_scales():
     s = Step(10, [70, 90], [9, 12], 8, 2, 64, 16)
     out, lse = s.attend()
