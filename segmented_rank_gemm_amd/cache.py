@@ -85,6 +85,8 @@ def _whole(t: torch.Tensor, dtype: torch.dtype, shape, name: str) -> int:
 
 def _words(masks: torch.Tensor, tokens: int):
     words = _dims(masks, 2, "masks")[1]
+    if not words:  # no address either: the library would take them for none at all
+        raise ValueError("masks have no words")
     return _whole(masks, _I64T, (tokens, words), "masks"), words
 
 

@@ -9,8 +9,10 @@ import re
 
 import numpy as np
 import pytest
+import torch
 
 import segmented_rank_gemm_amd as srg
+from segmented_rank_gemm_amd import cache
 from tests import cache_reference as C
 
 INCLUDE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
@@ -28,6 +30,11 @@ def test_header_entry_points_are_exported_and_bound():
         assert hasattr(L, n) and hasattr(srg, n) and n in srg.__all__, n
     assert int(re.search(r"LORA_MAX_MASK_WORDS (\d+)", open(os.path.join(INCLUDE, "lora_cache.h")).read())[1]) \
         == srg.LORA_MAX_MASK_WORDS
+
+
+def test_masks_have_words():
+    with pytest.raises(ValueError, match="no words"):
+        cache._words(torch.zeros(5, 0, dtype=torch.int64), 5)
 
 
 MASKS = dict(parents=FAKE, query_start=FAKE, num_tokens=5, num_seqs=2, masks=FAKE, mask_words=1, first=FAKE,

@@ -281,6 +281,19 @@ def test_the_binding_refuses(monkeypatch):
         refused(ValueError, call, **kw)
 
 
+def test_masks_without_words_are_not_left_out_masks():
+    s = Buffers()
+    s.draw(0)
+    none = s.masks[:, :0]
+    args = (s.q, s.start, s.lens, s.table, s.cache)
+    with pytest.raises(ValueError):
+        srg.lora_kv_tree_attention(*args, s.out, 0.125, none, s.ws, s.n, lse=s.lse)
+    with pytest.raises(ValueError):
+        srg.lora_kv_attention_mass(s.q, s.lse, *args[1:], s.mass, 0.125, none, s.n)
+    with pytest.raises(ValueError):
+        srg.lora_draft_masks(s.parents, s.start, none, s.positions)
+
+
 def test_calls_over_nothing():
     new = lambda *shape, dtype=torch.int32: torch.zeros(*shape, dtype=dtype, device="cuda")  # noqa: E731
     cache, mass = new(2, 2, 1, 16 * 34, dtype=torch.uint8), new(2, 1, 16, dtype=torch.float32)
