@@ -157,8 +157,9 @@ lora_status_t lora_kv_select(const float *mass, int32_t num_pages, int32_t page_
  *   page_table   int32 [num_seqs][ld_table], of which table_pages entries a sequence
  *                may be read (those of the places named above are).
  *   dst_table    int32 [num_seqs][ld_dst], dst_pages entries a sequence: the pages
- *                that take place first + j; NULL: in place.  None of these may be one
- *                that the call reads from, and none may take the tokens of two places.
+ *                that take place first + j; NULL: in place, and not page_table itself.
+ *                None of these may be one that the call reads from, and none may take
+ *                the tokens of two places.
  *   mass         may be NULL.
  * Entries below 0, and those whose source or destination lies outside its table or on
  * a page outside [0, num_pages), are skipped: their destinations stay as they are.

@@ -235,7 +235,8 @@ def lora_kv_compact(kept: torch.Tensor, counts: torch.Tensor, page_table: torch.
     of them), the tokens that move to the places first + 0, first + 1, ..., counted from
     first (int32 [num_seqs], or None: 0); counts: int32 [num_seqs], how many of the n;
     page_table, dst_table: int32 [num_seqs, pages a sequence], where they are and where
-    they go (None: in place); mass: fp32 (kv_mass_shape), moved along."""
+    they go (None: in place; other pages than those); mass: fp32 (kv_mass_shape), moved
+    along."""
     B, lists, n = _dims(kept, 3, "kept")
     pc, pages, kv_heads, page_size = _cache(cache, head_dim, page_size)
     per_seq = _dims(page_table, 2, "page_table")[1]

@@ -189,6 +189,8 @@ lora_status_t lora_kv_compact(const int32_t* kept, int32_t num_lists, int32_t ma
     return LORA_ERR_INVALID_ARGUMENT;
   if (st != LORA_OK) return st;
   if (!used) return LORA_OK;
+  // in place by the other table: the list would be shared out over places that it still reads
+  if (dst_table == page_table) return LORA_ERR_INVALID_ARGUMENT;
   return launch_status(lora::launch_kv_compact(kept, num_lists, max_kept, counts, first, page_table, ld_table,
                                                table_pages, dst_table, ld_dst, dst_pages, cache, num_pages,
                                                page_shift(page_size), num_seqs, kv_heads, head_dim, mass,

@@ -162,6 +162,13 @@ def test_compact_refuses(change, status):
     assert srg.lib().lora_kv_compact(*{**COMPACT, **change}.values()) == status
 
 
+@pytest.mark.parametrize("dst_pages", [4, 2])
+def test_compact_refuses_its_own_table_as_the_other(dst_pages):
+    """(in place is without another table)"""
+    args = {**COMPACT, "page_table": FAKE, "dst_table": FAKE, "ld_dst": 4, "dst_pages": dst_pages}
+    assert srg.lib().lora_kv_compact(*args.values()) == INVALID
+
+
 def test_calls_over_nothing():
     L = srg.lib()
     nothing = lambda d, *names: [0 if k in names else (None if v in (FAKE, FAKE + 64) else v) for k, v in d.items()]  # noqa: E731
