@@ -130,7 +130,7 @@ lora_status_t lora_kv_attention_mass(const uint16_t *q, int64_t ldq, const float
  *   budget       1..2^30.
  *   kept         int32 [num_seqs][kv_heads][budget], contiguous: the tokens' numbers,
  *                ascending; -1 past the last.
- *   new_lens     int32 [num_seqs]: how many each key head keeps; not seq_lens itself.
+ *   new_lens     int32 [num_seqs]: how many each key head keeps; no part of it is seq_lens'.
  *   workspace    of lora_kv_select_workspace_bytes(...), 256-byte aligned, free for
  *                reuse when the call's kernels have finished; may be NULL where that is 0.
  * Enqueues one kernel, or four for long sequences.

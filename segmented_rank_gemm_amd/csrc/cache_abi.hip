@@ -67,6 +67,12 @@ lora_status_t step_ok(const void* q, int64_t ldq, const void* lse, int64_t ldl, 
   return LORA_OK;
 }
 
+// Arrays of n numbers that have some in common.
+bool share_elements(const int32_t* a, const int32_t* b, int64_t n) {
+  const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return (x < y ? y - x : x - y) < static_cast<uintptr_t>(n) * sizeof(int32_t);
+}
+
 }  // namespace
 
 extern "C" {
@@ -159,7 +165,7 @@ lora_status_t lora_kv_select(const float* mass, int32_t num_pages, int32_t page_
       static_cast<int64_t>(sinks) + recent > budget || num_pages < 0 || page_size < 1)
     return LORA_ERR_INVALID_ARGUMENT;
   if (num_seqs > 0 && (!mass || !aligned(mass, 16) || num_pages < 1 || !seq_lens || !page_table || !kept ||
-                       !new_lens || new_lens == seq_lens ||
+                       !new_lens || share_elements(new_lens, seq_lens, num_seqs) ||
                        ld_table < (static_cast<int64_t>(max_seq_len) + page_size - 1) / page_size))
     return LORA_ERR_INVALID_ARGUMENT;
   if (page_shift(page_size) < 0) return LORA_ERR_UNSUPPORTED;

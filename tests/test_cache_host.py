@@ -132,6 +132,13 @@ def test_select_refuses(change, status):
     assert srg.lib().lora_kv_select(*{**SELECT, **change}.values()) == status
 
 
+@pytest.mark.parametrize("off", [0, 4, 4 * 6, -4, -4 * 6])
+def test_select_refuses_lengths_that_share_places(off):
+    """A key head's workgroup would read a length that another one has already replaced."""
+    args = {**SELECT, "num_seqs": 7, "new_lens": FAKE + off}
+    assert srg.lib().lora_kv_select(*args.values()) == INVALID
+
+
 def test_select_workspace():
     size = srg.lora_kv_select_workspace_bytes
     assert size(2, 2, 64) == size(64, 8, 131072) == size(0, 8, 131072) == size(1, 8, 1 << 30) == 0
