@@ -58,11 +58,17 @@ def _current_device() -> int:
     return torch._C._cuda_getDevice()
 
 
-def _stream_for(t: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> int:
-    """The stream's handle; refuses a call whose tensors are on another device than it."""
+# Of a process that has a single device, one tensor says what there is to say (each of
+# the others costs 0.1 us of a call that takes 8).
+_SEVERAL_DEVICES = torch.cuda.device_count() > 1
+
+
+def _stream_for(stream: Optional[torch.cuda.Stream], t: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
+    """The stream's handle; refuses a call that has a tensor on another device than it."""
     device = _current_device() if stream is None else stream.device_index
-    if t.get_device() != device:
-        raise ValueError(f"the tensors are on device {t.get_device()}, the stream is device {device}'s")
+    if t.get_device() != device or _SEVERAL_DEVICES and any(o is not None and o.get_device() != device for o in others):
+        on = sorted({o.get_device() for o in (t, *others) if o is not None})
+        raise ValueError(f"the tensors are on devices {on}, the stream is device {device}'s")
     return _stream_handle(stream)
 
 
@@ -104,7 +110,8 @@ def lora_draft_masks(parents: torch.Tensor, query_start: torch.Tensor, masks: Op
     pp = _vector(positions, _I32T, T, "positions") if positions is not None else 0
     pf = _vector(first_positions, _I32T, B, "first_positions") if first_positions is not None else 0
     status = _draft_masks(_vector(parents, _I32T, T, "parents"), _vector(query_start, _I32T, B + 1, "query_start"),
-                          T, B, pm, words, pf, pp, _stream_for(parents, stream))
+                          T, B, pm, words, pf, pp,
+                          _stream_for(stream, parents, query_start, masks, positions, first_positions))
     if status:
         raise LoraError("lora_draft_masks", status)
 
@@ -161,7 +168,8 @@ def lora_kv_tree_attention(q: torch.Tensor, query_start: torch.Tensor, seq_lens:
     wptr, wbytes = (0, 0) if workspace is None else _flat_dev_bytes(workspace, "workspace")
     status = _tree_attention(
         pq, ldq, ps, pn, pt, ldt, pc, pages, page_size, T, B, max_query_len, max_seq_len, q_heads, kv_heads,
-        head_dim, scale, window, pm, words, po, ldo, pl, ldl, wptr, wbytes, _stream_for(q, stream))
+        head_dim, scale, window, pm, words, po, ldo, pl, ldl, wptr, wbytes,
+        _stream_for(stream, q, query_start, seq_lens, page_table, cache, out, masks, lse, workspace))
     if status:
         raise LoraError("lora_kv_tree_attention", status)
 
@@ -184,7 +192,7 @@ def lora_kv_attention_mass(q: torch.Tensor, lse: torch.Tensor, query_start: torc
     status = _attention_mass(
         pq, ldq, pl, ldl, ps, pn, pt, ldt, pc, pages, page_size, T, B, max_query_len, max_seq_len, q_heads,
         kv_heads, head_dim, scale, window, pm, words, _whole(mass, _F32, (pages, kv_heads, page_size), "mass"),
-        _stream_for(q, stream))
+        _stream_for(stream, q, lse, query_start, seq_lens, page_table, cache, mass, masks))
     if status:
         raise LoraError("lora_kv_attention_mass", status)
 
@@ -212,7 +220,7 @@ def lora_kv_select(mass: torch.Tensor, seq_lens: torch.Tensor, page_table: torch
     budget = _dims(kept, 3, "kept")[2]
     B, max_seq_len, _, pn, pt, ldt = _step(None, seq_lens, page_table, page_size, max_seq_len, 1, 0)
     _fit(sinks=sinks, recent=recent, budget=budget, pages=pages)
-    handle = _stream_for(mass, stream)
+    handle = _stream_for(stream, mass, seq_lens, page_table, kept, new_lens, workspace)
     if workspace is None and max_seq_len > 0:
         need = _select_bytes(B, kv_heads, max_seq_len)
         if need:
@@ -251,6 +259,7 @@ def lora_kv_compact(kept: torch.Tensor, counts: torch.Tensor, page_table: torch.
     pf = _vector(first, _I32T, B, "first") if first is not None else 0
     status = _compact(
         _whole(kept, _I32T, (B, lists, n), "kept"), lists, n, _vector(counts, _I32T, B, "counts"), pf, pt, ldt,
-        per_seq, pd, ldd, per_dst, pc, pages, page_size, B, kv_heads, head_dim, pm, _stream_for(cache, stream))
+        per_seq, pd, ldd, per_dst, pc, pages, page_size, B, kv_heads, head_dim, pm,
+        _stream_for(stream, cache, kept, counts, page_table, mass, first, dst_table))
     if status:
         raise LoraError("lora_kv_compact", status)

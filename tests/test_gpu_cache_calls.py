@@ -294,6 +294,37 @@ def test_masks_without_words_are_not_left_out_masks():
         srg.lora_draft_masks(s.parents, s.start, none, s.positions)
 
 
+class Elsewhere(torch.Tensor):
+    """A tensor that says it is on another device."""
+
+    def get_device(self):
+        return 1
+
+
+def test_every_tensor_is_on_the_streams_device(monkeypatch):
+    s = Buffers()
+    s.draw(0)
+    monkeypatch.setattr(binding, "_SEVERAL_DEVICES", True)
+    step = dict(q=s.q, query_start=s.start, seq_lens=s.lens, page_table=s.table, cache=s.cache, scale=0.125, masks=s.masks,
+                max_query_len=s.n, lse=s.lse)
+    one = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    for call, args in (
+            (srg.lora_draft_masks, dict(parents=s.parents, query_start=s.start, masks=s.masks, positions=s.positions,
+                                        first_positions=s.text)),
+            (srg.lora_kv_tree_attention, dict(step, out=s.out, workspace=one)),
+            (srg.lora_kv_attention_mass, dict(step, mass=s.mass)),
+            (srg.lora_kv_select, dict(mass=s.mass, seq_lens=s.lens, page_table=s.table, sinks=2, recent=10, kept=s.kept,
+                                      new_lens=s.new_lens, workspace=one)),
+            (srg.lora_kv_compact, dict(kept=s.kept, counts=s.new_lens, page_table=s.table, cache=s.cache, head_dim=s.d,
+                                       mass=s.mass, first=torch.zeros_like(s.lens), dst_table=s.fresh_pages))):
+        for stream in (None, torch.cuda.current_stream()):
+            call(**args, stream=stream)
+            for name, value in args.items():
+                if isinstance(value, torch.Tensor):
+                    with pytest.raises(ValueError, match="device"):
+                        call(**{**args, name: value.as_subclass(Elsewhere)}, stream=stream)
+
+
 def test_calls_over_nothing():
     new = lambda *shape, dtype=torch.int32: torch.zeros(*shape, dtype=dtype, device="cuda")  # noqa: E731
     cache, mass = new(2, 2, 1, 16 * 34, dtype=torch.uint8), new(2, 1, 16, dtype=torch.float32)
