@@ -38,6 +38,8 @@
 // unit 20% of the cycles; 64 drafts of 32768 tokens: 94 us and 5 for the join, 64% and
 // 27%); with few rows by latency (26 drafts behind 500 tokens: 10 us and 2 for the masks).
 
+#include <type_traits>
+
 #include "kv_attention.hpp"
 
 namespace lora {
@@ -278,6 +280,8 @@ __device__ __forceinline__ int64_t unit_of(const AttentionArgs& a, int seq, int 
 
 // A call's arguments behind a loop that does not need them; of the views with more of
 // them they are loaded once more: kept in registers through it they put others out.
+// Only for kernels whose one parameter they are, at the front of their argument segment
+// (launch_for looks at that).
 template <int V>
 struct LateArgs {
   SumArgs args;
@@ -922,9 +926,16 @@ int64_t kv_tree_attention_workspace_bytes(int num_seqs, int max_query_len, int m
   return workspace_bytes(num_seqs, max_query_len, max_seq_len, q_heads, kv_heads, head_dim, kTree);
 }
 
+// Kernels that read their arguments by their place (LateArgs).
+template <int V>
+using LateKernel = void (*)(typename ArgsOf<V>::type);
 template <int D, int V>
 static void launch_for(const typename ArgsOf<V>::type& a, const AttentionPlan& p, int num_seqs,
                        hipStream_t stream) {
+  static_assert(std::is_same_v<decltype(&kv_attention_rows_kernel<D, V>), LateKernel<V>> &&
+                std::is_same_v<decltype(&kv_attention_kernel<D, 1, V>), LateKernel<V>> &&
+                std::is_same_v<decltype(&kv_attention_kernel<D, 2, V>), LateKernel<V>> &&
+                sizeof(SumArgs) % 8 == 0, "arguments are read as words from the segment's start");
   const int heads = a.cache.kv_heads;
   const dim3 grid(heads, p.row_tiles * p.parts, num_seqs);
   if (p.many)
