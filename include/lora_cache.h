@@ -100,9 +100,9 @@ lora_status_t lora_kv_tree_attention(const uint16_t *q, int64_t ldq, const int32
  *   mass[t]  = drawn[t]             for its last `queries`, this step's own, whatever
  *                                   their places held.
  * What a row sees is as for lora_kv_tree_attention on the same arguments; lse is what
- * that call wrote.  A row whose lse is -infinity counts for nothing; where it is NaN, or
- * a key that a row sees holds one, so is the mass of what the row sees.  Scores and
- * sums are fp32.
+ * that call wrote, or -infinity: such a row counts for nothing, whatever its q and the
+ * keys that it sees hold.  Where it is NaN, as where a key that the row sees holds one,
+ * so is the mass of what the row sees.  Scores and sums are fp32.
  * Sequences without rows in this call, places past a sequence's length and tokens of
  * pages outside [0, num_pages) are left as they are.  No page may stand twice among
  * those that hold the tokens of this call's sequences.

@@ -49,8 +49,19 @@ __device__ __forceinline__ int query_of(const MassArgs& m, int row) {
 }
 
 // A row's sum as the power that its scores are taken relative to; a row without a sum
-// (or none at all) counts for nothing.
+// counts for nothing, whatever its query holds.
 __device__ __forceinline__ float relative_to(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
+// Of a row that is not there and has a query of zeros: its powers are zero.
+constexpr float kNoRow = 3.402823466e38f;
+
+// What the rows [4 g, 4 g + 4) of a tile see (seen_by_rows), without those that count for
+// nothing: a NaN score less their infinity would be NaN.
+__device__ __forceinline__ uint32_t unless_silent(uint32_t seen, f32x4 top) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (top[i] == INFINITY) seen &= ~(15u << (4 * i));
+  return seen;
+}
 
 // Sums over the four lanes with the same c.
 __device__ __forceinline__ float over_groups(float v) {
@@ -199,6 +210,7 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_kernel(MassArgs m) {
   const int tiles = (t.rows + kTile - 1) / kTile;
   __shared__ u32x4 q[T * kSteps][kWave];
   __shared__ f32x4 tops[T * 4];
+  __shared__ unsigned long long silent[kMassWaves];  // rows that count for nothing
   __shared__ Draft drafts[V == kTree ? T * kTile : 1];
   for (int f = wave; f < tiles * kSteps; f += kMassWaves) {
     const int row = (f / kSteps) * kTile + c;
@@ -210,24 +222,32 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_kernel(MassArgs m) {
     }
     q[f][lane] = w;
   }
-  for (int row = static_cast<int>(threadIdx.x); row < tiles * kTile; row += kMassThreads) {
-    float top = INFINITY;
+  static_assert(T * kTile <= kMassThreads, "a row a thread");
+  {
+    const int row = static_cast<int>(threadIdx.x);
+    float top = kNoRow;
     if (row < t.rows) {
       const RowOf at = row_of(a, 0, 0, row);
       top = relative_to(a.lse[static_cast<int64_t>(t.start + at.query) * a.ldl + kv_head * a.group + at.head]);
     }
-    reinterpret_cast<float*>(tops)[row] = top;
+    if (row < T * kTile) reinterpret_cast<float*>(tops)[row] = top;
+    const unsigned long long out = __ballot(top == INFINITY);
+    if (lane == 0) silent[wave] = out;
   }
   if constexpr (V == kTree) stage_drafts(a, t, drafts, tiles * kTile, kMassThreads);
   __syncthreads();
+  // bit n: of tile n, some row counts for nothing
+  const unsigned long long silent_tiles =
+      __ballot(lane < T && reinterpret_cast<const uint16_t*>(silent)[lane < T ? lane : 0] != 0);
 
   // Adds up one tile's rows.
   const auto add = [&](f32x4& sums, const f32x4 (&s)[4], int base, bool masked, int n) {
     const f32x4 top = tops[4 * n + g];
-    if (masked) {
+    if (masked || (silent_tiles >> n & 1)) {
       const int query0 = n * kTile / a.group;
-      add_seen_rows(sums, s, top, m.scale_log2,
-                    seen_by_rows<V>(a, t, drafts, base, query0, n * kTile - query0 * a.group, t.rows - n * kTile));
+      const uint32_t seen =
+          seen_by_rows<V>(a, t, drafts, base, query0, n * kTile - query0 * a.group, t.rows - n * kTile);
+      add_seen_rows(sums, s, top, m.scale_log2, unless_silent(seen, top));
     } else {
       add_rows(sums, s, top, m.scale_log2);
     }
@@ -317,17 +337,30 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs 
   __shared__ u32x4 q[2][kShares][kSteps][kWave];
   __shared__ float tops[2][kStageRows];
   __shared__ float joined[kMassWaves][kWave];
+  __shared__ int again;  // chunks that have to be done once more
   __shared__ Draft drafts[V == kTree ? 64 * kDraftWords : 1];
   if constexpr (V == kTree) stage_drafts(a, t, drafts, t.query1 + 1, kMassThreads);  // (a barrier comes below)
 
-  for (int first = t.chunk0 + static_cast<int>(blockIdx.y) * kChunks; first < end;
-       first += kChunks * static_cast<int>(gridDim.y)) {
+  // Where a sum comes out as NaN, the chunks are done once more with care: it may be of a
+  // row that counts for nothing, whose infinity leaves a NaN score NaN.  Its query and
+  // such keys are then staged as finite ones.  (A look for such rows at every tile cost
+  // registers: 8 sequences in pieces 157 -> 161 us, 16 trees of 32 drafts behind 4096
+  // tokens 118 -> 138; this 158 and 120.)
+  bool careful = false;
+  if (threadIdx.x == 0) again = -1;
+  for (int first = t.chunk0 + static_cast<int>(blockIdx.y) * kChunks; first < end;) {
     const int chunk = first + wave % kChunks, base = chunk * kChunk;
     const bool mine = chunk < end;
     const int loaded = mine ? base : (end - 1) * kChunk;
     const int page = reader.page(loaded);
     Keys<D> keys;
     reader.load(keys, page, loaded);
+    if (careful) {
+      // (rows that see such a key, and count, have NaN for their sum)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (((keys.scales >> (8 * j)) & 255u) == kScaleNan) keys.scales &= ~(255u << (8 * j));
+    }
 
     // The rows that see some of these chunks; tiles are counted from the first of them on.
     int from = 0, to = t.rows;
@@ -377,7 +410,14 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs 
 #pragma unroll
       for (int f = 0; f < kLoads; ++f) {
         const int at = f * kMassWaves + wave;
-        q[buffer][at / kSteps][at % kSteps][lane] = part[f];
+        u32x4 w = part[f];
+        if (careful) {
+          const int row = row0 + at / kSteps * kTile + c, of = row < t.rows ? row : t.rows - 1;
+          const int query = query_of(m, of), head = of - query * a.group;
+          if (a.lse[static_cast<int64_t>(t.start + query) * a.ldl + kv_head * a.group + head] == -INFINITY)
+            w = u32x4{0, 0, 0, 0};
+        }
+        q[buffer][at / kSteps][at % kSteps][lane] = w;
       }
       if (wave == 0 && lane < kStageRows) tops[buffer][lane] = row0 + lane < to ? relative_to(lse) : INFINITY;
     };
@@ -410,17 +450,25 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs 
       bool masked;
       if constexpr (V == kTree) masked = base < t.all_first || base + kChunk > t.all_last;
       else masked = base + kChunk > t.before + query0 + 1 || (a.window && base <= t.before + last - a.window);
-      if (masked)
+      if (masked) {
+        // (not known to be the same each time: what follows from it takes no registers
+        // through the loop)
+        int here = base;
+        asm volatile("" : "+s"(here));
         add_seen_rows(sums, s, top, m.scale_log2,
-                      seen_by_rows<V>(a, t, drafts, base, query0, tile0 - query0 * a.group, to - tile0));
-      else
+                      seen_by_rows<V>(a, t, drafts, here, query0, tile0 - query0 * a.group, to - tile0));
+      } else {
         add_rows(sums, s, top, m.scale_log2);
+      }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) sums[j] = over_groups(sums[j]);
     const float drawn = of_group(sums);
     joined[wave][lane] = drawn;
+    if (!careful && __any(drawn != drawn)) again = first;  // (a sum of rows, so a barrier came before)
     __syncthreads();
+    careful = !careful && again == first;
+    if (careful) continue;
     const int token = base + 4 * c + g;
     if (share == 0 && mine && token < length && page >= 0) {
       float* at = reader.at(page, base);
@@ -430,6 +478,7 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs 
       *at = token >= t.before ? all : *at + all;
     }
     __syncthreads();  // the sums have been read
+    first += kChunks * static_cast<int>(gridDim.y);
   }
 }
 

@@ -362,6 +362,61 @@ def test_rows_without_a_sum_count_for_nothing():
     check(mass, after, slack, "mass")
 
 
+@pytest.mark.parametrize("kw", [
+    dict(lens=[77, 300, 64], queries=[3, 4, 1], hq=8, kv=2, d=64, page=16),                   # one tile of rows
+    dict(lens=[90, 300, 40], queries=[13, 21, 9], hq=8, kv=2, d=128, page=64),                # several
+    dict(lens=[90, 300], queries=[13, 21], hq=8, kv=2, d=64, page=16, window=30),
+    dict(lens=[150, 330, 90], queries=[40, 33, 64], hq=16, kv=2, d=128, page=64),             # many
+    dict(lens=[250, 300], queries=[70, 45], hq=15, kv=3, d=64, page=64, window=100)])
+@pytest.mark.parametrize("bits", ["tree", None])
+@pytest.mark.parametrize("silent", [0.0, 0.3])
+def test_rows_without_a_sum_count_for_nothing_whatever_they_hold(kw, bits, silent):
+    """Rejected drafts, whose sums a program sets to -infinity: NaN and infinities of their
+    queries, and of keys that only they see, reach no weight."""
+    s = Step(15, bits=bits, **kw)
+    lse = s.want()["lse"].copy()
+    rng = np.random.default_rng(4)
+    out = rng.random((s.T, s.hq)) < silent
+    out[:s.start[1]] = True  # all of the first sequence's
+    out[np.array(s.start[1:]) - 1] = True  # and the last of each, which alone sees the last token
+    lse[out] = -np.inf
+    q = s.q.float().numpy()
+    q[out] = rng.choice([np.nan, np.inf, -np.inf], (int(out.sum()), s.d))
+    s.q = R.bf16(q)
+    for b, length in enumerate(s.lens):
+        page, inside = s.table[b, (length - 1) // s.page], (length - 1) % s.page
+        s.cache[page, 0, :, s.page * (s.d // 2) + inside] = 255
+        s.values[page, 0, :, inside, :32] = np.nan
+    lse = torch.from_numpy(lse).float().cuda()
+    mass = torch.ones(s.pages, s.kv, s.page, device="cuda")
+    s.draw(mass, lse)
+    after, slack = C.mass_after(np.ones(mass.shape), s.want(lse_in=R.f64(lse)))
+    assert np.isfinite(after).all()
+    check(mass, after, slack, "mass")
+
+
+@pytest.mark.parametrize("hq,d", [(2, 64), (8, 128), (16, 128), (16, 64)])
+@pytest.mark.parametrize("bits", ["tree", None])
+def test_nan_sums_beside_rows_without_a_sum(hq, d, bits):
+    """A NaN key reaches what the rows that see it, and count, see; not the others' tokens."""
+    s = Step(16, [150, 330], [40, 33], hq, 2, d, 64, bits=bits)
+    t = s.lens[0] - s.queries[0] + 20
+    page, inside = s.table[0, t // 64], t % 64
+    s.cache[page, 0, 0, 64 * (d // 2) + inside] = 255
+    s.values[page, 0, 0, inside, :32] = np.nan
+    _, lse = s.attend()
+    rows = np.flatnonzero(lse.isnan().any(1).cpu().numpy())
+    assert len(rows)
+    for quiet in ([], [int(rows[0])], rows.tolist()):
+        sums = lse.clone()
+        sums[quiet] = -torch.inf
+        mass = torch.ones(s.pages, s.kv, s.page, device="cuda")
+        s.draw(mass, sums)
+        after, slack = C.mass_after(np.ones(mass.shape), s.want(lse_in=R.f64(sums)))
+        assert np.isnan(after).any() == (len(quiet) < len(rows))
+        check(mass, after, slack, "mass")
+
+
 # ------------------------------------------------------------------ select
 def selected(mass, lens, table, sinks, recent, budget, **more):
     kept = torch.full((len(lens), mass.shape[1], budget), -9, dtype=torch.int32, device="cuda")
