@@ -7,10 +7,14 @@
  *
  * A step with drafts: lora_draft_masks, lora_kv_append at its positions, attention by
  * lora_kv_tree_attention, and once the accepted ones are known lora_kv_compact, which
- * moves them to the places right behind the text.
+ * moves them to the places right behind the text.  From there on the sequence's length is
+ * that of the text and the accepted drafts: seq_lens still counts all drafts until the
+ * caller has set it.
  * A cache of bounded length: lora_kv_tree_attention with sums (and no masks, where
  * there are no drafts), lora_kv_attention_mass after it; when a sequence has grown
- * past its bound, lora_kv_select and lora_kv_compact.
+ * past its bound, lora_kv_select and lora_kv_compact.  With drafts, the mass is drawn
+ * between the choice of the accepted ones and their move, with lse set to -infinity in
+ * the rows of the others: these would count in the text's mass for good.
  *
  * The mass: fp32 [num_pages][kv_heads][page_size] beside the cache, 16-byte aligned;
  * an element is the attention that the token of its place has drawn from the rows of
@@ -163,9 +167,9 @@ lora_status_t lora_kv_select(const float *mass, int32_t num_pages, int32_t page_
  *   mass         may be NULL.
  * Entries below 0, and those whose source or destination lies outside its table or on
  * a page outside [0, num_pages), are skipped: their destinations stay as they are.
- * In place the entries ascend, those below 0 behind all others (what the places named
- * hold afterwards is open otherwise); kept[j] = j leaves the token where it is.  No page
- * may then stand twice among those that hold the places named.
+ * In place the entries ascend, each above the one before, those below 0 behind all others
+ * (what the places named hold afterwards is open otherwise); kept[j] = j leaves the token
+ * where it is.  No page may then stand twice among those that hold the places named.
  * Enqueues one kernel, or two for long lists of few key heads in place.
  */
 lora_status_t lora_kv_compact(const int32_t *kept, int32_t num_lists, int32_t max_kept,

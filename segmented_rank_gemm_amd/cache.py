@@ -181,7 +181,8 @@ def lora_kv_attention_mass(q: torch.Tensor, lse: torch.Tensor, query_start: torc
                            stream: Optional[torch.cuda.Stream] = None, page_size: Optional[int] = None) -> None:
     """The arguments of the lora_kv_tree_attention that wrote lse, and mass: fp32
     (kv_mass_shape), to which the attention that the tokens drew is added; that of
-    the step's own tokens is put there."""
+    the step's own tokens is put there.  Rows whose lse is -infinity count for nothing:
+    those of rejected drafts are set so, before lora_kv_compact moves the others."""
     T, q_heads, head_dim = _dims(q, 3, "q")
     pq, ldq = _heads(q, T, q_heads, head_dim, "q")
     pl, ldl = _matrix(lse, _F32, T, q_heads, "lse")
@@ -241,7 +242,7 @@ def lora_kv_compact(kept: torch.Tensor, counts: torch.Tensor, page_table: torch.
                     page_size: Optional[int] = None) -> None:
     """kept: int32 [num_seqs, kv_heads or 1, n]: of each sequence, and key head (or all
     of them), the tokens that move to the places first + 0, first + 1, ..., counted from
-    first (int32 [num_seqs], or None: 0); counts: int32 [num_seqs], how many of the n;
+    first (int32 [num_seqs], or None: 0), in place each above the one before; counts: int32 [num_seqs], how many of the n;
     page_table, dst_table: int32 [num_seqs, pages a sequence], where they are and where
     they go (None: in place; other pages than those); mass: fp32 (kv_mass_shape), moved
     along."""

@@ -325,6 +325,45 @@ def test_every_tensor_is_on_the_streams_device(monkeypatch):
                         call(**{**args, name: value.as_subclass(Elsewhere)}, stream=stream)
 
 
+def test_rejected_drafts_leave_neither_mass_nor_places():
+    """A step as the header has it: the mass between the choice of drafts and their move, without
+    the others' rows; the lengths set behind the move; the choice of tokens over these."""
+    text, n, page = [70, 41, 90], [12, 7, 12], 16
+    s = Step(4, [t + m for t, m in zip(text, n)], n, 8, 2, 64, page)
+    _, lse = s.attend()
+    want = s.want()
+    # the longest path of each tree
+    paths = [sorted(max(s.bits[a:b], key=len)) for a, b in zip(s.start, s.start[1:])]
+    rejected = torch.ones(s.T, dtype=torch.bool, device="cuda")
+    for a, path in zip(s.start, paths):
+        rejected[[a + p for p in path]] = False
+    lse.masked_fill_(rejected[:, None], -torch.inf)
+    mass = torch.zeros(s.pages, s.kv, page, device="cuda")
+    s.draw(mass, lse)
+    accepted = np.full((3, 1, 12), -1, dtype=np.int32)
+    for b, path in enumerate(paths):
+        accepted[b, 0, :len(path)] = path
+    counts, cache = ints([len(p) for p in paths]), dev(s.cache)
+    srg.lora_kv_compact(dev(accepted), counts, dev(s.table), cache, s.d, mass=mass, first=ints(text), page_size=page)
+    seq_lens = torch.empty_like(counts)
+    torch.add(ints(text), counts, out=seq_lens)
+    budget = 40
+    kept, new_lens = ints(np.zeros((3, 2, budget))), ints([0] * 3)
+    recent = max(len(p) for p in paths)
+    srg.lora_kv_select(mass, seq_lens, dev(s.table), 2, recent, kept, new_lens)
+    for b, path in enumerate(paths):
+        length = text[b] + len(path)
+        assert seq_lens[b] == length
+        held = mass[torch.from_numpy(s.table[b]).cuda().long().clamp(min=0)].transpose(0, 1).reshape(2, -1)[:, :length]
+        # the weights of every accepted row add up to one, each off by its score's and its sum's error
+        rows = len(path) * s.hq
+        slack = 2 * want["lse_slack"][s.start[b]:s.start[b + 1]].max() * rows
+        assert abs(float(held.double().sum()) - rows) <= slack
+        for h in range(2):
+            assert kept[b, h, budget - recent:].tolist() == list(range(length - recent, length))
+            assert kept[b, h].tolist() == C.select(held[h].tolist(), length, 2, recent, budget)
+
+
 def test_calls_over_nothing():
     new = lambda *shape, dtype=torch.int32: torch.zeros(*shape, dtype=dtype, device="cuda")  # noqa: E731
     cache, mass = new(2, 2, 1, 16 * 34, dtype=torch.uint8), new(2, 1, 16, dtype=torch.float32)
