@@ -7,8 +7,11 @@
 // steps as the tree is deep.  Parents lie before their children (others are taken for
 // roots), so that every climb ends.
 //
-// Bound by latency: two dependent loads, the climb and the stores (1 sequence of 26 drafts
-// 2.0 us, 16 of 32 4.7 us, an empty launch 1.9).
+// Bound by latency: two dependent loads, the climb and the stores, and where trees are
+// deep by the climb, two dependent reads of shared memory a step (us, an empty launch 1.9;
+// random trees / chains: 1 sequence of 26 drafts 2.2 / 3.5, of 64 2.3 / 6.0, of 512
+// 5.1 / 65; 16 of 32 2.6 / 4.5.  Behind an attention over 47 MB, whose lines have taken
+// the caches, 16 of 32 took 4.6 in a trace and 2.7 by themselves).
 
 #include "kv_attention.hpp"
 

@@ -34,9 +34,12 @@
 // the rows' sums (kSums), or what masks of drafts say (kTree).  A tree's drafts lie in the
 // last chunks alone; elsewhere a row sees all of a chunk, and the walk is the plain one.
 // With 256 to 512 rows a key head it is bound like prompts (16 sequences of up to 4096
-// tokens and 32 drafts, 64 query heads on 8: 67 us, vector instructions 58% and the matrix
-// unit 20% of the cycles; 64 drafts of 32768 tokens: 94 us and 5 for the join, 64% and
-// 27%); with few rows by latency (26 drafts behind 500 tokens: 10 us and 2 for the masks).
+// tokens and 32 drafts, 64 query heads on 8: 67 us, vector instructions 59% and the matrix
+// unit 21% of the cycles, and at the end the longest sequences' workgroups alone: 1.6 of 2
+// waves a SIMD; 64 drafts of 32768 tokens: 95 us and 5 for the join, 65% and 27%); with few
+// rows by latency (26 drafts behind 500 tokens: 10 us and 2 for the masks).  Sums without
+// masks beside plain attention, us: 64 single queries to 8192 tokens 65 / 64, one of 131072
+// 40 / 38, pieces of prompts 316 / 292.
 
 #include <type_traits>
 
@@ -859,9 +862,11 @@ static AttentionPlan attention_plan(bool views, int num_seqs, int max_query_len,
   // (us, one tile / two: 26 rows and 500 tokens, 32 key heads 12.5 / 14.6; 64 rows, 64
   // key heads of sequences, 1536 tokens 17 / 19, 2600 22.6 / 23.4, 4096 32 / 29; 512 rows
   // and 32768 tokens, 8 key heads 174 / 101), and where pairs of tiles are more than the
-  // units but single ones no more than two each (78 rows, 96 key heads of sequences, 480
-  // tiles in 288 pairs, heads of 64: 500 tokens 13.1 / 13.4, 1024 15.4 / 17.6, 4096 33 /
-  // 43; but 512 tiles in 256 pairs, heads of 128, 1024 tokens 20.3 / 17.3).  Where a call
+  // units but single ones no more than two each (9 counts of 408 to 504 tiles in 260 to 336
+  // pairs, heads of 64 and 128, 300 to 4096 tokens: one took less in all 126, by 1 to
+  // 25%, and with lengths from 100 to 4096 by 12 to 40%; 480 in 288, heads of 64: 300 tokens 10.4 / 12.1, 1024 14.6 / 17.1, 4096 31 / 41;
+  // 468 in 260, heads of 128: 13.2 / 13.6, 19.8 / 20.2, 45 / 50; but 512 tiles in 256
+  // pairs, heads of 128, 1024 tokens 20.3 / 17.3).  Where a call
   // with a window has one tile, and the workspace is sized for two and longer walks, it is
   // large enough: at most 3 parts of 16 rows, or a workgroup a compute unit, against at
   // least 7 of 32, or as many workgroups.

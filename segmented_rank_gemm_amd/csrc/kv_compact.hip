@@ -9,7 +9,7 @@
 // and no other workgroup touches these bytes.
 //
 // Long lists of few key heads leave the device idle that way (2 x 8 workgroups, 65536
-// tokens: 225 us).  Where the tokens lie a thousand places ahead of where they go, and
+// tokens: 248 us).  Where the tokens lie a thousand places ahead of where they go, and
 // further on always do, the moves are followed from the other end: a place that is no
 // source itself takes its token, whose place takes its own, and so on.  These chains
 // have nothing in common, each step is a thousand places long, and there are as many of
@@ -264,10 +264,11 @@ static void launch_compact(const CompactArgs& a, int num_seqs, hipStream_t strea
   const int64_t units = static_cast<int64_t>(num_seqs) * a.cache.kv_heads * 2;
   const dim3 grid(2 * a.cache.kv_heads, num_seqs, 1);
   // By chains where the device has more compute units than half of them could use, and
-  // the list more than a few blocks (us, chains / blocks, heads of 128: 5000 entries of
-  // one sequence 14.2 / 14.0, 16384 of 32768 tokens 21 / 39.5, 65536 of 131072 71 / 225;
-  // 16384 of 4 sequences, 64 units, 112 / 114).  A list that leaves out next to nothing
-  // has few chains (16 tokens of 65552: 151 / 119).
+  // the list more than a few blocks (us, chains / blocks, half of the tokens, 8 heads of
+  // 128: 5000 entries of one sequence 16.8 / 18.6, 16384 22 / 47, 65536 72 / 248; of 4
+  // sequences, 64 units, 5000 22.4 / 22.1, 16384 65 / 78, 32768 130 / 154, where the bytes
+  // that move take 27 and 54).  A list that leaves out next to nothing has few chains (16
+  // tokens of 65552: 147 / 141).
   if (!a.dst_table && units <= kCus / 4 && a.max_kept > 4 * kNearBlock) {
     hipLaunchKernelGGL(kv_compact_near_kernel<D>, grid, dim3(kNearBlock), 0, stream, a);
     const int64_t all = (static_cast<int64_t>(a.max_kept) + kChainWaves * kWave - 1) / (kChainWaves * kWave);

@@ -19,9 +19,11 @@
 // Bound by: HBM with one tile of rows (64 sequences of up to 8192 tokens, 8 key heads of
 // 128: 39.5 us, 4.1 TB/s where a copy reaches 5.0 to 5.5); with many rows by the
 // instructions that the units take in turn (8 sequences in pieces of 129 to 512 queries, 8
-// key heads of 8: 155 us, 790 TFLOP/s; vector instructions 51% of the cycles, of which the
+// key heads of 8: 157 us, 780 TFLOP/s; vector instructions 51% of the cycles, of which the
 // exponentials, their arguments and sums are 48 of 89 a tile and chunk, the matrix unit
-// 31%).
+// 31%).  For heads of 128 that kernel keeps 17 registers (27 with masks) in scratch memory,
+// stored at its start and read again once a chunk, not in the loop over the rows: 47 MB of
+// writes where its output is 1 MB.
 
 #include "kv_attention.hpp"
 
@@ -315,9 +317,9 @@ __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_kernel(MassArgs m) {
   }
 }
 
-// Any number of rows: each of the workgroup's waves has the keys of one of four chunks,
-// and takes every second pair of row tiles; tiles come by in shared memory, staged as
-// the matrix unit's operands two steps' tiles at a time.
+// Any number of rows: a workgroup has two chunks, each wave the keys of one of them, and
+// the four waves of a chunk share the rows, a tile of 16 of a step's 64 each.  Tiles come
+// by in shared memory, staged as the matrix unit's operands, in two buffers of a step.
 template <int D, int V>
 __global__ __launch_bounds__(kMassThreads, 4) void kv_mass_rows_kernel(MassArgs m) {
   constexpr int kSteps = D / 32;

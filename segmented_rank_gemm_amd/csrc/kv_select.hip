@@ -20,8 +20,11 @@
 // Bound by: the histogram's additions in shared memory and the steps that follow from each
 // other (64 sequences of 4097 to 8192 tokens, 8 key heads: 13.9 us, the 21 MB at 1.5 TB/s:
 // up to the first histogram's end 6, then the digits 4, counting and writing 4; with 16
-// waves 15.4); of one sequence of 131072 tokens, the four launches' latencies (21 us;
-// whole 58 us).
+// waves 15.4); of few long lists what their pieces join: behind the first launch each
+// piece reads the histograms of all of its list, 4 KB a piece (131072 tokens, 16 pieces:
+// launches of 3.4, 5.8, 5.4 and 7 us, 21 in all, whole 58; 1048576 tokens, 128 pieces:
+// 8.8, 35, 40 and 42); of many long lists HBM, for the three readings (64 sequences of
+// 131072: 890 MB read and 135 written, 5.8 TB/s).
 //
 // Non-negative numbers compare as their bits do.  Where there are others (NaNs, which
 // count as -infinity, and pages that do not exist, which weigh as much, among them),
